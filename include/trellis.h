@@ -36,7 +36,7 @@
  *     Calls that overlap in time (several streams) need separate workspaces.
  *   - The error word is sticky: kernels only OR bits into it (1: a routed id out of range
  *     or a table entry with an invalid K/cb was skipped; 2: a prefill workgroup's bounded
- *     wait for another ran out).  The caller reads it and clears it by writing 0 to the
+ *     wait for another ran out; 4 and 8: trellis_kv4.h).  The caller reads it and clears it by writing 0 to the
  *     first 4 bytes of the workspace (any device fill, e.g. on the same stream).
  */
 #ifndef TRELLIS_H_

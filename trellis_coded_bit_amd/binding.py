@@ -105,6 +105,29 @@ def lib() -> ctypes.CDLL:
             L.trellis_gemv_list.argtypes = [vp, i32, i32, vp, sz, vp]
             L.trellis_gemv_list_noalloc.restype = i32
             L.trellis_gemv_list_noalloc.argtypes = [vp, i32, i32, vp]
+            i64, f32 = ctypes.c_int64, ctypes.c_float
+            L.trellis_kv4_page_bytes.restype = sz
+            L.trellis_kv4_page_bytes.argtypes = [i32, i32, i32]
+            L.trellis_kv4_workspace_bytes.restype = sz
+            L.trellis_kv4_workspace_bytes.argtypes = []
+            L.trellis_kv4_attn_workspace_bytes.restype = sz
+            L.trellis_kv4_attn_workspace_bytes.argtypes = [vp, vp, i32]
+            L.trellis_kv4_pages_workspace_bytes.restype = sz
+            L.trellis_kv4_pages_workspace_bytes.argtypes = [vp, i32]
+            L.trellis_kv4_append.restype = i32
+            L.trellis_kv4_append.argtypes = [vp, i32, vp, i32, vp, i64, i64, vp, i64, i64, vp, sz, vp]
+            L.trellis_kv4_read.restype = i32
+            L.trellis_kv4_read.argtypes = [vp, i32, vp, i32, vp, vp, vp, sz, vp]
+            L.trellis_kv4_attn.restype = i32
+            L.trellis_kv4_attn.argtypes = [vp, i32, vp, i32, vp, i64, i64, i32, f32, i32, i32, i32, vp, vp, vp, sz, vp]
+            L.trellis_kv4_reserve.restype = i32
+            L.trellis_kv4_reserve.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, sz, vp]
+            L.trellis_kv4_fork.restype = i32
+            L.trellis_kv4_fork.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, sz, vp]
+            L.trellis_kv4_compact.restype = i32
+            L.trellis_kv4_compact.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, sz, vp]
+            L.trellis_kv4_free.restype = i32
+            L.trellis_kv4_free.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp, sz, vp]
             L.trellis_validate_table.restype = i32
             L.trellis_validate_table.argtypes = [ctypes.POINTER(CLinear), i32, i32, i32, i32]
             _lib = L
@@ -554,6 +577,231 @@ def trellis_moe_mlp(tables: MoEMLPTables, routed: torch.Tensor, router_w: torch.
                                  _ptr(r_hidden_out), _ptr(s_hidden_out), _ptr(act), out.data_ptr(),
                                  ws.data_ptr(), ws.numel(), _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------------------
+# The paged 4-bit key/value cache (include/trellis_kv4.h)
+# ---------------------------------------------------------------------------------------
+
+class CKV4Cache(ctypes.Structure):
+    """Mirror of ``trellis_kv4_cache`` in include/trellis_kv4.h."""
+
+    _fields_ = [("pool", ctypes.c_void_p), ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class CKV4Batch(ctypes.Structure):
+    """Mirror of ``trellis_kv4_batch`` in include/trellis_kv4.h."""
+
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("cu", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_seq", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
+_KV4_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def trellis_kv4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of one layer."""
+    nb = lib().trellis_kv4_page_bytes(page_size, n_kv_heads, head_dim)
+    if nb == 0:
+        raise ValueError(f"page_size={page_size} n_kv_heads={n_kv_heads} head_dim={head_dim}: pages of 16, 32, 64, 128 "
+                         "or 256 tokens, 1..1024 heads of 128 or 256 expected")
+    return nb
+
+
+class KV4Cache:
+    """A cache of keys and values in 4 bits: ``pool`` uint8 [n_layers, n_pages, page_bytes] on a
+    GPU.  The page table (int32 [slots, max_pages]), the lengths (int32 [slots]) and the pages'
+    reference counts (int32 [n_pages]) are the caller's tensors, passed to each call."""
+
+    def __init__(self, pool: torch.Tensor, page_size: int, n_kv_heads: int, head_dim: int):
+        nb = trellis_kv4_page_bytes(page_size, n_kv_heads, head_dim)
+        _req(pool, torch.uint8, "pool")
+        if pool.dim() != 3 or pool.shape[2] != nb or pool.shape[0] < 1 or pool.shape[1] < 1:
+            raise ValueError(f"pool must be [n_layers, n_pages, {nb}], got {tuple(pool.shape)}")
+        self.pool, self.page_size, self.n_kv_heads, self.head_dim = pool, page_size, n_kv_heads, head_dim
+        self.n_layers, self.n_pages = pool.shape[0], pool.shape[1]
+        self.device = pool.device
+        self._c = CKV4Cache(pool.data_ptr(), self.n_layers, self.n_pages, page_size, n_kv_heads, head_dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def allocate(cls, n_layers: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                 device="cuda") -> "KV4Cache":
+        nb = trellis_kv4_page_bytes(page_size, n_kv_heads, head_dim)
+        return cls(torch.zeros((n_layers, n_pages, nb), dtype=torch.uint8, device=device), page_size, n_kv_heads, head_dim)
+
+
+def _kv4_state(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor) -> None:
+    _req(table, torch.int32, "table", cache.device)
+    _req(lens, torch.int32, "lens", cache.device)
+    if table.dim() != 2 or lens.numel() != table.shape[0]:
+        raise ValueError(f"table must be [slots, max_pages] with one length per slot, got {tuple(table.shape)} and "
+                         f"{lens.numel()} lengths")
+
+
+def _kv4_batch(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+               slots: Optional[torch.Tensor], rows: int) -> CKV4Batch:
+    _kv4_state(cache, table, lens)
+    _req(cu, torch.int32, "cu", cache.device)
+    n_seq = cu.numel() - 1
+    if slots is not None:
+        _req(slots, torch.int32, "slots", cache.device)
+        if slots.numel() != n_seq:
+            raise ValueError(f"slots must have one entry per sequence ({n_seq}), got {slots.numel()}")
+    elif n_seq > lens.numel():
+        raise ValueError(f"{n_seq} sequences over {lens.numel()} slots")
+    if n_seq < 0:
+        raise ValueError("cu must have one entry more than there are sequences")
+    return CKV4Batch(table.data_ptr(), lens.data_ptr(), _ptr(slots), cu.data_ptr(), table.shape[0], table.shape[1], n_seq,
+                     rows)
+
+
+def _kv4_rows(cache: KV4Cache, x: torch.Tensor, heads: Optional[int], name: str):
+    """Checks a [rows, heads, head_dim] tensor whose vectors are contiguous; its strides."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in _KV4_DTYPE:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {x.dtype}")
+    if x.device != cache.device:
+        raise ValueError(f"{name} is on {x.device}, expected {cache.device}")
+    if x.dim() != 3 or x.shape[2] != cache.head_dim or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {heads if heads is not None else 'heads'}, {cache.head_dim}], got "
+                         f"{tuple(x.shape)}")
+    row, head, last = x.stride()
+    if last != 1:
+        raise ValueError(f"{name}: each head's vector must be contiguous")
+    return row, head
+
+
+def trellis_kv4_append(cache: KV4Cache, layer: int, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                       k: torch.Tensor, v: torch.Tensor, slots: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None) -> None:
+    """Quantise new keys and values, [rows, n_kv_heads, head_dim] fp16 or bf16 (slices of a
+    fused projection's output are fine), into one layer.  Sequence b (slot ``slots[b]``, or b)
+    has the rows cu[b] .. cu[b+1]-1, its last tokens; ``lens`` already counts them."""
+    k_row, k_head = _kv4_rows(cache, k, cache.n_kv_heads, "k")
+    v_row, v_head = _kv4_rows(cache, v, cache.n_kv_heads, "v")
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same type and number of rows")
+    b = _kv4_batch(cache, table, lens, cu, slots, k.shape[0])
+    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    _check(lib().trellis_kv4_append(cache._ref, layer, ctypes.byref(b), _KV4_DTYPE[k.dtype], k.data_ptr(), k_row, k_head,
+                                    v.data_ptr(), v_row, v_head, ws.data_ptr(), ws.numel(), _stream()))
+
+
+def trellis_kv4_read(cache: KV4Cache, layer: int, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, rows: int,
+                     dtype: torch.dtype = torch.float16, slots: Optional[torch.Tensor] = None,
+                     out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, ws: Optional[torch.Tensor] = None):
+    """The keys and values that the cache holds for each sequence's last cu[b+1] - cu[b]
+    tokens, rotated back: (k, v), each [rows, n_kv_heads, head_dim]."""
+    if dtype not in _KV4_DTYPE:
+        raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+    shape = (rows, cache.n_kv_heads, cache.head_dim)
+    k, v = (_out(o, shape, cache.device, dtype, n) for o, n in zip(out if out is not None else (None, None), ("k", "v")))
+    b = _kv4_batch(cache, table, lens, cu, slots, rows)
+    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    _check(lib().trellis_kv4_read(cache._ref, layer, ctypes.byref(b), _KV4_DTYPE[dtype], k.data_ptr(), v.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), _stream()))
+    return k, v
+
+
+def trellis_kv4_attn_workspace_bytes(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                                     rows: int, n_q_heads: int, slots: Optional[torch.Tensor] = None) -> int:
+    """Workspace bytes of trellis_kv4_attn for these sizes."""
+    b = _kv4_batch(cache, table, lens, cu, slots, rows)
+    nb = lib().trellis_kv4_attn_workspace_bytes(cache._ref, ctypes.byref(b), n_q_heads)
+    if nb == 0:
+        raise TrellisError(-1, lib().trellis_last_error().decode())
+    return nb
+
+
+def trellis_kv4_attn(cache: KV4Cache, layer: int, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                     q: torch.Tensor, window: int = 0, sinks: int = 0, scale: Optional[float] = None, max_q: int = 0,
+                     slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of q [rows, n_q_heads, head_dim] (fp16 or bf16) over the cache: row
+    cu[b] + i is sequence b's token at lens - (cu[b+1] - cu[b]) + i and sees the keys up to
+    itself, with ``window`` only the last ``window`` of them and the first ``sinks`` tokens.
+    ``scale`` defaults to head_dim ** -0.5.  ``max_q``: a bound on a sequence's rows if the
+    caller knows one (it chooses kernels).  ``lse``: optional f32 [rows, n_q_heads] output, the
+    logarithm of each softmax's denominator."""
+    q_row, q_head = _kv4_rows(cache, q, None, "q")
+    rows, heads = q.shape[0], q.shape[1]
+    out = _out(out, (rows, heads, cache.head_dim), cache.device, q.dtype)
+    if lse is not None:
+        _out(lse, (rows, heads), cache.device, torch.float32, "lse")
+    b = _kv4_batch(cache, table, lens, cu, slots, rows)
+    bref = ctypes.byref(b)
+    nb = lib().trellis_kv4_attn_workspace_bytes(cache._ref, bref, heads)
+    if nb == 0:
+        raise TrellisError(-1, lib().trellis_last_error().decode())
+    ws = _ws_arg(ws, nb, cache.device)
+    _check(lib().trellis_kv4_attn(cache._ref, layer, bref, _KV4_DTYPE[q.dtype], q.data_ptr(), q_row, q_head, heads,
+                                  cache.head_dim ** -0.5 if scale is None else scale, window, sinks, max_q,
+                                  out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()))
+    return out
+
+
+def _kv4_pages(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, **lists) -> int:
+    """Checks the page operations' tensors; the number of items (the first list's length)."""
+    _kv4_state(cache, table, lens)
+    _req(ref, torch.int32, "ref", cache.device)
+    if ref.numel() != cache.n_pages:
+        raise ValueError(f"ref must have one count per page ({cache.n_pages}), got {ref.numel()}")
+    n = None
+    for name, (t, extra) in lists.items():
+        if t is None:
+            continue
+        _req(t, torch.int32, name, cache.device)
+        if n is None:
+            n = t.numel()
+        elif t.numel() != n + extra:
+            raise ValueError(f"{name} must have {n + extra} entries, got {t.numel()}")
+    return n
+
+
+def trellis_kv4_reserve(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, add: torch.Tensor,
+                        slots: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> None:
+    """lens[slots[i]] += add[i] (slots None: slot i) with the pages that takes, lowest first.
+    If there are not enough, nothing changes and bit 8 of the error word is set."""
+    n = _kv4_pages(cache, table, lens, ref, add=(add, 0), slots=(slots, 0))
+    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    _check(lib().trellis_kv4_reserve(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
+                                     ref.data_ptr(), _ptr(slots), add.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
+
+
+def trellis_kv4_fork(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, src: torch.Tensor,
+                     dst: torch.Tensor, ws: Optional[torch.Tensor] = None) -> None:
+    """Slot dst[i] becomes a copy of slot src[i]: full pages shared, a partly filled last page
+    copied.  What dst held is released."""
+    n = _kv4_pages(cache, table, lens, ref, src=(src, 0), dst=(dst, 0))
+    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    _check(lib().trellis_kv4_fork(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
+                                  ref.data_ptr(), src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
+
+
+def trellis_kv4_compact(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, src: torch.Tensor,
+                        dst: torch.Tensor, keep: torch.Tensor, keep_cu: torch.Tensor,
+                        ws: Optional[torch.Tensor] = None) -> None:
+    """Slot dst[i] becomes the tokens keep[keep_cu[i]:keep_cu[i+1]] of slot src[i] (positions),
+    packed into new pages; dst[i] may be src[i].  What dst held is released."""
+    n = _kv4_pages(cache, table, lens, ref, src=(src, 0), dst=(dst, 0), keep_cu=(keep_cu, 1))
+    _req(keep, torch.int32, "keep", cache.device)
+    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    _check(lib().trellis_kv4_compact(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
+                                     ref.data_ptr(), src.data_ptr(), dst.data_ptr(), n, keep.data_ptr(),
+                                     keep_cu.data_ptr(), keep.numel(), ws.data_ptr(), ws.numel(), _stream()))
+
+
+def trellis_kv4_free(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, slots: torch.Tensor,
+                     ws: Optional[torch.Tensor] = None) -> None:
+    """Release slots: their pages' counts drop, their lengths become 0."""
+    n = _kv4_pages(cache, table, lens, ref, slots=(slots, 0))
+    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    _check(lib().trellis_kv4_free(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
+                                  ref.data_ptr(), slots.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
 
 
 # ---------------------------------------------------------------------------------------

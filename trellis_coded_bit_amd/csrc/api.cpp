@@ -8,6 +8,7 @@
 
 #include "../../include/trellis.h"
 #include "../../include/trellis_micro.h"
+#include "abi.h"
 #include "launch.h"
 
 namespace {
@@ -49,6 +50,22 @@ int check_linear(const trellis_linear *L, int need_side_vectors) {
 hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
+
+namespace trellis {
+
+int abi_fail(int status, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+void abi_clear() { g_err[0] = 0; }
+
+int abi_hip_status(hipError_t e, const char *what) { return hip_status(e, what); }
+
+}  // namespace trellis
 
 extern "C" {
 

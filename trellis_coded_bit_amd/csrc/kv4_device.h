@@ -1,0 +1,124 @@
+// Device-side building blocks of the 4-bit key/value cache (format: include/trellis_kv4.h).
+#pragma once
+#include "launch.h"
+#include "launch_kv4.h"
+#include "trellis_device.h"
+
+namespace trellis {
+
+constexpr float kRsqrt128 = 0.08838834764831845f;
+
+// Error-word bits (TRELLIS_KV4_ERR_*).
+__device__ __forceinline__ void kv4_error(uint32_t *errword, uint32_t bit) {
+  __hip_atomic_fetch_or(errword, bit, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// 16-bit element types.  bf16 is rounded to nearest even; a NaN stays one.
+template <bool BF>
+__device__ __forceinline__ float kv4_widen(uint16_t v) {
+  return BF ? __builtin_bit_cast(float, (uint32_t)v << 16) : h2f(v);
+}
+template <bool BF>
+__device__ __forceinline__ uint16_t kv4_narrow(float f) {
+  if (!BF) return f2h(f);
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+// Where one (page, head) chunk's parts lie, in bytes from its start: T tokens, NB blocks.
+struct Kv4Chunk {
+  int T, NB;
+  __device__ __forceinline__ int k_code(int nb, int t) const { return (nb * T + t) * 64; }
+  __device__ __forceinline__ int v_code(int nb, int t) const { return ((NB + nb) * T + t) * 64; }
+  __device__ __forceinline__ int k_scale(int nb, int t) const { return 128 * NB * T + (nb * T + t) * 2; }
+  __device__ __forceinline__ int v_scale(int nb, int t) const { return 128 * NB * T + ((NB + nb) * T + t) * 2; }
+  __device__ __forceinline__ int bytes() const { return 132 * NB * T; }
+};
+
+// The chunk of (layer, page, head); 64-bit, a pool may be far over 4 GiB.
+__device__ __forceinline__ char *kv4_chunk(const trellis_kv4_cache &c, int layer, int page, int head) {
+  const size_t chunk = (size_t)132 * (c.head_dim >> 7) * c.page_size;
+  return static_cast<char *>(c.pool) + (((size_t)layer * c.n_pages + page) * c.n_kv_heads + head) * chunk;
+}
+
+// The sequence of a row: how many of cu[1..n_seq] are <= row.  The 16 lanes of a DPP row share
+// the count (lane i takes every 16th entry), so the loads are in flight together.
+__device__ __forceinline__ int kv4_seq_of(const int32_t *cu, int n_seq, int row, int lane16) {
+  int n = 0;
+  for (int j = lane16; j < n_seq; j += 16) n += ldg(cu + j + 1) <= row;
+  n += __builtin_amdgcn_update_dpp(0, n, 0xB1, 0xF, 0xF, true);
+  n += __builtin_amdgcn_update_dpp(0, n, 0x4E, 0xF, 0xF, true);
+  n += __builtin_amdgcn_update_dpp(0, n, 0x141, 0xF, 0xF, true);  // the other four of eight
+  n += __builtin_amdgcn_update_dpp(0, n, 0x128, 0xF, 0xF, true);
+  return n;
+}
+
+// A row's place: its page and place in it, or page = -1 where cu, the slot, the length or the
+// table does not give one (nothing of the table is read at an index out of its bounds).
+struct Kv4Place {
+  int page, at;
+};
+__device__ __forceinline__ Kv4Place kv4_place(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int row,
+                                              int lane16) {
+  Kv4Place r{-1, 0};
+  const int s = kv4_seq_of(b.cu, b.n_seq, row, lane16);
+  if (s >= b.n_seq) return r;
+  const int slot = b.slots ? ldg(b.slots + s) : s;
+  if ((uint32_t)slot >= (uint32_t)b.n_slots) return r;
+  const int c0 = ldg(b.cu + s), c1 = ldg(b.cu + s + 1);
+  const long long pos = (long long)ldg(b.lens + slot) - c1 + row;  // len - (c1 - c0) + (row - c0)
+  if (row < c0 || pos < 0 || pos >= (long long)b.max_pages * c.page_size) return r;
+  const int page = ldg(b.table + (size_t)slot * b.max_pages + (int)(pos / c.page_size));
+  if ((uint32_t)page >= (uint32_t)c.n_pages) return r;
+  r.page = page;
+  r.at = (int)(pos % c.page_size);
+  return r;
+}
+
+// H_128 (unnormalised) over 16 lanes holding elements 8i .. 8i+7, strides 1, 2, 4 .. 64 in
+// ascending order.
+__device__ __forceinline__ void kv4_fwht16(float (&v)[8], int lane) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if ((t & h) == 0) {
+        const float a = v[t], b = v[t + h];
+        v[t] = a + b;
+        v[t + h] = a - b;
+      }
+  const float sg1 = (lane & 1) ? -1.f : 1.f, sg2 = (lane & 2) ? -1.f : 1.f;
+  const float sg4 = (lane & 4) ? -1.f : 1.f, sg8 = (lane & 8) ? -1.f : 1.f;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = lane_xor<1>(v[t]) + sg1 * v[t];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = lane_xor<2>(v[t]) + sg2 * v[t];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = lane_xor<4>(v[t]) + sg4 * v[t];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = lane_xor<8>(v[t]) + sg8 * v[t];
+}
+
+template <bool BF>
+__device__ __forceinline__ void kv4_unpack8(u32x4 p, float (&v)[8]) {
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = kv4_widen<BF>((t & 1) ? (uint16_t)(p[t >> 1] >> 16) : (uint16_t)p[t >> 1]);
+}
+
+template <bool BF>
+__device__ __forceinline__ u32x4 kv4_pack8(const float (&v)[8]) {
+  u32x4 o;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] = (uint32_t)kv4_narrow<BF>(v[2 * t]) | ((uint32_t)kv4_narrow<BF>(v[2 * t + 1]) << 16);
+  return o;
+}
+
+// Eight E2M1 codes (one word, element 0 in the low nibble) as numbers.
+__device__ __forceinline__ void kv4_values8(uint32_t w, float (&v)[8]) {
+  const floatx2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+  const floatx2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+  const floatx2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+  const floatx2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
+}
+
+}  // namespace trellis

@@ -37,8 +37,8 @@ int check_cache(const trellis_kv4_cache *c) {
 
 int check_sizes(int n_slots, int max_pages, const trellis_kv4_cache *c) {
   if (n_slots < 1 || max_pages < 1) return abi_fail(TRELLIS_EINVAL, "n_slots=%d max_pages=%d must be positive", n_slots, max_pages);
-  if ((long long)max_pages * c->page_size > (1LL << 30))
-    return abi_fail(TRELLIS_EINVAL, "max_pages=%d pages of %d tokens exceed 2^30 tokens", max_pages, c->page_size);
+  if ((long long)max_pages * c->page_size > (1LL << 29))
+    return abi_fail(TRELLIS_EINVAL, "max_pages=%d pages of %d tokens exceed 2^29 tokens", max_pages, c->page_size);
   return TRELLIS_OK;
 }
 

@@ -72,6 +72,21 @@ __device__ Seq seq_of(const AttnArgs &g, int s, bool flag) {
   return q;
 }
 
+// The same with every field in scalar registers, from lane `l`.
+__device__ __forceinline__ Seq seq_from(const Seq &q, int l) {
+  Seq r;
+  r.slot = __builtin_amdgcn_readlane(q.slot, l);
+  r.len = __builtin_amdgcn_readlane(q.len, l);
+  r.n = __builtin_amdgcn_readlane(q.n, l);
+  r.c0 = __builtin_amdgcn_readlane(q.c0, l);
+  r.lo = __builtin_amdgcn_readlane(q.lo, l);
+  r.n_sink = __builtin_amdgcn_readlane(q.n_sink, l);
+  r.first = __builtin_amdgcn_readlane(q.first, l);
+  r.tiles = __builtin_amdgcn_readlane(q.tiles, l);
+  r.col_tiles = __builtin_amdgcn_readlane(q.col_tiles, l);
+  return r;
+}
+
 __device__ __forceinline__ int tile_at(const Seq &q, int t) { return t < q.n_sink ? t : q.first + t - q.n_sink; }
 
 // One wave's share of shared memory: a value tile (then, at a segment's end, its sums), and the
@@ -114,165 +129,165 @@ __device__ __forceinline__ float sum4(float v) {
   return a + b;
 }
 
-// H_128 over 32 values a lane and the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ void fwht_cols(float (&x)[32]) {
-#pragma unroll
-  for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-    for (int t = 0; t < 32; ++t)
-      if ((t & h) == 0) {
-        const float a = x[t], b = x[t + h];
-        x[t] = a + b;
-        x[t + h] = a - b;
-      }
-#pragma unroll
-  for (int t = 0; t < 32; t += 2) {
-    float a = x[t], b = x[t + 1];
-    swap16(a, b);
-    float s = a + b, d = a - b;
-    swap16(s, d);
-    swap32(s, d);
-    a = s + d;
-    b = s - d;
-    swap32(a, b);
-    x[t] = a;
-    x[t + 1] = b;
-  }
-}
-
 // Byte of a power of two 2^e as a matrix instruction's scale.
 __device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
 
-// 16 columns' rotated queries as matrix operands.  Lane (n = l & 15, g = l >> 4) holds column
-// n's elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block: the E4M3 operand's order.
-template <int NB>
-struct Queries {
-  v8i part[NB][3];
-  float cf[NB];  // score = cf * (sum over parts), in powers of two; >= 0
-  int pos;       // the column's position (-1: sees nothing)
+// C columns' rotated queries as matrix operands, in shared memory: lane group g of a column's
+// E4M3 operand holds elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block.
+template <int NB, int C>
+struct QueryLds {
+  alignas(16) int part[NB][3][C][4][8];
+  float cf[NB][C];  // score = cf * (sum over parts), in powers of two; >= 0
 };
 
-template <bool BF, int NB, int R>
-__device__ __forceinline__ Queries<NB> load_queries(const AttnArgs &g, const Seq &q, int head, int col0) {
-  Queries<NB> r;
-  const int lane = threadIdx.x & 63, c = col0 + (lane & (kCols / R - 1)), k = lane >> 4;
-  const bool ok = c < (long long)q.n * g.group;
-  const int i = ok ? c / g.group : 0, h = head * g.group + (ok ? c % g.group : 0);
-  r.pos = ok ? q.len - q.n + i : -1;
-  const uint16_t *p = static_cast<const uint16_t *>(g.a.q.p) + (int64_t)(q.c0 + i) * g.a.q.row_stride + h * g.a.q.head_stride;
+// Sixteen lanes to a column, eight elements each.
+template <int NB>
+struct QueryRaw {
+  u32x4 x[NB];
+};
+template <int NB, int C>
+__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, int col0) {
+  QueryRaw<NB> r;
+  const int c = col0 + (threadIdx.x >> 4);
+  const bool ok = (int)(threadIdx.x >> 4) < C && c < (long long)q.n * g.group;
+  const uint16_t *p = static_cast<const uint16_t *>(g.a.q.p);
+  if (ok) p += (int64_t)(q.c0 + c / g.group) * g.a.q.row_stride + (head * g.group + c % g.group) * g.a.q.head_stride + 8 * (threadIdx.x & 15);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    float x[32];
+    r.x[nb] = u32x4{0, 0, 0, 0};
+    if (ok) r.x[nb] = ldg(reinterpret_cast<const u32x4 *>(p + nb * 128));
+  }
+  return r;
+}
+
+template <bool BF, int NB, int C>
+__device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> &raw, QueryLds<NB, C> &lds) {
+  const int c = threadIdx.x >> 4, i = threadIdx.x & 15;
+  if (c >= C) return;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      u32x4 raw = {0, 0, 0, 0};
-      if (ok) raw = ldg(reinterpret_cast<const u32x4 *>(p + nb * 128 + (w >> 1) * 64 + 16 * k + (w & 1) * 8));
-      float v[8];
-      kv4_unpack8<BF>(raw, v);
-#pragma unroll
-      for (int t = 0; t < 8; ++t) x[8 * w + t] = v[t];
-    }
-    fwht_cols(x);
+  for (int nb = 0; nb < NB; ++nb) {
+    float x[8];
+    kv4_unpack8<BF>(raw.x[nb], x);
+    kv4_fwht16(x, threadIdx.x & 63);
     float top = 0.f;
     bool finite = true;
 #pragma unroll
-    for (int t = 0; t < 32; ++t) {
+    for (int t = 0; t < 8; ++t) {
       top = fmaxf(top, fabsf(x[t]));
       finite &= fabsf(x[t]) <= 3.4028234e38f;
     }
-    top = max4(finite ? top : __builtin_inff());
+    top = finite ? top : __builtin_inff();
+    top = fmaxf(top, lane_xor<1>(top));
+    top = fmaxf(top, lane_xor<2>(top));
+    top = fmaxf(top, lane_xor<4>(top));
+    top = fmaxf(top, lane_xor<8>(top));
     // the largest element comes to [128, 256); a column that is not finite becomes NaN
     const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 8);
     float f = __builtin_bit_cast(float, (uint32_t)min(261 - e, 254) << 23);
     if (top > 3.4028234e38f) f = __builtin_nanf("");
     if (g.a.scale < 0.f) f = -f;
-    r.cf[nb] = __builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128);
+    if (i == 0) lds.cf[nb][c] = __builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128);
 #pragma unroll
-    for (int t = 0; t < 32; ++t) x[t] *= f;
+    for (int t = 0; t < 8; ++t) x[t] *= f;
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
+    for (int s = 0; s < 3; ++s) {
+      v2i o;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        int o = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w], x[4 * w + 1], 0, false);
-        o = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w + 2], x[4 * w + 3], o, true);
-        r.part[nb][s][w] = o;
-        if (s < 2) {  // what is left, times 16: at most 128
-          const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(o, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(o, true);
-          x[4 * w] = (x[4 * w] - lo[0]) * 16.f;
-          x[4 * w + 1] = (x[4 * w + 1] - lo[1]) * 16.f;
-          x[4 * w + 2] = (x[4 * w + 2] - hi[0]) * 16.f;
-          x[4 * w + 3] = (x[4 * w + 3] - hi[1]) * 16.f;
-        }
+      for (int w = 0; w < 2; ++w) {
+        int z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w], x[4 * w + 1], 0, false);
+        z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w + 2], x[4 * w + 3], z, true);
+        o[w] = z;
+        const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8(z, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(z, true);
+        // what is left, times 16: at most 128
+        x[4 * w] = (x[4 * w] - a[0]) * 16.f;
+        x[4 * w + 1] = (x[4 * w + 1] - a[1]) * 16.f;
+        x[4 * w + 2] = (x[4 * w + 2] - b[0]) * 16.f;
+        x[4 * w + 3] = (x[4 * w + 3] - b[1]) * 16.f;
       }
+      *reinterpret_cast<v2i *>(&lds.part[nb][s][c][(i & 7) >> 1][(i >> 3) * 4 + (i & 1) * 2]) = o;
+    }
   }
-  return r;
 }
 
-// A tile's codes and scales in registers: a wave's 16-byte loads, lane l the key l & 15 of a
-// subtile of 16 and the elements 32 (l >> 4) .. + 31 (keys: the E2M1 operand's order), or the
-// token l >> 2 and its 16-byte part l & 3 (values, bound for shared memory).
+// What a lane keeps of its column.
+template <int NB>
+struct Column {
+  float cf[NB];
+  int pos;  // the column's position (-1: sees nothing)
+};
+
+// Where a tile's keys go.  The 128 keys are eight subtiles of 16, each within one page.  Lane l
+// (m = l & 15, part = l >> 4) loads from subtile m >> 1 alone: of its tokens 2 j + (m & 1), j =
+// 0 .. 7, the 16-byte part `part`, so one address and constant offsets serve the whole tile, and a
+// wave's load covers 128 contiguous bytes of each subtile.  For the keys that is the E2M1 operand
+// of product j with row m <-> key 16 (m >> 1) + 2 j + (m & 1); its result has in lane (n, g) the
+// keys 32 g + 16 (i >> 1) + 2 j + (i & 1), i = 0 .. 3: over all j the keys 32 g .. 32 g + 31, and
+// four consecutive keys make one word of the weights' E4M3 operand.
 template <int NB>
 struct Tile {
   v4i k[NB][8], v[NB][8];
-  uint32_t ks[NB], vs[NB];  // scales of the tokens 2 l, 2 l + 1
-  int page;                 // of these tokens
+  uint32_t ks[NB], vs[NB];  // scales of two tokens: first_token(l), + 1
+  int page;                 // of the lane's subtile, -1: none
 };
 
-// The pages of a tile: lane l has that of its tokens 2 l, 2 l + 1, or -1 where there is none:
-// past the length, or a number that is no page.
-__device__ __forceinline__ int tile_pages(const AttnArgs &g, const Seq &q, int tile) {
-  const int tok = tile * kTile + 16 * ((threadIdx.x & 63) >> 3);
-  if (tok >= q.len) return -1;
-  const int page = ldg(g.a.b.table + (size_t)q.slot * g.a.b.max_pages + (tok >> g.page_shift));
-  if ((uint32_t)page < (uint32_t)g.a.c.n_pages) return page;
-  if (tok + 15 >= q.lo || tok < g.a.sinks) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);  // some row would see it
-  return -1;
+__device__ __forceinline__ int subtile_of(int lane) { return (lane & 15) >> 1; }
+__device__ __forceinline__ int first_token(int lane) { return 16 * subtile_of(lane) + 8 * (lane & 1) + 2 * (lane >> 4); }
+
+// The table's entry of the lane's subtile, not looked at yet (a look would wait for it and for
+// every load before it); kNoEntry past the length.
+constexpr int kNoEntry = -0x7FFFFFFF - 1;
+__device__ __forceinline__ int tile_entry(const AttnArgs &g, const Seq &q, int tile) {
+  const int tok = tile * kTile + 16 * subtile_of(opaque_tid() & 63);
+  int e = kNoEntry;
+  if (tok < q.len) e = ldg(g.a.b.table + (size_t)q.slot * g.a.b.max_pages + (tok >> g.page_shift));
+  return e;
 }
 
 // `base`: the head's chunk of page 0 of the layer.  (A subtile without a page reads page 0's.)
 template <int NB>
-__device__ __forceinline__ void load_tile(const AttnArgs &g, const char *base, int tile, int page, Tile<NB> &x) {
-  const uint32_t lane = threadIdx.x & 63, T = g.a.c.page_size;
-  const uint32_t lk = (lane & 15) * 64 + (lane >> 4) * 16, lv = lane * 16 + NB * T * 64;
-  const uint64_t mine = (uint64_t)(uint32_t)max(page, 0) * g.page_stride;
-  x.page = page;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)mine, 8 * j), hi = __builtin_amdgcn_readlane((uint32_t)(mine >> 32), 8 * j);
-    const char *p = base + (((uint64_t)hi << 32) | lo) + ((tile * kTile + 16 * j) & (T - 1)) * 64;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      x.k[nb][j] = ldg(reinterpret_cast<const v4i *>(p + nb * T * 64 + lk));
-      x.v[nb][j] = ldg(reinterpret_cast<const v4i *>(p + nb * T * 64 + lv));
-    }
-  }
-  const char *p = base + mine + 128 * NB * T + ((tile * kTile + 2 * lane) & (T - 1)) * 2;
+__device__ __forceinline__ void load_tile(const AttnArgs &g, int seen_from, const char *base, int tile, int entry, Tile<NB> &x) {
+  const int lane = opaque_tid() & 63, T = g.a.c.page_size;
+  const int tok = tile * kTile + 16 * subtile_of(lane), at = tok & (T - 1);
+  x.page = (uint32_t)entry < (uint32_t)g.a.c.n_pages ? entry : -1;
+  if (x.page < 0 && entry != kNoEntry && (tok + 15 >= seen_from || tok < g.a.sinks))
+    kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);  // some row would see it
+  const char *chunk = base + (uint64_t)(uint32_t)max(x.page, 0) * g.page_stride;
+  const char *p = chunk + at * 64 + (lane & 1) * 64 + (lane >> 4) * 16;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    x.ks[nb] = ldg(reinterpret_cast<const uint32_t *>(p + nb * T * 2));
-    x.vs[nb] = ldg(reinterpret_cast<const uint32_t *>(p + (NB + nb) * T * 2));
+    const char *pk = p + nb * T * 64, *pv = p + (NB + nb) * T * 64;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x.v[nb][j] = ldg(reinterpret_cast<const v4i *>(pv + 128 * j));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x.k[nb][j] = ldg(reinterpret_cast<const v4i *>(pk + 128 * j));
+  }
+  const char *ps = chunk + 128 * NB * T + (at + 8 * (lane & 1) + 2 * (lane >> 4)) * 2;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    x.ks[nb] = ldg(reinterpret_cast<const uint32_t *>(ps + nb * T * 2));
+    x.vs[nb] = ldg(reinterpret_cast<const uint32_t *>(ps + (NB + nb) * T * 2));
   }
 }
 
 // Moves a tile's values and scales to the wave's shared memory.  Keys that no row sees get
 // scale zero.  The value scales are multiplied by a power of two that brings the tile's largest
 // to [128, 256); returns its inverse as a matrix instruction's scale byte, per block.
-// A token's four 16-byte parts are permuted by its subtile, which spreads the transposed reads
-// below over the banks.
+// A token's four 16-byte parts are permuted by bits 2 and 3 of its number, which spreads the
+// transposed reads below over the banks.
 template <int NB, int R>
 __device__ __forceinline__ void stage_tile(const AttnArgs &g, const Seq &q, int tile, const Tile<NB> &x, WaveLds<NB, R> &lds,
                                            int (&vbyte)[NB]) {
-  const int lane = threadIdx.x & 63;
+  const int lane = opaque_tid() & 63;
+  char *const to = lds.v + subtile_of(lane) * 1024 + (lane & 1) * 64;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<v4i *>(lds.v + nb * 8192 + j * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ (j & 3)) * 16)) = x.v[nb][j];
-  const int tok = tile * kTile + 2 * lane;
+      *reinterpret_cast<v4i *>(to + (((lane >> 4) ^ (j >> 1)) * 16) + nb * 8192 + 128 * j) = x.v[nb][j];
+  const int at = first_token(lane), tok = tile * kTile + at;
   const bool here = x.page >= 0;
-  const uint32_t keep = (here && tok < q.len && (tok >= q.lo || tok < g.a.sinks) ? 0xFFFFu : 0u) |
-                        (here && tok + 1 < q.len && (tok + 1 >= q.lo || tok + 1 < g.a.sinks) ? 0xFFFF0000u : 0u);
-  const int at = ((lane & 7) >> 1) * 32 + (lane >> 3) * 4 + 2 * (lane & 1);
+  const uint32_t keep = ((here & (tok < q.len) & ((tok >= q.lo) | (tok < g.a.sinks))) ? 0xFFFFu : 0u) |
+                        ((here & (tok + 1 < q.len) & ((tok + 1 >= q.lo) | (tok + 1 < g.a.sinks))) ? 0xFFFF0000u : 0u);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     *reinterpret_cast<uint32_t *>(&lds.ks[nb][at]) = x.ks[nb] & keep;
@@ -294,16 +309,26 @@ __device__ __forceinline__ void stage_tile(const AttnArgs &g, const Seq &q, int 
 }
 
 // A lane's own keys.  With R = 16 / C columns held R times over (few columns: the matrix
-// instruction is 16 wide anyway), replica r of a column takes the NT = 8 / R subtiles from r NT
-// on through the softmax.  Their scales: 2 NT words from shared memory.
+// instruction is 16 wide anyway), replica r of a column takes NW = 8 / R of the lane's eight words
+// of keys through the softmax: NW / 2 from r NW / 2 on in each half.
+template <int R>
+__device__ __forceinline__ int own_key(int lane, int w) {  // first of own word w's four keys
+  constexpr int H = 4 / R;
+  return 32 * (lane >> 4) + 16 * (w / H) + 4 * ((lane & 15) / (kCols / R) * H + w % H);
+}
+// Their scales, two words each.
 template <int R>
 __device__ __forceinline__ void read_scales(const uint16_t *s, uint32_t (&w)[16 / R]) {
-  const int lane = threadIdx.x & 63, r = (lane & 15) / (kCols / R);
-  const u32x4 *p = reinterpret_cast<const u32x4 *>(s + (lane >> 4) * 32 + r * (32 / R));
+  constexpr int H = 4 / R;
+  const int lane = opaque_tid() & 63;
 #pragma unroll
-  for (int t = 0; t < 4 / R; ++t) {
-    const u32x4 v = p[t];
-    w[4 * t] = v[0], w[4 * t + 1] = v[1], w[4 * t + 2] = v[2], w[4 * t + 3] = v[3];
+  for (int half = 0; half < 2; ++half) {
+    const uint16_t *p = s + own_key<R>(lane, half * H);
+#pragma unroll
+    for (int t = 0; t < H; ++t) {
+      const v2i v = reinterpret_cast<const v2i *>(p)[t];
+      w[2 * (half * H + t)] = v[0], w[2 * (half * H + t) + 1] = v[1];
+    }
   }
 }
 template <int N>
@@ -322,41 +347,52 @@ struct Sums {
   float l;  // this lane's share of the sum of weights
 };
 
-// A tile's values as the left operand of the second product: rows are elements 16 dt + (l & 15),
-// the 32 keys of the lane's depth share those that the weights' E4M3 operand has there (lane
-// group g of it: keys 16 t + 4 g + i, t = 0..3 in its first half, 4..7 in its second).
+// A tile's values as the left operand of the second product: rows are elements 16 dt + (l & 15);
+// the lane's depth holds the keys that the weights' E4M3 operand has there: two whole subtiles,
+// read transposed.
 template <int NB, int R>
 __device__ __forceinline__ v8i read_values(const WaveLds<NB, R> &lds, int nb, int dt) {
-  const int lane = threadIdx.x & 63, gv = lane >> 4, r = lane & 15;
-  const int tok = 64 * (gv >> 1) + 16 * (r >> 2) + 8 * (gv & 1) + (r & 3);
-  const char *p = lds.v + nb * 8192 + tok * 64 + (((dt >> 1) ^ (r >> 2)) * 16) + (dt & 1) * 8;
+  const int lane = opaque_tid() & 63, r = lane & 15;
+  const char *p = lds.v + (4 * ((lane >> 4) & 1) + (lane >> 5)) * 1024 + r * 64 + (((dt >> 1) ^ (r >> 2)) * 16);
   typedef __attribute__((address_space(3))) v2i lds_v2i;
-  const v2i a = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)p);
-  const v2i b = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(p + 4 * 64));
+  const v2i a = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(p + nb * 8192 + (dt & 1) * 8));
+  const v2i b = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(p + nb * 8192 + (dt & 1) * 8 + 2048));
   return v8i{a[0], a[1], b[0], b[1], 0, 0, 0, 0};
 }
 
-// Scores of a lane's own keys: x[t][i] belongs to key 16 (r NT + t) + 4 g + i and the lane's
-// column, in units of cf[0] (one block) or in powers of two (two blocks).
+__device__ __forceinline__ v8i read8(const int *p) {
+  const v4i a = *reinterpret_cast<const v4i *>(p), b = *reinterpret_cast<const v4i *>(p + 4);
+  return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// Scores of a lane's own keys (own word t's key i), in units of cf[0] (one block) or in powers of
+// two (two blocks).
 template <int NB, int R>
-__device__ __forceinline__ void scores(const v4i (&k)[NB][8], const Queries<NB> &qr, const WaveLds<NB, R> &lds,
-                                       float (&x)[8 / R][4]) {
-  constexpr int NT = 8 / R;
-  const int r = (threadIdx.x & 15) / (kCols / R);
+__device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB, kCols / R> &q, const Column<NB> &col,
+                                       const WaveLds<NB, R> &lds, float (&x)[8 / R][4]) {
+  constexpr int NT = 8 / R, C = kCols / R;
+  const int lane = opaque_tid() & 63, r = (lane & 15) / C;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     uint32_t ks[16 / R];
     read_scales<R>(lds.ks[nb], ks);
+    v8i part[3];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) part[s] = read8(q.part[nb][s][lane & (C - 1)][lane >> 4]);
     float y[NT][4];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const v8i a = {k[nb][t][0], k[nb][t][1], k[nb][t][2], k[nb][t][3], 0, 0, 0, 0};
+    for (int j = 0; j < 8; ++j) {
+      const v8i a = {k[nb][j][0], k[nb][j][1], k[nb][j][2], k[nb][j][3], 0, 0, 0, 0};
       floatx4 s = {0.f, 0.f, 0.f, 0.f};
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, qr.part[nb][0], s, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, qr.part[nb][1], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, qr.part[nb][2], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+      constexpr int H = 4 / R;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[t % NT][i] = t < NT || r == t / NT ? s[i] : y[t % NT][i];
+      for (int i = 0; i < 4; ++i) {
+        float &z = y[(i >> 1) * H + (j >> 1) % H][2 * (j & 1) + (i & 1)];
+        z = (j >> 1) / H == 0 ? s[i] : r == (j >> 1) / H ? s[i] : z;
+      }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -364,7 +400,7 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const Queries<NB> 
       for (int i = 0; i < 4; ++i) {
         const float z = y[t][i] * scale_of(ks, t, i);
         if (NB == 1) x[t][i] = z;
-        else x[t][i] = nb ? fmaf(z, qr.cf[nb], x[t][i]) : z * qr.cf[nb];
+        else x[t][i] = nb ? fmaf(z, col.cf[nb], x[t][i]) : z * col.cf[nb];
       }
   }
 }
@@ -390,29 +426,23 @@ __device__ __forceinline__ void split3(const float (&w)[4], int &p0, int &p1, in
   p2 = __builtin_bit_cast(int, z);
 }
 
-__device__ __forceinline__ v8i read8(const int *p) {
-  const v4i a = *reinterpret_cast<const v4i *>(p), b = *reinterpret_cast<const v4i *>(p + 4);
-  return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
-
 // One tile into a column tile's sums.  MASK: some row does not see some key of the tile; bad: bit
-// 8 t of a subtile t without a page.
+// 2 s of a subtile s without a page.
 template <int NB, int R, bool MASK>
-__device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint64_t bad, const int (&vbyte)[NB],
-                                         float (&x)[8 / R][4], const Queries<NB> &qr, WaveLds<NB, R> &lds, Sums<NB> &sum) {
-  constexpr int NT = 8 / R, C = kCols / R;
-  const int lane = threadIdx.x & 63, r = (lane & 15) / C, k = lane >> 4;
+__device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t bad, const int (&vbyte)[NB],
+                                         float (&x)[8 / R][4], const Column<NB> &col, WaveLds<NB, R> &lds, Sums<NB> &sum) {
+  constexpr int NT = 8 / R, C = kCols / R, H = 4 / R;
+  const int lane = opaque_tid() & 63, r = (lane & 15) / C, k = lane >> 4;
   uint32_t seen = 0;
   if (MASK) {
-    const int k0 = tile * kTile + 16 * NT * r + 4 * k, rel = qr.pos - k0;
+    const int k0 = tile * kTile + own_key<R>(lane, 0), rel = col.pos - k0;
     const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - k0 : 0;
-    const uint64_t mine = bad >> (8 * NT * r);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int j = 16 * t + i;
-        const bool ok = j <= rel && (j > after || j < sink) && !((mine >> (8 * t)) & 1);
+        const int j = 16 * (t / H) + 4 * (t % H) + i;  // from k0
+        const bool ok = (j <= rel) & ((j > after) | (j < sink)) & !((bad >> (4 * k + 2 * (t / H))) & 1);
         x[t][i] = ok ? x[t][i] : kNegInf;
         seen |= ok ? 1u << (4 * t + i) : 0u;
       }
@@ -423,7 +453,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint64_t b
   if (R >= 4) top = fmaxf(top, lane_xor<4>(top));
   if (R >= 2) top = fmaxf(top, lane_xor<8>(top));
   top = max4(top);
-  const float cf = NB == 1 ? qr.cf[0] : 1.f;
+  const float cf = NB == 1 ? col.cf[0] : 1.f;
   const float m = fmaxf(sum.m, top == kNegInf ? kNegInf : top * cf);
   const float mu = m == kNegInf ? 0.f : m;  // nothing seen so far
   const float alpha = __builtin_amdgcn_exp2f(sum.m - mu);
@@ -459,23 +489,29 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint64_t b
 #pragma unroll
       for (int t = 0; t < 8; ++t) p0[t] = part[0][t], p1[t] = part[1][t], p2[t] = part[2][t];
     } else {
-      // replica r turns from the keys r NT .. of all parts to all keys of part r
+      // replica r turns from its own keys of all parts to all keys of part r
       const int h = lane & (C - 1), row = (k * C + h) * 3;
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
-        int *to = lds.w[row + s] + r * NT;
-        if constexpr (R == 4) *reinterpret_cast<v2i *>(to) = v2i{part[s][0], part[s][1]};
-        else *reinterpret_cast<v4i *>(to) = v4i{part[s][0], part[s][1], part[s][2], part[s][3]};
+        int *to = lds.w[row + s] + r * H;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if constexpr (R == 4) to[4 * half] = part[s][half];
+          else *reinterpret_cast<v2i *>(to + 4 * half) = v2i{part[s][2 * half], part[s][2 * half + 1]};
+        }
       }
       constexpr int zeros = 4 * C * 3;
       p0 = read8(lds.w[r < 3 ? row + r : zeros]);
       if constexpr (R == 2) p1 = read8(lds.w[r == 0 ? row + 2 : zeros]);
     }
     const int b0 = vbyte[nb] - (R > 1 ? 5 * r : 0);
+    if (__any(alpha != 1.f))  // (rare once the first tiles are done)
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) sum.o[nb][dt] *= alpha;
 #pragma unroll
     for (int dt = 0; dt < 8; ++dt) {
       const v8i v = read_values(lds, nb, dt);
-      floatx4 o = sum.o[nb][dt] * alpha;
+      floatx4 o = sum.o[nb][dt];
       o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p0, o, 4, 0, 0, scale_byte(0), 0, b0);
       if constexpr (R == 2) o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p1, o, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
       if constexpr (R == 1) {
@@ -514,20 +550,24 @@ __device__ __forceinline__ void write_block(const AttnArgs &g, const Seq &q, int
 // turn, each with its own sums, joined in shared memory at a segment's end (a segment: one
 // (sequence, head, column tile)).  A segment that several workgroups share is joined by the last
 // of them to arrive, in order, so results do not depend on timing.
-constexpr int kWaves = 4;
-constexpr int kMinChunk = 8;  // tiles: two a wave; a join costs more than a second tile
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kMinChunk = 2 * kWaves;  // tiles: two a wave; a join costs more than a second tile
+// What starting and ending a segment costs a workgroup, in tiles (64 ragged contexts: 106.7 us at 0,
+// 100.0 at 2, 98.0 at 4, 98.3 at 6).
+constexpr int kSegCost = 4;
 
 template <int NB, int R>
 struct NarrowLds {
+  QueryLds<NB, kCols / R> q;
   WaveLds<NB, R> wave[kWaves];
   float ml[kWaves][2][kCols];
-  long long scan[kWaves + 1];
+  long long scan[kWaves];
   long long found[2];
   int last;
 };
 
 // Exclusive prefix sum over the workgroup; *total gets the sum.
-__device__ __forceinline__ long long prefix256(long long v, long long *lds, long long *total) {
+__device__ __forceinline__ long long block_prefix(long long v, long long *lds, long long *total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   long long x = v;
 #pragma unroll
@@ -550,83 +590,187 @@ __device__ __forceinline__ long long prefix256(long long v, long long *lds, long
 
 __device__ __forceinline__ int padded(int tiles) { return (tiles + kMinChunk - 1) / kMinChunk * kMinChunk; }
 
+__device__ __forceinline__ long long quotient(long long a, long long b) {  // of small numbers quickly
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// One segment, or the stretch of it that a workgroup has: key tiles t0 .. t1 - 1.
+struct Segment {
+  Seq q;
+  int s, head, col0, t0, t1;
+  int per;          // the segment's length in the line: its tiles after kSegCost (its tiles rounded up to whole
+                    // chunks where all are)
+  long long begin;  // the place of its first tile
+};
+
+// Resident waves a SIMD: two blocks need more than 256 registers for a tile on its way and the sums.
+template <int NB, int R>
+constexpr int narrow_waves() { return NB == 1 ? 2 : 1; }
+
 template <bool BF, int NB, int R>
-__global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(AttnArgs g) {
+__global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_narrow_kernel(AttnArgs g) {
   constexpr int D = 128 * NB, C = kCols / R, kPart = C * (D + 8);
   extern __shared__ __attribute__((aligned(16))) char raw[];
   NarrowLds<NB, R> &lds = *reinterpret_cast<NarrowLds<NB, R> *>(raw);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n_seq = g.a.b.n_seq, Hk = g.a.c.n_kv_heads;
-  // the line's length, with and without segments rounded up to whole chunks
-  long long exact = 0, round = 0, w_exact = 0, w_round = 0, p_exact = 0, p_round = 0;
-  for (int s0 = 0; s0 < n_seq; s0 += 256) {
-    const int s = s0 + tid;
-    w_exact = w_round = 0;
-    if (s < n_seq) {
-      const Seq q = seq_of<C>(g, s, blockIdx.x == 0);
-      w_exact = (long long)Hk * q.col_tiles * q.tiles;
-      w_round = (long long)Hk * q.col_tiles * padded(q.tiles);
-    }
-    long long t;
-    p_exact = exact + prefix256(w_exact, lds.scan, &t);
-    exact += t;
-    p_round = round + prefix256(w_round, lds.scan, &t);
-    round += t;
-  }
+  const int G = gridDim.x;
   if (blockIdx.x == 0) {  // rows that no sequence has
     const int end = min(max(n_seq ? ldg(g.a.b.cu + n_seq) : 0, 0), g.a.b.rows);
     if (end < g.a.b.rows) {
       if (tid == 0) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
       const size_t words = (size_t)g.a.n_q_heads * D / 2;
-      for (size_t i = end * words + tid; i < g.a.b.rows * words; i += 256) static_cast<uint32_t *>(g.a.y)[i] = 0;
+      for (size_t i = end * words + tid; i < g.a.b.rows * words; i += kThreads) static_cast<uint32_t *>(g.a.y)[i] = 0;
       if (g.a.lse)
-        for (size_t i = (size_t)end * g.a.n_q_heads + tid; i < (size_t)g.a.b.rows * g.a.n_q_heads; i += 256) g.a.lse[i] = kNegInf;
+        for (size_t i = (size_t)end * g.a.n_q_heads + tid; i < (size_t)g.a.b.rows * g.a.n_q_heads; i += kThreads) g.a.lse[i] = kNegInf;
     }
   }
-  const int G = gridDim.x;
-  const bool whole = round <= (long long)kMinChunk * G;  // short contexts: whole chunks to a segment
-  const long long U = whole ? round : exact, chunk = whole ? kMinChunk : (exact + G - 1) / G;
-  long long u = blockIdx.x * chunk;
-  const long long u1 = min(u + chunk, U);
-  if (u >= u1) return;
-  // the sequence of the first unit
-  if (tid == 0) lds.found[0] = -1;
-  __syncthreads();
-  if (n_seq <= 256) {
-    const long long p = whole ? p_round : p_exact, w = whole ? w_round : w_exact;
-    if (u >= p && u < p + w) lds.found[0] = tid, lds.found[1] = p;
-  } else {
-    long long base = 0;
-    for (int s0 = 0; s0 < n_seq; s0 += 256) {
-      const int s = s0 + tid;
-      long long w = 0, t;
-      if (s < n_seq) {
-        const Seq q = seq_of<C>(g, s, false);
-        w = (long long)Hk * q.col_tiles * (whole ? padded(q.tiles) : q.tiles);
+  // ---- the line's length, with and without segments rounded up to whole chunks, and the
+  // sequence of this workgroup's first unit
+  bool whole = false;  // short contexts: whole chunks to a segment
+  long long U = 0, chunk = 0, u = 0, u1 = 0, pre = 0;
+  Segment c;
+  c.s = -1;
+  bool small = n_seq <= 64;
+  if (small) {  // every wave by itself, a lane a sequence
+    Seq q{};
+    int we = 0, wr = 0;
+    if (lane < n_seq) {
+      q = seq_of<C>(g, lane, blockIdx.x == 0 && wave == 0);
+      const long long segs = (long long)Hk * q.col_tiles;
+      small = segs * padded(q.tiles) < (1 << 24);
+      we = (int)min(segs * (kSegCost + q.tiles), 1LL << 24);
+      wr = (int)min(segs * padded(q.tiles), 1LL << 24);
+    }
+    small = __all(small);
+    if (small) {
+      int pe = we, pr = wr;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int a = __shfl_up(pe, d, 64), b = __shfl_up(pr, d, 64);
+        if (lane >= d) pe += a, pr += b;
       }
-      const long long p = base + prefix256(w, lds.scan, &t);
-      if (u >= p && u < p + w) lds.found[0] = s, lds.found[1] = p;
-      base += t;
-      if (u < base) break;  // (uniform)
+      const int exact = __builtin_amdgcn_readlane(pe, 63), round = __builtin_amdgcn_readlane(pr, 63);
+      whole = round <= (long long)kMinChunk * G;
+      U = whole ? round : exact;
+      chunk = whole ? kMinChunk : ((uint32_t)exact + G - 1) / (uint32_t)G;
+      u = blockIdx.x * chunk;
+      u1 = min(u + chunk, U);
+      if (u >= u1) return;
+      const int end = whole ? pr : pe, w = whole ? wr : we;
+      const uint64_t hit = __ballot(u >= end - w && u < end);
+      c.s = __builtin_ctzll(hit);  // (the weights cover [0, U): one lane has it)
+      pre = __builtin_amdgcn_readlane(end - w, c.s);
+      c.q = seq_from(q, c.s);
     }
   }
-  __syncthreads();
-  int s = __builtin_amdgcn_readfirstlane((int)lds.found[0]);
-  if (s < 0) return;  // (the lengths changed under the call)
-  long long pre = lds.found[1];
-  Seq q = seq_of<C>(g, s, false);
-  if (q.col_tiles == 0) return;
+  if (!small) {
+    long long exact = 0, round = 0;
+    for (int s0 = 0; s0 < n_seq; s0 += kThreads) {
+      long long we = 0, wr = 0, t;
+      if (s0 + tid < n_seq) {
+        const Seq q = seq_of<C>(g, s0 + tid, blockIdx.x == 0);
+        we = (long long)Hk * q.col_tiles * (kSegCost + q.tiles);
+        wr = (long long)Hk * q.col_tiles * padded(q.tiles);
+      }
+      block_prefix(we, lds.scan, &t);
+      exact += t;
+      block_prefix(wr, lds.scan, &t);
+      round += t;
+    }
+    whole = round <= (long long)kMinChunk * G;
+    U = whole ? round : exact;
+    chunk = whole ? kMinChunk : (exact + G - 1) / G;
+    u = blockIdx.x * chunk;
+    u1 = min(u + chunk, U);
+    if (u >= u1) return;
+    if (tid == 0) lds.found[0] = -1;
+    __syncthreads();
+    long long base = 0;
+    for (int s0 = 0; s0 < n_seq && u >= base; s0 += kThreads) {
+      long long w = 0, t;
+      if (s0 + tid < n_seq) {
+        const Seq q = seq_of<C>(g, s0 + tid, false);
+        w = (long long)Hk * q.col_tiles * (whole ? padded(q.tiles) : kSegCost + q.tiles);
+      }
+      const long long p = base + block_prefix(w, lds.scan, &t);
+      if (u >= p && u < p + w) lds.found[0] = s0 + tid, lds.found[1] = p;
+      base += t;
+    }
+    __syncthreads();
+    c.s = __builtin_amdgcn_readfirstlane((int)lds.found[0]);
+    if (c.s < 0) return;  // (the lengths changed under the call)
+    pre = lds.found[1];
+    c.q = seq_from(seq_of<C>(g, c.s, false), 0);
+  }
+  if (c.q.col_tiles == 0) return;  // (as above)
+  const int ahead = whole ? 0 : kSegCost;  // of a segment's tiles
+  c.per = whole ? padded(c.q.tiles) : ahead + c.q.tiles;
+  {
+    const long long seg = quotient(u - pre, c.per);
+    c.begin = pre + seg * c.per + ahead;
+    c.t0 = (int)max(u - c.begin, 0LL);
+    c.t1 = (int)min((long long)c.q.tiles, u1 - c.begin);
+    c.head = (int)quotient(seg, c.q.col_tiles);
+    c.col0 = (int)(seg - (long long)c.head * c.q.col_tiles) * C;
+    if (c.t1 <= 0) return;  // (only the start of a segment that others have)
+  }
+  // ---- segment by segment; the next one's query, pages and first tile are on their way while this
+  // one is worked on
+  WaveLds<NB, R> &mine = lds.wave[wave];
+  if (R > 1 && lane < 8) mine.w[4 * C * 3][lane] = 0;
+  Tile<NB> x;
+  QueryRaw<NB> query = load_query<NB, C>(g, c.q, c.head, c.col0);
+  const char *base = kv4_chunk(g.a.c, g.a.layer, 0, c.head);
+  {
+    const int t = c.t0 + wave;
+    if (t < c.t1 && c.q.len > 0) load_tile(g, c.q.lo, base, tile_at(c.q, t), tile_entry(g, c.q, tile_at(c.q, t)), x);
+  }
   for (;;) {
-    const int per = whole ? padded(q.tiles) : q.tiles;
-    const long long r = u - pre;
-    const int seg = (int)(r / per), t0 = (int)(r % per);
-    const int t1 = (int)min((long long)q.tiles, t0 + (u1 - u));
-    const int head = seg / q.col_tiles, col0 = (seg % q.col_tiles) * C;
-    const long long begin = pre + (long long)seg * per;
-    // ---- this wave's tiles
-    const Queries<NB> qr = load_queries<BF, NB, R>(g, q, head, col0);
+    const Seq &q = c.q;
+    const int head = c.head, col0 = c.col0;
+    int t = c.t0 + wave;
+    const int t1 = c.t1;
+    int entry = kNoEntry, entry_n = kNoEntry;
+    if (t + kWaves < t1 && q.len > 0) entry = tile_entry(g, q, tile_at(q, t + kWaves));
+    // the next segment
+    Segment n = c;
+    n.begin = c.begin + c.per;
+    bool more = n.begin < u1;
+    bool first_n = false;  // this wave has a tile of it
+    QueryRaw<NB> query_n = query;
+    if (more) {
+      n.t0 = 0;
+      n.col0 += C;
+      if (n.col0 >= q.col_tiles * C) {
+        n.col0 = 0;
+        if (++n.head == Hk) {
+          n.head = 0;
+          do {
+            if (++n.s >= n_seq) return;  // (the lengths changed under the call)
+            n.q = seq_from(seq_of<C>(g, n.s, false), 0);
+          } while (n.q.col_tiles == 0);
+          n.per = whole ? padded(n.q.tiles) : ahead + n.q.tiles;
+        }
+      }
+      n.t1 = (int)min((long long)n.q.tiles, u1 - n.begin);
+      first_n = wave < n.t1 && n.q.len > 0;
+      if (first_n) entry_n = tile_entry(g, n.q, tile_at(n.q, wave));
+      query_n = load_query<NB, C>(g, n.q, n.head, n.col0);
+    }
+    const char *base_n = kv4_chunk(g.a.c, g.a.layer, 0, n.head);
+    put_query<BF, NB, C>(g, query, lds.q);
+    __syncthreads();
     const int cols = (int)min((long long)C, (long long)q.n * g.group - col0);
     const int pos0 = q.len - q.n + col0 / g.group, pos1 = q.len - q.n + (col0 + cols - 1) / g.group;
+    Column<NB> column;
+    {
+      const int cc = lane & (C - 1);
+      column.pos = cc < cols ? q.len - q.n + (col0 + cc) / g.group : -1;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) column.cf[nb] = lds.q.cf[nb][cc];
+    }
+    // ---- this wave's tiles
     Sums<NB> sum;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -634,34 +778,31 @@ __global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(A
       for (int dt = 0; dt < 8; ++dt) sum.o[nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
     sum.m = kNegInf;
     sum.l = 0.f;
-    WaveLds<NB, R> &mine = lds.wave[wave];
-    if (R > 1 && lane < 8) mine.w[4 * C * 3][lane] = 0;
-    const char *base = kv4_chunk(g.a.c, g.a.layer, 0, head);
-    int t = t0 + wave;
-    Tile<NB> x;
-    int pages = -1;
-    if (t < t1 && q.len > 0) {
-      load_tile(g, base, tile_at(q, t), tile_pages(g, q, tile_at(q, t)), x);
-      if (t + kWaves < t1) pages = tile_pages(g, q, tile_at(q, t + kWaves));
-      while (true) {
-        const int tile = tile_at(q, t), k0 = tile * kTile;
-        const uint64_t bad = __ballot(x.page < 0);
-        int vbyte[NB];
+    for (;; t += kWaves) {
+      const bool work = t < t1 && q.len > 0, last = t + kWaves >= t1;
+      const int tile = tile_at(q, t), k0 = tile * kTile;
+      uint32_t bad = 0;
+      int vbyte[NB];
+      float sc[8 / R][4];
+      if (work) {
+        bad = (uint32_t)__ballot(x.page < 0) & 0x5555u;  // (lanes 2 s have subtile s)
         stage_tile(g, q, tile, x, mine, vbyte);
-        float sc[8 / R][4];
-        scores<NB, R>(x.k, qr, mine, sc);
-        const int next = t + kWaves;
-        if (next < t1) {
-          load_tile(g, base, tile_at(q, next), pages, x);
-          if (next + kWaves < t1) pages = tile_pages(g, q, tile_at(q, next + kWaves));
-        }
+        scores<NB, R>(x.k, lds.q, column, mine, sc);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // (the next tile's loads reuse the registers of this one)
+      if (!last || first_n) {
+        load_tile(g, last ? n.q.lo : q.lo, last ? base_n : base, last ? tile_at(n.q, wave) : tile_at(q, t + kWaves),
+                  last ? entry_n : entry, x);
+        if (t + 2 * kWaves < t1) entry = tile_entry(g, q, tile_at(q, t + 2 * kWaves));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (work) {
         const bool all = k0 + kTile - 1 <= pos0 && bad == 0 &&
                          (g.a.window == 0 || k0 > pos1 - g.a.window || k0 + kTile <= g.a.sinks);
-        if (all) add_tile<NB, R, false>(g, tile, bad, vbyte, sc, qr, mine, sum);
-        else add_tile<NB, R, true>(g, tile, bad, vbyte, sc, qr, mine, sum);
-        if (next >= t1) break;
-        t = next;
+        if (all) add_tile<NB, R, false>(g, tile, bad, vbyte, sc, column, mine, sum);
+        else add_tile<NB, R, true>(g, tile, bad, vbyte, sc, column, mine, sum);
       }
+      if (last) break;
     }
     // ---- join the waves
     float l = sum.l;
@@ -709,7 +850,8 @@ __global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(A
         }
       }
     }
-    const int w0 = (int)(begin / chunk), w1 = (int)((begin + q.tiles - 1) / chunk);  // the workgroups that share the segment
+    // the workgroups that share the segment
+    const int w0 = (int)quotient(c.begin, chunk), w1 = (int)quotient(c.begin + q.tiles - 1, chunk);
     if (w0 == w1) {
       if ((tid >> 4) < cols)
 #pragma unroll
@@ -745,35 +887,44 @@ __global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(A
       __syncthreads();
       if (__builtin_amdgcn_readfirstlane(lds.last)) {
         // `sub` shares of the parts run side by side where there are few columns
-        const int width = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : cols <= 8 ? 8 : 16, subs = kCols / width;
-        const int sub = (tid >> 4) / width, c = (tid >> 4) % width;
+        const int width = cols <= 1 ? 1 : cols <= 2 ? 2 : cols <= 4 ? 4 : cols <= 8 ? 8 : 16, subs = kThreads / 16 / width;
+        const int sub = (tid >> 4) / width, cc = (tid >> 4) % width;
         float m = kNegInf, l2 = 0.f, acc[NB][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[nb][e] = 0.f;
-        if (c < cols)
-#pragma unroll 4
-          for (int w = w0 + sub; w <= w1; w += subs) {
-            const int at = ((w * 2 + (w == w0 ? 1 : 0)) * kPart + c * (D + 8)) * 4;
-            const u32x2 ml = __builtin_amdgcn_raw_buffer_load_b64(rs, at + D * 4, 0, kSC1);
-            u32x4 p[NB][2];
+        // the loads of several parts are in flight together (each is a trip to memory)
+        constexpr int kBatch = NB == 1 ? 8 : 4;
+        if (cc < cols)
+          for (int w = w0 + sub; w <= w1; w += kBatch * subs) {
+            u32x2 ml[kBatch];
+            u32x4 p[kBatch][NB][2];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              p[nb][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i) * 4, 0, kSC1);
-              p[nb][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
+            for (int k = 0; k < kBatch; ++k) {
+              const int from = min(w + k * subs, w1), at = ((from * 2 + (from == w0 ? 1 : 0)) * kPart + cc * (D + 8)) * 4;
+              ml[k] = __builtin_amdgcn_raw_buffer_load_b64(rs, at + D * 4, 0, kSC1);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                p[k][nb][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i) * 4, 0, kSC1);
+                p[k][nb][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
+              }
             }
-            const uint32_t mw = ml[0], lw = ml[1];
-            const float pm = __builtin_bit_cast(float, mw), pl = __builtin_bit_cast(float, lw);
-            const float m2 = fmaxf(m, pm), u2 = m2 == kNegInf ? 0.f : m2;
-            const float fa = __builtin_amdgcn_exp2f(m - u2), fb = __builtin_amdgcn_exp2f(pm - u2);
-            m = m2;
-            l2 = l2 * fa + pl * fb;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int k = 0; k < kBatch; ++k) {
+              if (w + k * subs > w1) break;
+              const uint32_t mw = ml[k][0], lw = ml[k][1];
+              const float pm = __builtin_bit_cast(float, mw), pl = __builtin_bit_cast(float, lw);
+              const float m2 = fmaxf(m, pm), u2 = m2 == kNegInf ? 0.f : m2;
+              const float fa = __builtin_amdgcn_exp2f(m - u2), fb = __builtin_amdgcn_exp2f(pm - u2);
+              m = m2;
+              l2 = l2 * fa + pl * fb;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                acc[nb][e] = acc[nb][e] * fa + __builtin_bit_cast(float, (uint32_t)p[nb][e >> 2][e & 3]) * fb;
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  acc[nb][e] = acc[nb][e] * fa + __builtin_bit_cast(float, (uint32_t)p[k][nb][e >> 2][e & 3]) * fb;
+            }
           }
         // the shares, in order
         float *all = reinterpret_cast<float *>(lds.wave);
@@ -787,7 +938,7 @@ __global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(A
           put[8 * NB + 1] = l2;
         }
         __syncthreads();
-        if (sub == 0 && c < cols) {
+        if (sub == 0 && cc < cols) {
           for (int k = 1; k < subs; ++k) {
             const float *from = all + (tid + k * width * 16) * (8 * NB + 2);
             const float pm = from[8 * NB], m2 = fmaxf(m, pm), u2 = m2 == kNegInf ? 0.f : m2;
@@ -800,26 +951,20 @@ __global__ __launch_bounds__(256, NB == 1 ? 2 : 1) void kv4_attn_narrow_kernel(A
               for (int e = 0; e < 8; ++e) acc[nb][e] = acc[nb][e] * fa + from[nb * 8 + e] * fb;
           }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + c, nb, acc[nb], m, l2);
+          for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + cc, nb, acc[nb], m, l2);
         }
       }
     }
-    // ---- the next segment
-    u = min(u1, begin + per);
-    if (u >= u1) break;
+    if (!more) break;
+    c = n;
+    query = query_n;
+    base = base_n;
     __syncthreads();  // shared memory is free again
-    while (u >= pre + (long long)Hk * q.col_tiles * per) {
-      pre += (long long)Hk * q.col_tiles * (whole ? padded(q.tiles) : q.tiles);
-      if (++s >= n_seq) return;  // (as above)
-      q = seq_of<C>(g, s, false);
-      if (q.col_tiles > 0) break;
-    }
   }
 }
 
 // How often the narrow kernel holds a column: as many columns as the sequences' rows are known or
-// expected to have, up to 4, 8 or 16 a tile.  64 ragged contexts of 32 / 8 heads (4 columns):
-// MEASURED_R.
+// expected to have, up to 4, 8 or 16 a tile.
 int replicas(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads, int max_rows) {
   const long long rows = max_rows > 0 ? max_rows : ((long long)b.rows + b.n_seq - 1) / b.n_seq;
   const long long cols = rows * (n_q_heads / c.n_kv_heads);
@@ -833,7 +978,7 @@ int narrow_grid(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_
   const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
   const long long cols = ((long long)b.rows * group + C - 1) / C + b.n_seq;  // column tiles, at most
   const long long chunks = (tiles + kMinChunk - 1) / kMinChunk;
-  const long long most = (long long)micro_cus() * (c.head_dim == 128 ? 2 : 1);
+  const long long most = (long long)micro_cus() * (c.head_dim == 128 ? narrow_waves<1, 1>() : narrow_waves<2, 1>());
   const double want = (double)cols * c.n_kv_heads * chunks;
   return want < (double)most ? (want < 1 ? 1 : (int)want) : (int)most;
 }
@@ -846,7 +991,7 @@ hipError_t launch_narrow(const AttnArgs &g, hipStream_t stream) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  kernel<<<narrow_grid(g.a.c, g.a.b, g.a.n_q_heads, kCols / R), 256, lds, stream>>>(g);
+  kernel<<<narrow_grid(g.a.c, g.a.b, g.a.n_q_heads, kCols / R), kThreads, lds, stream>>>(g);
   return hipGetLastError();
 }
 

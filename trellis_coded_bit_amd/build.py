@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtrellis.so")
 SOURCES = ["api.cpp", "decode.hip", "hadamard.hip", "gemv.hip", "gemm.hip", "encode.hip", "micro.hip",
-           "api_kv4.cpp", "kv4.hip", "kv4_attn.hip"]
+           "api_kv4.cpp", "kv4.hip", "kv4_attn.hip", "kv4_attn_wide.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 COMMON = [

@@ -1,0 +1,240 @@
+// What the attention kernels over the 4-bit cache share (their mathematics: kv4_attn.hip).
+#pragma once
+#include "kv4_device.h"
+
+namespace trellis {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef short v2s __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 128;  // keys of a tile: the depth of one matrix instruction
+constexpr int kCols = 16;   // (row, head) pairs of a tile: its width
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+struct AttnArgs {
+  Kv4Attn a;
+  uint32_t *errword;
+  uint32_t *counters;  // one per workgroup, zero between calls
+  int few;             // sequences of at most so many columns are the narrow kernel's, others the wide one's
+  int tends;           // this launch checks the sequences and clears the rows that none has
+  int splits;          // wide: workgroups that share a segment
+  float *parts;        // [workgroups][2][C][D + 8]: unnormalised sums, then maximum, sum of weights
+  int group;           // query heads per key/value head
+  int page_shift;      // log2 of the page size
+  uint32_t page_stride;  // bytes from page to page of a layer
+};
+
+// A sequence's geometry, from device memory (every thread of a workgroup computes the same).
+struct Seq {
+  int slot, len, n, c0;     // n rows from c0 on
+  int lo;                   // keys below lo are seen by no row but as sinks
+  int n_sink, first, tiles; // key tiles: [0, n_sink), then first ..; `tiles` in all, at least one
+  int col_tiles;            // tiles of C (row, head) columns of one key/value head; 0: not this kernel's
+};
+
+template <int C>
+__device__ Seq seq_of(const AttnArgs &g, int s, bool flag) {
+  const trellis_kv4_batch &b = g.a.b;
+  Seq q;
+  const int c0 = ldg(b.cu + s), c1 = ldg(b.cu + s + 1);
+  const bool rows_ok = c0 >= 0 && c1 >= c0 && c1 <= b.rows;
+  q.c0 = rows_ok ? c0 : 0;
+  q.n = rows_ok ? c1 - c0 : 0;
+  q.slot = b.slots ? ldg(b.slots + s) : s;
+  bool ok = (uint32_t)q.slot < (uint32_t)b.n_slots;
+  q.slot = ok ? q.slot : 0;
+  q.len = ldg(b.lens + q.slot);
+  if (q.len < 0 || q.len > (long long)b.max_pages * g.a.c.page_size) ok = false;
+  if (!ok) q.len = 0;
+  if (flag && !(ok && rows_ok)) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
+  const int lo = q.len - q.n - g.a.window + 1;  // of the first row
+  q.lo = g.a.window && lo > 0 ? lo : 0;
+  q.first = q.lo / kTile;
+  const int sinks = (min(g.a.sinks, q.len) + kTile - 1) / kTile;
+  q.n_sink = min(sinks, q.first);
+  q.tiles = max(1, q.n_sink + (q.len + kTile - 1) / kTile - q.first);
+  const long long cols = (long long)q.n * g.group;
+  q.col_tiles = (cols <= g.few) == (C <= kCols) ? (int)((cols + C - 1) / C) : 0;
+  return q;
+}
+
+// The same with every field in scalar registers, from lane `l`.
+__device__ __forceinline__ Seq seq_from(const Seq &q, int l) {
+  Seq r;
+  r.slot = __builtin_amdgcn_readlane(q.slot, l);
+  r.len = __builtin_amdgcn_readlane(q.len, l);
+  r.n = __builtin_amdgcn_readlane(q.n, l);
+  r.c0 = __builtin_amdgcn_readlane(q.c0, l);
+  r.lo = __builtin_amdgcn_readlane(q.lo, l);
+  r.n_sink = __builtin_amdgcn_readlane(q.n_sink, l);
+  r.first = __builtin_amdgcn_readlane(q.first, l);
+  r.tiles = __builtin_amdgcn_readlane(q.tiles, l);
+  r.col_tiles = __builtin_amdgcn_readlane(q.col_tiles, l);
+  return r;
+}
+
+__device__ __forceinline__ int tile_at(const Seq &q, int t) { return t < q.n_sink ? t : q.first + t - q.n_sink; }
+
+// Exchanges between the lanes l, l ^ 32 (16) of two registers: afterwards a has both registers'
+// lanes of the lower half (even rows of 16), b the upper.
+__device__ __forceinline__ void swap32(float &a, float &b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = r[0], y = r[1];  // (a bit cast of a vector's element itself reads element 0)
+  a = __builtin_bit_cast(float, x);
+  b = __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ void swap16(float &a, float &b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = r[0], y = r[1];  // (a bit cast of a vector's element itself reads element 0)
+  a = __builtin_bit_cast(float, x);
+  b = __builtin_bit_cast(float, y);
+}
+// The value's maximum / sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float max4(float v) {
+  float a = v, b = v;
+  swap16(a, b);
+  a = b = fmaxf(a, b);
+  swap32(a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float sum4(float v) {
+  float a = v, b = v;
+  swap16(a, b);
+  a = b = a + b;
+  swap32(a, b);
+  return a + b;
+}
+
+// Byte of a power of two 2^e as a matrix instruction's scale.
+__device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
+
+// C columns' rotated queries as matrix operands, in shared memory: lane group g of a column's
+// E4M3 operand holds elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block.
+template <int NB, int C>
+struct QueryLds {
+  alignas(16) int part[NB][3][C][4][8];
+  float cf[NB][C];  // score = cf * (sum over parts), in powers of two; >= 0
+};
+
+// Sixteen lanes to a column, eight elements each.
+template <int NB>
+struct QueryRaw {
+  u32x4 x[NB];
+};
+template <int NB, int C>
+__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, int col0) {
+  QueryRaw<NB> r;
+  const int c = col0 + (threadIdx.x >> 4);
+  const bool ok = (int)(threadIdx.x >> 4) < C && c < (long long)q.n * g.group;
+  const uint16_t *p = static_cast<const uint16_t *>(g.a.q.p);
+  if (ok) p += (int64_t)(q.c0 + c / g.group) * g.a.q.row_stride + (head * g.group + c % g.group) * g.a.q.head_stride + 8 * (threadIdx.x & 15);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    r.x[nb] = u32x4{0, 0, 0, 0};
+    if (ok) r.x[nb] = ldg(reinterpret_cast<const u32x4 *>(p + nb * 128));
+  }
+  return r;
+}
+
+template <bool BF, int NB, int C>
+__device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> &raw, QueryLds<NB, C> &lds) {
+  const int c = threadIdx.x >> 4, i = threadIdx.x & 15;
+  if (c >= C) return;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float x[8];
+    kv4_unpack8<BF>(raw.x[nb], x);
+    kv4_fwht16(x, threadIdx.x & 63);
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      top = fmaxf(top, fabsf(x[t]));
+      finite &= fabsf(x[t]) <= 3.4028234e38f;
+    }
+    top = finite ? top : __builtin_inff();
+    top = fmaxf(top, lane_xor<1>(top));
+    top = fmaxf(top, lane_xor<2>(top));
+    top = fmaxf(top, lane_xor<4>(top));
+    top = fmaxf(top, lane_xor<8>(top));
+    // the largest element comes to [128, 256); a column that is not finite becomes NaN
+    const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 8);
+    float f = __builtin_bit_cast(float, (uint32_t)min(261 - e, 254) << 23);
+    if (top > 3.4028234e38f) f = __builtin_nanf("");
+    if (g.a.scale < 0.f) f = -f;
+    if (i == 0) lds.cf[nb][c] = __builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) x[t] *= f;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      v2i o;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        int z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w], x[4 * w + 1], 0, false);
+        z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w + 2], x[4 * w + 3], z, true);
+        o[w] = z;
+        const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8(z, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(z, true);
+        // what is left, times 16: at most 128
+        x[4 * w] = (x[4 * w] - a[0]) * 16.f;
+        x[4 * w + 1] = (x[4 * w + 1] - a[1]) * 16.f;
+        x[4 * w + 2] = (x[4 * w + 2] - b[0]) * 16.f;
+        x[4 * w + 3] = (x[4 * w + 3] - b[1]) * 16.f;
+      }
+      *reinterpret_cast<v2i *>(&lds.part[nb][s][c][(i & 7) >> 1][(i >> 3) * 4 + (i & 1) * 2]) = o;
+    }
+  }
+}
+
+// What a lane keeps of its column.
+template <int NB>
+struct Column {
+  float cf[NB];
+  int pos;  // the column's position (-1: sees nothing)
+};
+
+__device__ __forceinline__ v8i read8(const int *p) {
+  const v4i a = *reinterpret_cast<const v4i *>(p), b = *reinterpret_cast<const v4i *>(p + 4);
+  return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+constexpr int kRowF = 132;  // floats of a column's sums in shared memory: 128, and 4 to spread the banks
+
+// Clears the rows past the last sequence's (one workgroup).
+template <int NB, int THREADS>
+__device__ __forceinline__ void clear_rest(const AttnArgs &g) {
+  const int n_seq = g.a.b.n_seq, end = min(max(n_seq ? ldg(g.a.b.cu + n_seq) : 0, 0), g.a.b.rows);
+  if (end >= g.a.b.rows) return;
+  if (threadIdx.x == 0) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
+  const size_t words = (size_t)g.a.n_q_heads * 64 * NB;
+  for (size_t i = end * words + threadIdx.x; i < g.a.b.rows * words; i += THREADS) static_cast<uint32_t *>(g.a.y)[i] = 0;
+  if (g.a.lse)
+    for (size_t i = (size_t)end * g.a.n_q_heads + threadIdx.x; i < (size_t)g.a.b.rows * g.a.n_q_heads; i += THREADS) g.a.lse[i] = kNegInf;
+}
+
+// Writes one column block's result: 16 lanes, eight elements each, still rotated and not
+// normalised.
+template <bool BF>
+__device__ __forceinline__ void write_block(const AttnArgs &g, const Seq &q, int head, int c, int nb, float (&v)[8], float m,
+                                            float l) {
+  const int i = threadIdx.x & 15;
+  kv4_fwht16(v, threadIdx.x & 63);
+  const float f = l == 0.f ? 0.f : kRsqrt128 / l;  // (nothing seen: zero)
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] *= f;
+  if (l == 0.f)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = 0.f;
+  const size_t at = (size_t)(q.c0 + c / g.group) * g.a.n_q_heads + head * g.group + c % g.group;
+  uint16_t *y = static_cast<uint16_t *>(g.a.y) + at * g.a.c.head_dim + nb * 128 + 8 * i;
+  *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(v);
+  if (g.a.lse && nb == 0 && i == 0) g.a.lse[at] = l == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Many columns per sequence (kv4_attn_wide.hip).
+size_t kv4_attn_wide_parts(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads);  // bytes of g.parts
+hipError_t launch_kv4_attn_wide(const AttnArgs &g, hipStream_t stream);
+
+}  // namespace trellis

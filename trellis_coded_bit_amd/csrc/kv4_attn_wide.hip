@@ -1,0 +1,486 @@
+// Attention over the 4-bit key/value cache, many columns per sequence: prompts and chunks of them.
+// (Mathematics and formats: kv4_attn.hip.)
+//
+// A workgroup takes 128 columns (rows times the query heads of one key/value head) of one sequence
+// and walks its key tiles of 128; a wave has 32 of the columns, as two tiles of 16.  A tile's codes
+// pass through shared memory once for all four waves, in two buffers, with one barrier a tile.
+//
+// Scores are as in the narrow kernel: codes against three E4M3 parts of the query.  The second
+// product is different: at 32 columns a wave the three-way split of the weights would cost more
+// vector instructions than unpacking the values, so a value tile's codes are read transposed and
+// turned to fp16 in registers (exactly), once for both column tiles, and the weights p vs are rounded
+// once to fp16 (within 2^-12), with one power of two per wave that follows the tiles' largest value
+// scale.  The softmax's vector instructions and the two products' matrix instructions take about the
+// same time (MEASURED_WIDE); two workgroups a CU overlap them.
+#include "kv4_attn_device.h"
+
+namespace trellis {
+
+namespace {
+
+constexpr int kWideCols = 128, kWideThreads = 256, kColTiles = 2;  // column tiles a wave
+
+template <int NB>
+struct WideTiles {
+  alignas(16) char k[2][NB][8192], v[2][NB][8192];
+  alignas(16) uint16_t ks[2][NB][kTile], vs[2][NB][kTile];
+  int bad[2][8];  // subtiles without a page
+};
+template <int NB>
+union WideLds {
+  WideTiles<NB> t;
+  QueryLds<NB, kCols> q[4];           // before the tiles: one column tile a wave
+  float o[4][NB][kCols][kRowF];       // after them
+  int last;
+};
+
+// A thread's share of a tile on its way to shared memory: 32 lanes have a subtile, 16 bytes twice.
+template <int NB>
+struct Share {
+  v4i k[NB][2], v[NB][2];
+  uint32_t s;  // two tokens' scales: lanes 0..7 of a subtile key scales, 8..15 value scales (16..31: block 1)
+  int page;
+};
+
+__device__ __forceinline__ int share_entry(const AttnArgs &g, const Seq &q, int tile) {
+  const int tok = tile * kTile + 16 * (threadIdx.x >> 5);
+  int e = -0x7FFFFFFF - 1;
+  if (tok < q.len) e = ldg(g.a.b.table + (size_t)q.slot * g.a.b.max_pages + (tok >> g.page_shift));
+  return e;
+}
+
+template <int NB>
+__device__ __forceinline__ void load_share(const AttnArgs &g, int lo, const char *base, int tile, int entry, Share<NB> &x) {
+  const int T = g.a.c.page_size, i = threadIdx.x & 31;
+  const int tok = tile * kTile + 16 * (threadIdx.x >> 5), at = tok & (T - 1);
+  x.page = (uint32_t)entry < (uint32_t)g.a.c.n_pages ? entry : -1;
+  if (x.page < 0 && entry != -0x7FFFFFFF - 1 && (tok + 15 >= lo || tok < g.a.sinks))
+    kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
+  const char *chunk = base + (uint64_t)(uint32_t)max(x.page, 0) * g.page_stride;
+  const char *p = chunk + at * 64 + i * 16;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x.k[nb][h] = ldg(reinterpret_cast<const v4i *>(p + nb * T * 64 + h * 512));
+      x.v[nb][h] = ldg(reinterpret_cast<const v4i *>(p + (NB + nb) * T * 64 + h * 512));
+    }
+  x.s = 0;
+  const int nb = i >> 4, kind = (i >> 3) & 1;
+  if (nb < NB) x.s = ldg(reinterpret_cast<const uint32_t *>(chunk + 128 * NB * T + ((kind * NB + nb) * T + at + 2 * (i & 7)) * 2));
+}
+
+// The 16-byte parts of a tile in shared memory are permuted so that the products' reads spread over
+// the banks: key parts by their subtile (a product reads two tokens of each subtile), value parts by
+// bits 2 and 3 of their token, and a part's halves by the subtile's pair.
+__device__ __forceinline__ int key_swizzle(int subtile) { return (subtile & 3) | ((subtile & 4) << 1); }
+
+template <int NB>
+__device__ __forceinline__ void put_share(const AttnArgs &g, const Seq &q, int tile, const Share<NB> &x, WideTiles<NB> &lds, int buf) {
+  const int s = threadIdx.x >> 5, i = threadIdx.x & 31;
+  const bool swap = (s >> 1) & 1;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h * 32 + i;  // part c & 3 of token c >> 2
+      *reinterpret_cast<v4i *>(lds.k[buf][nb] + s * 1024 + (c ^ key_swizzle(s)) * 16) = x.k[nb][h];
+      const v4i v = x.v[nb][h];
+      *reinterpret_cast<v4i *>(lds.v[buf][nb] + s * 1024 + (c ^ ((c >> 4) & 3)) * 16) = swap ? v4i{v[2], v[3], v[0], v[1]} : v;
+    }
+  const int nb = i >> 4, kind = (i >> 3) & 1, at = 16 * s + 2 * (i & 7), tok = tile * kTile + at;
+  if (nb < NB) {
+    const bool here = x.page >= 0;
+    const uint32_t keep = ((here & (tok < q.len) & ((tok >= q.lo) | (tok < g.a.sinks))) ? 0xFFFFu : 0u) |
+                          ((here & (tok + 1 < q.len) & ((tok + 1 >= q.lo) | (tok + 1 < g.a.sinks))) ? 0xFFFF0000u : 0u);
+    uint16_t *to = kind ? lds.vs[buf][nb] : lds.ks[buf][nb];
+    *reinterpret_cast<uint32_t *>(to + at) = x.s & keep;
+    if (i == 0) lds.bad[buf][s] = !here;
+  }
+}
+
+// A lane's 32 keys' scales (32 g .. 32 g + 31), two a word.
+__device__ __forceinline__ void read_scales32(const uint16_t *s, uint32_t (&w)[16]) {
+  const u32x4 *p = reinterpret_cast<const u32x4 *>(s + ((threadIdx.x & 63) >> 4) * 32);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const u32x4 v = p[t];
+    w[4 * t] = v[0], w[4 * t + 1] = v[1], w[4 * t + 2] = v[2], w[4 * t + 3] = v[3];
+  }
+}
+// Key (j, i) of the products' results is key 16 (i >> 1) + 2 j + (i & 1) of the lane's.
+__device__ __forceinline__ float scale32(const uint32_t (&w)[16], int j, int i) {
+  const uint32_t x = w[8 * (i >> 1) + j];
+  return __builtin_bit_cast(float, (i & 1) ? x & 0xFFFF0000u : x << 16);
+}
+
+template <int NB>
+constexpr int wide_waves() { return NB == 1 ? 2 : 1; }  // a SIMD
+
+template <bool BF, int NB>
+__global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wide_kernel(AttnArgs g) {
+  constexpr int D = 128 * NB, CT = kColTiles;
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  WideLds<NB> &lds = *reinterpret_cast<WideLds<NB> *>(raw);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n_seq = g.a.b.n_seq, Hk = g.a.c.n_kv_heads;
+  if (blockIdx.x == 0 && g.tends) clear_rest<NB, kWideThreads>(g);
+  // ---- which columns: the last sequence's last ones first, as they see the most keys.  The head
+  // varies fastest: with eight of them each XCD's cache has one head's keys.
+  const int split = blockIdx.x % g.splits, head = blockIdx.x / g.splits % Hk;
+  int item = blockIdx.x / g.splits / Hk, s = -1;
+  Seq q{};
+  for (int s1 = n_seq; s1 > 0 && s < 0; s1 -= 64) {  // 64 sequences at a time, a lane a sequence
+    const int mine = s1 - 1 - lane;
+    Seq x{};
+    int tiles = 0;
+    if (mine >= 0) {
+      x = seq_of<kWideCols>(g, mine, blockIdx.x == 0 && wave == 0 && g.tends);
+      tiles = x.col_tiles;
+    }
+    int p = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int a = __shfl_up(p, d, 64);
+      if (lane >= d) p += a;
+    }
+    const uint64_t hit = __ballot(item < p);
+    if (hit && s < 0) {
+      const int l = __builtin_ctzll(hit);
+      s = s1 - 1 - l;
+      q = seq_from(x, l);
+      item -= __builtin_amdgcn_readlane(p, l) - q.col_tiles;
+    }
+    if (s < 0) item -= __builtin_amdgcn_readlane(p, 63);
+    if (blockIdx.x == 0 && g.tends && s >= 0 && s1 > 64)  // (the rest only to be checked)
+      for (int r = s1 - 64 - 1 - lane; wave == 0 && r >= 0; r -= 64) seq_of<kWideCols>(g, r, true);
+  }
+  if (s < 0) return;
+  const int col0 = (q.col_tiles - 1 - item) * kWideCols;
+  const int cols = (int)min((long long)kWideCols, (long long)q.n * g.group - col0);
+  const int p0 = q.len - q.n + col0 / g.group, p1 = q.len - q.n + (col0 + cols - 1) / g.group;  // positions
+  // the key tiles of these rows
+  q.lo = g.a.window ? max(p0 - g.a.window + 1, 0) : 0;
+  q.first = q.lo / kTile;
+  q.n_sink = min((min(g.a.sinks, q.len) + kTile - 1) / kTile, q.first);
+  q.tiles = max(q.n_sink + (min(max(p1 + 1, 0), q.len) + kTile - 1) / kTile - q.first, 0);
+  const int t0 = (int)((long long)q.tiles * split / g.splits), t1 = (int)((long long)q.tiles * (split + 1) / g.splits);
+  const char *base = kv4_chunk(g.a.c, g.a.layer, 0, head);
+  // ---- queries: four column tiles at a time, then each wave takes its own into registers
+  Share<NB> x;
+  int entry = 0, entry2 = 0;
+  if (t0 < t1) entry = share_entry(g, q, tile_at(q, t0));
+  if (t0 + 1 < t1) entry2 = share_entry(g, q, tile_at(q, t0 + 1));
+  v8i part[CT][NB][3];
+  Column<NB> col[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    QueryRaw<NB> r[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) r[w] = load_query<NB, kCols>(g, q, head, col0 + (w * CT + ct) * kCols);
+    if (ct == 0 && t0 < t1) load_share(g, q.lo, base, tile_at(q, t0), entry, x);
+    if (ct) __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) put_query<BF, NB, kCols>(g, r[w], lds.q[w]);
+    __syncthreads();
+    const int c = col0 + (wave * CT + ct) * kCols + (lane & 15);
+    col[ct].pos = c < col0 + cols ? q.len - q.n + c / g.group : -1;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      col[ct].cf[nb] = lds.q[wave].cf[nb][lane & 15];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) part[ct][nb][k] = read8(lds.q[wave].part[nb][k][lane & 15][lane >> 4]);
+    }
+  }
+  __syncthreads();
+  floatx4 o[CT][NB][8];
+  float m[CT], l[CT];
+  int e_run[NB];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    m[ct] = kNegInf;
+    l[ct] = 0.f;
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) e_run[nb] = 127;
+  if (t0 < t1) {
+    put_share(g, q, tile_at(q, t0), x, lds.t, 0);
+    if (t0 + 1 < t1) load_share(g, q.lo, base, tile_at(q, t0 + 1), entry2, x);
+  }
+  const int wp0 = q.len - q.n + min(col0 + wave * CT * kCols, col0 + cols - 1) / g.group;
+  const int wp1 = q.len - q.n + min(col0 + (wave + 1) * CT * kCols, col0 + cols) / g.group;  // (one more at most)
+  const bool idle = wave * CT * kCols >= cols;  // no column of this wave's
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1, tile = tile_at(q, t), k0 = tile * kTile;
+    if (t + 2 < t1) entry = share_entry(g, q, tile_at(q, t + 2));
+    __syncthreads();  // this tile is complete, and the one before it is read
+    if (!idle && k0 <= wp1) {
+      const uint32_t bad = (uint32_t)__ballot(lane < 8 && lds.t.bad[buf][lane & 7]);
+      const bool mask = !(k0 + kTile - 1 <= wp0 && bad == 0 &&
+                          (g.a.window == 0 || k0 > wp1 - g.a.window || k0 + kTile <= g.a.sinks));
+      // ---- the value scales' power of two: the tile's largest finite one comes below 2^8; it stays
+      // unless the tiles' scales outgrow it or fall far below
+      float f[NB], keep[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&lds.t.vs[buf][nb][2 * lane]);
+        const float a = fabsf(__builtin_bit_cast(float, w << 16)), b = fabsf(__builtin_bit_cast(float, w & 0xFFFF0000u));
+        float big = fmaxf(a <= 3.4028234e38f ? a : 0.f, b <= 3.4028234e38f ? b : 0.f);
+        big = fmaxf(big, lane_xor<1>(big));
+        big = fmaxf(big, lane_xor<2>(big));
+        big = fmaxf(big, lane_xor<4>(big));
+        big = fmaxf(big, lane_xor<8>(big));
+        big = max4(big);
+        const int e = __builtin_amdgcn_readfirstlane(max((int)(__builtin_bit_cast(uint32_t, big) >> 23), 32));
+        keep[nb] = 1.f;
+        if (e > e_run[nb] || e < e_run[nb] - 8) {
+          const int to = min(e + 2, 254), by = min(max(e_run[nb] - to, -126), 127);
+          keep[nb] = __builtin_bit_cast(float, (uint32_t)(127 + by) << 23);
+          e_run[nb] = to;
+        }
+        f[nb] = __builtin_bit_cast(float, (uint32_t)(261 - e_run[nb]) << 23);
+      }
+      half8 w[CT][NB][4];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        // ---- scores
+        float y[8][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t ks[16];
+          read_scales32(lds.t.ks[buf][nb], ks);
+          const int row = lane & 15, sub = row >> 1;
+          const char *kp = lds.t.k[buf][nb] + sub * 1024;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = (8 * (j & 1) + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
+            const v4i kv = *reinterpret_cast<const v4i *>(kp + (j >> 1) * 256 + c * 16);
+            const v8i a = {kv[0], kv[1], kv[2], kv[3], 0, 0, 0, 0};
+            floatx4 z = {0.f, 0.f, 0.f, 0.f};
+            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
+            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
+            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float u = z[i] * scale32(ks, j, i);
+              if (NB == 1) y[j][i] = u;
+              else y[j][i] = nb ? fmaf(u, col[ct].cf[nb], y[j][i]) : u * col[ct].cf[nb];
+            }
+          }
+        }
+        // ---- softmax
+        uint32_t hidden = 0;
+        if (mask) {
+          const int kk = k0 + 32 * (lane >> 4), rel = col[ct].pos - kk;
+          const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
+          const uint32_t gone = bad >> (2 * (lane >> 4));
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 16 * (i >> 1) + 2 * j + (i & 1);
+              const bool ok = (k <= rel) & ((k > after) | (k < sink)) & !((gone >> (i >> 1)) & 1);
+              y[j][i] = ok ? y[j][i] : kNegInf;
+              hidden |= ok ? 0u : 1u << (4 * j + i);
+            }
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
+        top = max4(top);
+        const float cf = NB == 1 ? col[ct].cf[0] : 1.f;
+        const float m2 = fmaxf(m[ct], top == kNegInf ? kNegInf : top * cf);
+        const float mu = m2 == kNegInf ? 0.f : m2;
+        const float alpha = __builtin_amdgcn_exp2f(m[ct] - mu);
+        m[ct] = m2;
+        float add = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // (a hidden score is minus infinity, and cf may be zero)
+            const float d = mask && ((hidden >> (4 * j + i)) & 1) ? kNegInf : fmaf(y[j][i], cf, -mu);
+            y[j][i] = __builtin_amdgcn_exp2f(d);
+            add += y[j][i];
+          }
+        l[ct] = fmaf(l[ct], alpha, add);
+        // ---- weights
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t vs[16];
+          read_scales32(lds.t.vs[buf][nb], vs);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float u = y[j][i] * (scale32(vs, j, i) * f[nb]);
+              if (mask) u = (hidden >> (4 * j + i)) & 1 ? 0.f : u;  // (its scale may be NaN)
+              // key 16 (i >> 1) + 2 j + (i & 1): step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
+              w[ct][nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
+            }
+          const float r = alpha * keep[nb];
+          if (__any(r != 1.f))
+#pragma unroll
+            for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] *= r;
+        }
+      }
+      // ---- values
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int row = lane & 15, sub = 2 * (lane >> 4);
+        const char *vp = lds.t.v[buf][nb] + sub * 1024 + row * 64;
+        typedef __attribute__((address_space(3))) v2i lds_v2i;
+#pragma unroll
+        for (int dt = 0; dt < 8; ++dt) {
+          const char *at = vp + (((dt >> 1) ^ (row >> 2)) * 16) + (((dt & 1) ^ ((lane >> 4) & 1)) * 8);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const v2i codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + h * 1024));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t c = codes[k];
+              const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
+              const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
+              const half8 a = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct)
+                o[ct][nb][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[ct][nb][2 * h + k], o[ct][nb][dt], 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+    if (t + 1 < t1) put_share(g, q, tile_at(q, t + 1), x, lds.t, buf ^ 1);
+    if (t + 2 < t1) load_share(g, q.lo, base, tile_at(q, t + 2), entry, x);
+  }
+  // ---- results: back to the values' units, through shared memory, 16 lanes a column
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    l[ct] = sum4(l[ct]);
+    __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float f = __builtin_bit_cast(float, (uint32_t)max(e_run[nb] - 7, 1) << 23);
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt)
+        *reinterpret_cast<floatx4 *>(&lds.o[wave][nb][lane & 15][16 * dt + 4 * (lane >> 4)]) = o[ct][nb][dt] * f;
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int i = lane & 15;
+    for (int p = 0; p < 4; ++p) {
+      const int c = 4 * p + (lane >> 4), at = (wave * CT + ct) * kCols + c;
+      const float mm = __shfl(m[ct], c, 64), ll = __shfl(l[ct], c, 64);
+      if (at >= cols) continue;  // (16 lanes together)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const floatx4 a = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i]);
+        const floatx4 b = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i + 4]);
+        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        if (g.splits == 1) {
+          write_block<BF>(g, q, head, col0 + at, nb, v, mm, ll);
+        } else {
+          const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)(blockIdx.x / g.splits) * g.splits * kWideCols * (D + 8),
+                                                        (long long)g.splits * kWideCols * (D + 8) * 4);
+          const int to = ((split * kWideCols + at) * (D + 8)) * 4;
+          const u32x4 x0 = {__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]), __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
+          const u32x4 x1 = {__builtin_bit_cast(uint32_t, v[4]), __builtin_bit_cast(uint32_t, v[5]), __builtin_bit_cast(uint32_t, v[6]), __builtin_bit_cast(uint32_t, v[7])};
+          __builtin_amdgcn_raw_buffer_store_b128(x0, rs, to + (nb * 128 + 8 * i) * 4, 0, kSC1);
+          __builtin_amdgcn_raw_buffer_store_b128(x1, rs, to + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
+          if (nb == 0 && i == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, mm), __builtin_bit_cast(uint32_t, ll)}, rs, to + D * 4, 0, kSC1);
+        }
+      }
+    }
+  }
+  if (g.splits == 1) return;
+  // ---- the join, by the last of the segment's workgroups
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): every thread's stores have completed
+  __syncthreads();
+  const int seg = blockIdx.x / g.splits;
+  if (tid == 0) {
+    const uint32_t old = __hip_atomic_fetch_add(g.counters + seg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    lds.last = old == (uint32_t)(g.splits - 1);
+    if (lds.last) __hip_atomic_store(g.counters + seg, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!__builtin_amdgcn_readfirstlane(lds.last)) return;
+  const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)seg * g.splits * kWideCols * (D + 8), (long long)g.splits * kWideCols * (D + 8) * 4);
+  const int i = tid & 15;
+  for (int c = tid >> 4; c < cols; c += kWideThreads / 16) {
+    float mm = kNegInf, ll = 0.f, acc[NB][8];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[nb][e] = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < g.splits; ++w) {
+      const int at = ((w * kWideCols + c) * (D + 8)) * 4;
+      const u32x2 ml = __builtin_amdgcn_raw_buffer_load_b64(rs, at + D * 4, 0, kSC1);
+      const uint32_t mw = ml[0], lw = ml[1];
+      const float pm = __builtin_bit_cast(float, mw), pl = __builtin_bit_cast(float, lw);
+      const float m2 = fmaxf(mm, pm), u2 = m2 == kNegInf ? 0.f : m2;
+      const float fa = __builtin_amdgcn_exp2f(mm - u2), fb = __builtin_amdgcn_exp2f(pm - u2);
+      mm = m2;
+      ll = ll * fa + pl * fb;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const u32x4 p0 = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i) * 4, 0, kSC1);
+        const u32x4 p1 = __builtin_amdgcn_raw_buffer_load_b128(rs, at + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          acc[nb][e] = acc[nb][e] * fa + __builtin_bit_cast(float, (uint32_t)(e < 4 ? p0[e & 3] : p1[e & 3])) * fb;
+      }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + c, nb, acc[nb], mm, ll);
+  }
+}
+
+// Segments (column tiles of 128 times heads), at most.
+long long wide_segments(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
+  return (((long long)b.rows * (n_q_heads / c.n_kv_heads) + kWideCols - 1) / kWideCols + b.n_seq) * c.n_kv_heads;
+}
+
+// Workgroups that share a segment's keys: where there are too few segments to fill the card, as
+// many as do, but none with less than eight tiles of the longest context that the tables hold.
+int wide_splits(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
+  const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? 2 : 1);
+  const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
+  long long n = room / segs;
+  if (n > tiles / 8) n = tiles / 8;
+  return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+}
+
+template <bool BF, int NB>
+hipError_t launch(const AttnArgs &g, unsigned grid, hipStream_t stream) {
+  const size_t lds = sizeof(WideLds<NB>);
+  const auto kernel = kv4_attn_wide_kernel<BF, NB>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  kernel<<<grid, kWideThreads, lds, stream>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t kv4_attn_wide_parts(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
+  const int n = wide_splits(c, b, n_q_heads);
+  return n == 1 ? 0 : (size_t)wide_segments(c, b, n_q_heads) * n * kWideCols * (c.head_dim + 8) * 4;
+}
+
+hipError_t launch_kv4_attn_wide(const AttnArgs &args, hipStream_t stream) {
+  AttnArgs g = args;
+  g.splits = wide_splits(g.a.c, g.a.b, g.a.n_q_heads);
+  const unsigned grid = (unsigned)(wide_segments(g.a.c, g.a.b, g.a.n_q_heads) * g.splits);
+  const bool bf = g.a.dtype == TRELLIS_KV4_BF16;
+  if (g.a.c.head_dim == 128) return bf ? launch<true, 1>(g, grid, stream) : launch<false, 1>(g, grid, stream);
+  return bf ? launch<true, 2>(g, grid, stream) : launch<false, 2>(g, grid, stream);
+}
+
+}  // namespace trellis

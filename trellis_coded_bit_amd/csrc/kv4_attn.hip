@@ -82,11 +82,12 @@ __device__ __forceinline__ void load_tile(const AttnArgs &g, int seen_from, cons
 
 // Moves a tile's values and scales to the wave's shared memory.  Keys that no row sees get
 // scale zero.  The value scales are multiplied by a power of two that brings the tile's largest
-// to [128, 256); returns its inverse as a matrix instruction's scale byte, per block.
+// to [128, 256); vbyte is its inverse as a matrix instruction's scale byte, per block.  Returns
+// whether one of them is not finite.
 // A token's four 16-byte parts are permuted by bits 2 and 3 of its number, which spreads the
 // transposed reads below over the banks.
 template <int NB, int R>
-__device__ __forceinline__ void stage_tile(const AttnArgs &g, const Seq &q, int tile, const Tile<NB> &x, WaveLds<NB, R> &lds,
+__device__ __forceinline__ bool stage_tile(const AttnArgs &g, const Seq &q, int tile, const Tile<NB> &x, WaveLds<NB, R> &lds,
                                            int (&vbyte)[NB]) {
   const int lane = opaque_tid() & 63;
   char *const to = lds.v + subtile_of(lane) * 1024 + (lane & 1) * 64;
@@ -99,6 +100,7 @@ __device__ __forceinline__ void stage_tile(const AttnArgs &g, const Seq &q, int 
   const bool here = x.page >= 0;
   const uint32_t keep = ((here & (tok < q.len) & ((tok >= q.lo) | (tok < g.a.sinks))) ? 0xFFFFu : 0u) |
                         ((here & (tok + 1 < q.len) & ((tok + 1 >= q.lo) | (tok + 1 < g.a.sinks))) ? 0xFFFF0000u : 0u);
+  bool odd = false;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     *reinterpret_cast<uint32_t *>(&lds.ks[nb][at]) = x.ks[nb] & keep;
@@ -111,12 +113,14 @@ __device__ __forceinline__ void stage_tile(const AttnArgs &g, const Seq &q, int 
     top = fmaxf(top, lane_xor<4>(top));
     top = fmaxf(top, lane_xor<8>(top));
     top = max4(top);
+    odd |= __any((w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u);
     const int e = __builtin_amdgcn_readfirstlane(max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 32));
     const float f = __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);
     const uint32_t fa = __builtin_bit_cast(uint32_t, a * f), fb = __builtin_bit_cast(uint32_t, b * f);
     *reinterpret_cast<uint32_t *>(&lds.vs[nb][at]) = (fa >> 16) | (fb & 0xFFFF0000u);
     vbyte[nb] = e - 7;
   }
+  return odd;
 }
 
 // A lane's own keys.  With R = 16 / C columns held R times over (few columns: the matrix
@@ -232,25 +236,24 @@ __device__ __forceinline__ void split3(const float (&w)[4], int &p0, int &p1, in
   p2 = __builtin_bit_cast(int, z);
 }
 
-// One tile into a column tile's sums.  MASK: some row does not see some key of the tile; bad: bit
-// 2 s of a subtile s without a page.
-template <int NB, int R, bool MASK>
-__device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t bad, const int (&vbyte)[NB],
+// One tile into a column tile's sums.  mask: some row does not see some key of the tile; bad: bit
+// 2 s of a subtile s without a page; odd: some value scale is not finite.
+template <int NB, int R>
+__device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask, uint32_t bad, bool odd, const int (&vbyte)[NB],
                                          float (&x)[8 / R][4], const Column<NB> &col, WaveLds<NB, R> &lds, Sums<NB> &sum) {
   constexpr int NT = 8 / R, C = kCols / R, H = 4 / R;
   const int lane = opaque_tid() & 63, r = (lane & 15) / C, k = lane >> 4;
-  uint32_t seen = 0;
-  if (MASK) {
+  if (mask) {
+    asm volatile("");  // (a branch, not selects on every tile)
     const int k0 = tile * kTile + own_key<R>(lane, 0), rel = col.pos - k0;
     const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - k0 : 0;
+    const uint32_t gone = bad >> (4 * k);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = 16 * (t / H) + 4 * (t % H) + i;  // from k0
-        const bool ok = (j <= rel) & ((j > after) | (j < sink)) & !((bad >> (4 * k + 2 * (t / H))) & 1);
-        x[t][i] = ok ? x[t][i] : kNegInf;
-        seen |= ok ? 1u << (4 * t + i) : 0u;
+        x[t][i] = ((j <= rel) & ((j > after) | (j < sink)) & !((gone >> (2 * (t / H))) & 1)) ? x[t][i] : kNegInf;
       }
   }
   float top = kNegInf;
@@ -260,7 +263,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t b
   if (R >= 2) top = fmaxf(top, lane_xor<8>(top));
   top = max4(top);
   const float cf = NB == 1 ? col.cf[0] : 1.f;
-  const float m = fmaxf(sum.m, top == kNegInf ? kNegInf : top * cf);
+  const float m = fmaxf(sum.m, top * cf);
   const float mu = m == kNegInf ? 0.f : m;  // nothing seen so far
   const float alpha = __builtin_amdgcn_exp2f(sum.m - mu);
   sum.m = m;
@@ -269,9 +272,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t b
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // (cf may be zero, and a score that is not seen minus infinity)
-      const float d = MASK && !((seen >> (4 * t + i)) & 1) ? kNegInf : fmaf(x[t][i], cf, -mu);
-      x[t][i] = __builtin_amdgcn_exp2f(d);
+      x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], cf, -mu));
       add += x[t][i];
     }
   sum.l = fmaf(sum.l, alpha, add);
@@ -279,6 +280,14 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t b
   for (int nb = 0; nb < NB; ++nb) {
     uint32_t vs[16 / R];
     read_scales<R>(lds.vs[nb], vs);
+    if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
+      asm volatile("");
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (x[t][i] == 0.f) vs[2 * t + (i >> 1)] &= (i & 1) ? 0xFFFFu : 0xFFFF0000u;
+    }
     int part[3][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -286,7 +295,6 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, uint32_t b
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w[i] = x[t][i] * scale_of(vs, t, i);
-        if (MASK && !((seen >> (4 * t + i)) & 1)) w[i] = 0.f;  // (its scale may be NaN)
       }
       split3(w, part[0][t], part[1][t], part[2][t]);
     }
@@ -496,7 +504,9 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   // ---- segment by segment; the next one's query, pages and first tile are on their way while this
   // one is worked on
   WaveLds<NB, R> &mine = lds.wave[wave];
-  if (R > 1 && lane < 8) mine.w[4 * C * 3][lane] = 0;
+  if constexpr (R > 1) {
+    if (lane < 8) mine.w[4 * C * 3][lane] = 0;
+  }
   Tile<NB> x;
   QueryRaw<NB> query = load_query<NB, C>(g, c.q, c.head, c.col0);
   const char *base = kv4_chunk(g.a.c, g.a.layer, 0, c.head);
@@ -560,11 +570,12 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       const bool work = t < t1 && q.len > 0, last = t + kWaves >= t1;
       const int tile = tile_at(q, t), k0 = tile * kTile;
       uint32_t bad = 0;
+      bool odd = false;
       int vbyte[NB];
       float sc[8 / R][4];
       if (work) {
         bad = (uint32_t)__ballot(x.page < 0) & 0x5555u;  // (lanes 2 s have subtile s)
-        stage_tile(g, q, tile, x, mine, vbyte);
+        odd = stage_tile(g, q, tile, x, mine, vbyte);
         scores<NB, R>(x.k, lds.q, column, mine, sc);
       }
       __builtin_amdgcn_sched_barrier(0);  // (the next tile's loads reuse the registers of this one)
@@ -577,8 +588,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       if (work) {
         const bool all = k0 + kTile - 1 <= pos0 && bad == 0 &&
                          (g.a.window == 0 || k0 > pos1 - g.a.window || k0 + kTile <= g.a.sinks);
-        if (all) add_tile<NB, R, false>(g, tile, bad, vbyte, sc, column, mine, sum);
-        else add_tile<NB, R, true>(g, tile, bad, vbyte, sc, column, mine, sum);
+        add_tile<NB, R>(g, tile, !all, bad, odd, vbyte, sc, column, mine, sum);
       }
       if (last) break;
     }

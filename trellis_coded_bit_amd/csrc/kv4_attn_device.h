@@ -116,7 +116,7 @@ __device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
 template <int NB, int C>
 struct QueryLds {
   alignas(16) int part[NB][3][C][4][8];
-  float cf[NB][C];  // score = cf * (sum over parts), in powers of two; >= 0
+  float cf[NB][C];  // score = cf * (sum over parts), in powers of two; > 0, so a hidden score stays minus infinity
 };
 
 // Sixteen lanes to a column, eight elements each.
@@ -165,7 +165,7 @@ __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> 
     float f = __builtin_bit_cast(float, (uint32_t)min(261 - e, 254) << 23);
     if (top > 3.4028234e38f) f = __builtin_nanf("");
     if (g.a.scale < 0.f) f = -f;
-    if (i == 0) lds.cf[nb][c] = __builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128);
+    if (i == 0) lds.cf[nb][c] = fmaxf(__builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128), 1e-37f);
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
 #pragma unroll

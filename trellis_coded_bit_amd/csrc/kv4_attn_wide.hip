@@ -18,12 +18,12 @@ namespace trellis {
 
 namespace {
 
-constexpr int kWideCols = 128, kWideThreads = 256, kColTiles = 2;  // column tiles a wave
+constexpr int kColTiles = 1, kWideCols = 64 * kColTiles, kWideThreads = 256;  // column tiles a wave
 
 template <int NB>
 struct WideTiles {
   alignas(16) char k[2][NB][8192], v[2][NB][8192];
-  alignas(16) uint16_t ks[2][NB][kTile], vs[2][NB][kTile];
+  alignas(16) float ks[2][NB][kTile], vs[2][NB][kTile];
   int bad[2][8];  // subtiles without a page
 };
 template <int NB>
@@ -93,29 +93,170 @@ __device__ __forceinline__ void put_share(const AttnArgs &g, const Seq &q, int t
     const bool here = x.page >= 0;
     const uint32_t keep = ((here & (tok < q.len) & ((tok >= q.lo) | (tok < g.a.sinks))) ? 0xFFFFu : 0u) |
                           ((here & (tok + 1 < q.len) & ((tok + 1 >= q.lo) | (tok + 1 < g.a.sinks))) ? 0xFFFF0000u : 0u);
-    uint16_t *to = kind ? lds.vs[buf][nb] : lds.ks[buf][nb];
-    *reinterpret_cast<uint32_t *>(to + at) = x.s & keep;
+    const uint32_t w = x.s & keep;
+    float *to = kind ? lds.vs[buf][nb] : lds.ks[buf][nb];
+    *reinterpret_cast<floatx2 *>(to + at) = floatx2{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
     if (i == 0) lds.bad[buf][s] = !here;
   }
 }
 
-// A lane's 32 keys' scales (32 g .. 32 g + 31), two a word.
-__device__ __forceinline__ void read_scales32(const uint16_t *s, uint32_t (&w)[16]) {
-  const u32x4 *p = reinterpret_cast<const u32x4 *>(s + ((threadIdx.x & 63) >> 4) * 32);
+// A lane's 32 keys' scales (32 g .. 32 g + 31).
+__device__ __forceinline__ void read_scales32(const float *s, float (&w)[32]) {
+  const floatx4 *p = reinterpret_cast<const floatx4 *>(s + ((threadIdx.x & 63) >> 4) * 32);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const u32x4 v = p[t];
-    w[4 * t] = v[0], w[4 * t + 1] = v[1], w[4 * t + 2] = v[2], w[4 * t + 3] = v[3];
+  for (int t = 0; t < 8; ++t) {
+    const floatx4 v = p[t];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[4 * t + e] = v[e];
   }
 }
 // Key (j, i) of the products' results is key 16 (i >> 1) + 2 j + (i & 1) of the lane's.
-__device__ __forceinline__ float scale32(const uint32_t (&w)[16], int j, int i) {
-  const uint32_t x = w[8 * (i >> 1) + j];
-  return __builtin_bit_cast(float, (i & 1) ? x & 0xFFFF0000u : x << 16);
+__device__ __forceinline__ constexpr int key32(int j, int i) { return 16 * (i >> 1) + 2 * j + (i & 1); }
+
+// One tile into a wave's sums.  mask: some row does not see some key; bad: subtiles without a page;
+// odd: some value scale is not finite.
+template <int NB>
+__device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB> &lds, int buf, int k0, bool mask, uint32_t bad, bool odd,
+                                          const v8i (&part)[kColTiles][NB][3], const Column<NB> (&col)[kColTiles],
+                                          const float (&f)[NB], const float (&keep)[NB], const int (&e_run)[NB], float (&m)[kColTiles],
+                                          float (&l)[kColTiles], floatx4 (&o)[kColTiles][NB][8]) {
+  constexpr int CT = kColTiles;
+  const int lane = opaque_tid() & 63;
+        half8 w[CT][NB][4];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          // ---- scores
+          float y[8][4];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float ks[32];
+            read_scales32(lds.ks[buf][nb], ks);
+            const int row = lane & 15, sub = row >> 1;
+            const char *kp = lds.k[buf][nb] + sub * 1024;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int c = (8 * (j & 1) + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
+              const v4i kv = *reinterpret_cast<const v4i *>(kp + (j >> 1) * 256 + c * 16);
+              const v8i a = {kv[0], kv[1], kv[2], kv[3], 0, 0, 0, 0};
+              floatx4 z = {0.f, 0.f, 0.f, 0.f};
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float u = z[i] * ks[key32(j, i)];
+                if (NB == 1) y[j][i] = u;
+                else y[j][i] = nb ? fmaf(u, col[ct].cf[nb], y[j][i]) : u * col[ct].cf[nb];
+              }
+            }
+          }
+          // ---- softmax
+          if (mask) {
+      asm volatile("");  // (a branch, not 32 selects on every tile)
+      const int kk = k0 + 32 * (lane >> 4), rel = col[ct].pos - kk;
+      const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
+      const uint32_t gone = bad >> (2 * (lane >> 4));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 16 * (i >> 1) + 2 * j + (i & 1);
+          y[j][i] = ((k <= rel) & ((k > after) | (k < sink)) & !((gone >> (i >> 1)) & 1)) ? y[j][i] : kNegInf;
+        }
+    }
+    // The running maximum stays until a lane's weights outgrow 2^7 together: most tiles then need
+    // neither a maximum nor a rescaling.  (A column that has seen nothing has m = -inf and comes here
+    // with infinite or NaN weights.)  The power of two f[0] is taken into the exponent.
+    const float cf = NB == 1 ? col[ct].cf[0] : 1.f;
+    const float log2f = (float)(134 - e_run[0]);
+    float x[8][4], add = 0.f, alpha = 1.f;
+    {
+      const float c0 = log2f - m[ct];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[j][i] = __builtin_amdgcn_exp2f(fmaf(y[j][i], cf, c0));
+          add += x[j][i];
+        }
+    }
+    if (__any(!(add <= 128.f * f[0]))) {
+      float top = kNegInf;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
+      top = max4(top);
+      const float m2 = fmaxf(m[ct], top * cf);
+      const float mu = m2 == kNegInf ? 0.f : m2;  // nothing seen so far
+      alpha = __builtin_amdgcn_exp2f(m[ct] - mu);
+      m[ct] = m2;
+      add = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[j][i] = __builtin_amdgcn_exp2f(fmaf(y[j][i], cf, log2f - mu));
+          add += x[j][i];
+        }
+    }
+    l[ct] = fmaf(l[ct], alpha, add * __builtin_amdgcn_exp2f(-log2f));
+    // ---- weights
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float vs[32];
+      read_scales32(lds.vs[buf][nb], vs);
+      if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
+        asm volatile("");
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs[key32(j, i)] = x[j][i] == 0.f ? 0.f : vs[key32(j, i)];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u = x[j][i] * vs[key32(j, i)];
+          if (nb) u *= f[nb] * __builtin_amdgcn_exp2f(-log2f);
+          // step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
+          w[ct][nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
+        }
+        const float r = alpha * keep[nb];
+            if (__any(r != 1.f))
+#pragma unroll
+              for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] *= r;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // (keeps the phases' registers apart)
+  // ---- values
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = lane & 15, sub = 2 * (lane >> 4);
+          const char *vp = lds.v[buf][nb] + sub * 1024 + row * 64;
+          typedef __attribute__((address_space(3))) v2i lds_v2i;
+#pragma unroll
+          for (int dt = 0; dt < 8; ++dt) {
+            const char *at = vp + (((dt >> 1) ^ (row >> 2)) * 16) + (((dt & 1) ^ ((lane >> 4) & 1)) * 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v2i codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + h * 1024));
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t c = codes[k];
+                const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
+                const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
+                const half8 a = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                  o[ct][nb][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[ct][nb][2 * h + k], o[ct][nb][dt], 0, 0, 0);
+              }
+            }
+          }
+        }
 }
 
 template <int NB>
-constexpr int wide_waves() { return NB == 1 ? 2 : 1; }  // a SIMD
+constexpr int wide_waves() { return NB == 1 ? 3 : 1; }  // a SIMD
 
 template <bool BF, int NB>
 __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wide_kernel(AttnArgs g) {
@@ -202,7 +343,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    m[ct] = kNegInf;
+    m[ct] = col[ct].pos < 0 ? 0.f : kNegInf;  // (a column past the last never sees a score)
     l[ct] = 0.f;
   }
 #pragma unroll
@@ -225,11 +366,14 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
       // ---- the value scales' power of two: the tile's largest finite one comes below 2^8; it stays
       // unless the tiles' scales outgrow it or fall far below
       float f[NB], keep[NB];
+      bool odd = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(&lds.t.vs[buf][nb][2 * lane]);
-        const float a = fabsf(__builtin_bit_cast(float, w << 16)), b = fabsf(__builtin_bit_cast(float, w & 0xFFFF0000u));
-        float big = fmaxf(a <= 3.4028234e38f ? a : 0.f, b <= 3.4028234e38f ? b : 0.f);
+        const floatx2 w = *reinterpret_cast<const floatx2 *>(&lds.t.vs[buf][nb][2 * lane]);
+        const float a = fabsf(w[0]), b = fabsf(w[1]);
+        const bool fa = a <= 3.4028234e38f, fb = b <= 3.4028234e38f;
+        odd |= __any(!(fa & fb));
+        float big = fmaxf(fa ? a : 0.f, fb ? b : 0.f);
         big = fmaxf(big, lane_xor<1>(big));
         big = fmaxf(big, lane_xor<2>(big));
         big = fmaxf(big, lane_xor<4>(big));
@@ -244,115 +388,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
         }
         f[nb] = __builtin_bit_cast(float, (uint32_t)(261 - e_run[nb]) << 23);
       }
-      half8 w[CT][NB][4];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        // ---- scores
-        float y[8][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          uint32_t ks[16];
-          read_scales32(lds.t.ks[buf][nb], ks);
-          const int row = lane & 15, sub = row >> 1;
-          const char *kp = lds.t.k[buf][nb] + sub * 1024;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = (8 * (j & 1) + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
-            const v4i kv = *reinterpret_cast<const v4i *>(kp + (j >> 1) * 256 + c * 16);
-            const v8i a = {kv[0], kv[1], kv[2], kv[3], 0, 0, 0, 0};
-            floatx4 z = {0.f, 0.f, 0.f, 0.f};
-            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
-            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
-            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float u = z[i] * scale32(ks, j, i);
-              if (NB == 1) y[j][i] = u;
-              else y[j][i] = nb ? fmaf(u, col[ct].cf[nb], y[j][i]) : u * col[ct].cf[nb];
-            }
-          }
-        }
-        // ---- softmax
-        uint32_t hidden = 0;
-        if (mask) {
-          const int kk = k0 + 32 * (lane >> 4), rel = col[ct].pos - kk;
-          const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
-          const uint32_t gone = bad >> (2 * (lane >> 4));
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 16 * (i >> 1) + 2 * j + (i & 1);
-              const bool ok = (k <= rel) & ((k > after) | (k < sink)) & !((gone >> (i >> 1)) & 1);
-              y[j][i] = ok ? y[j][i] : kNegInf;
-              hidden |= ok ? 0u : 1u << (4 * j + i);
-            }
-        }
-        float top = kNegInf;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
-        top = max4(top);
-        const float cf = NB == 1 ? col[ct].cf[0] : 1.f;
-        const float m2 = fmaxf(m[ct], top == kNegInf ? kNegInf : top * cf);
-        const float mu = m2 == kNegInf ? 0.f : m2;
-        const float alpha = __builtin_amdgcn_exp2f(m[ct] - mu);
-        m[ct] = m2;
-        float add = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // (a hidden score is minus infinity, and cf may be zero)
-            const float d = mask && ((hidden >> (4 * j + i)) & 1) ? kNegInf : fmaf(y[j][i], cf, -mu);
-            y[j][i] = __builtin_amdgcn_exp2f(d);
-            add += y[j][i];
-          }
-        l[ct] = fmaf(l[ct], alpha, add);
-        // ---- weights
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          uint32_t vs[16];
-          read_scales32(lds.t.vs[buf][nb], vs);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float u = y[j][i] * (scale32(vs, j, i) * f[nb]);
-              if (mask) u = (hidden >> (4 * j + i)) & 1 ? 0.f : u;  // (its scale may be NaN)
-              // key 16 (i >> 1) + 2 j + (i & 1): step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
-              w[ct][nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
-            }
-          const float r = alpha * keep[nb];
-          if (__any(r != 1.f))
-#pragma unroll
-            for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] *= r;
-        }
-      }
-      // ---- values
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int row = lane & 15, sub = 2 * (lane >> 4);
-        const char *vp = lds.t.v[buf][nb] + sub * 1024 + row * 64;
-        typedef __attribute__((address_space(3))) v2i lds_v2i;
-#pragma unroll
-        for (int dt = 0; dt < 8; ++dt) {
-          const char *at = vp + (((dt >> 1) ^ (row >> 2)) * 16) + (((dt & 1) ^ ((lane >> 4) & 1)) * 8);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v2i codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + h * 1024));
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t c = codes[k];
-              const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
-              const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
-              const half8 a = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct)
-                o[ct][nb][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[ct][nb][2 * h + k], o[ct][nb][dt], 0, 0, 0);
-            }
-          }
-        }
-      }
+      wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, part, col, f, keep, e_run, m, l, o);
     }
     if (t + 1 < t1) put_share(g, q, tile_at(q, t + 1), x, lds.t, buf ^ 1);
     if (t + 2 < t1) load_share(g, q.lo, base, tile_at(q, t + 2), entry, x);
@@ -448,7 +484,7 @@ long long wide_segments(const trellis_kv4_cache &c, const trellis_kv4_batch &b, 
 // Workgroups that share a segment's keys: where there are too few segments to fill the card, as
 // many as do, but none with less than eight tiles of the longest context that the tables hold.
 int wide_splits(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
-  const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? 2 : 1);
+  const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? wide_waves<1>() : wide_waves<2>());
   const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
   long long n = room / segs;
   if (n > tiles / 8) n = tiles / 8;

@@ -8,6 +8,7 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -151,7 +152,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current stream of the current device (without building a torch.cuda.Stream: that
+    costs several microseconds a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _req(t: torch.Tensor, dtype: torch.dtype, name: str, device=None) -> None:
@@ -601,6 +604,7 @@ class CKV4Batch(ctypes.Structure):
 _KV4_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
 
 
+@functools.lru_cache(maxsize=None)
 def trellis_kv4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of one layer."""
     nb = lib().trellis_kv4_page_bytes(page_size, n_kv_heads, head_dim)
@@ -608,6 +612,11 @@ def trellis_kv4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> in
         raise ValueError(f"page_size={page_size} n_kv_heads={n_kv_heads} head_dim={head_dim}: pages of 16, 32, 64, 128 "
                          "or 256 tokens, 1..1024 heads of 128 or 256 expected")
     return nb
+
+
+@functools.lru_cache(maxsize=None)
+def _kv4_ws_bytes() -> int:
+    return lib().trellis_kv4_workspace_bytes()
 
 
 class KV4Cache:
@@ -633,9 +642,23 @@ class KV4Cache:
         return cls(torch.zeros((n_layers, n_pages, nb), dtype=torch.uint8, device=device), page_size, n_kv_heads, head_dim)
 
 
+def _kv4_int(t: torch.Tensor, name: str, device) -> None:
+    """_req for the int32 tensors of a call, the usual case first."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.is_contiguous()):
+        _req(t, torch.int32, name, device)
+
+
+def _kv4_ws(ws: Optional[torch.Tensor], nb: int, device, stream: int) -> torch.Tensor:
+    """_ws_arg with the stream at hand."""
+    if ws is None:
+        w = _ws.get((device.index, stream))
+        return w if w is not None and w.numel() >= nb else workspace(nb, device)
+    return _ws_arg(ws, nb, device)
+
+
 def _kv4_state(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor) -> None:
-    _req(table, torch.int32, "table", cache.device)
-    _req(lens, torch.int32, "lens", cache.device)
+    _kv4_int(table, "table", cache.device)
+    _kv4_int(lens, "lens", cache.device)
     if table.dim() != 2 or lens.numel() != table.shape[0]:
         raise ValueError(f"table must be [slots, max_pages] with one length per slot, got {tuple(table.shape)} and "
                          f"{lens.numel()} lengths")
@@ -644,10 +667,10 @@ def _kv4_state(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor) -> None
 def _kv4_batch(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
                slots: Optional[torch.Tensor], rows: int) -> CKV4Batch:
     _kv4_state(cache, table, lens)
-    _req(cu, torch.int32, "cu", cache.device)
+    _kv4_int(cu, "cu", cache.device)
     n_seq = cu.numel() - 1
     if slots is not None:
-        _req(slots, torch.int32, "slots", cache.device)
+        _kv4_int(slots, "slots", cache.device)
         if slots.numel() != n_seq:
             raise ValueError(f"slots must have one entry per sequence ({n_seq}), got {slots.numel()}")
     elif n_seq > lens.numel():
@@ -686,9 +709,10 @@ def trellis_kv4_append(cache: KV4Cache, layer: int, table: torch.Tensor, lens: t
     if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have the same type and number of rows")
     b = _kv4_batch(cache, table, lens, cu, slots, k.shape[0])
-    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, _kv4_ws_bytes(), cache.device, stream)
     _check(lib().trellis_kv4_append(cache._ref, layer, ctypes.byref(b), _KV4_DTYPE[k.dtype], k.data_ptr(), k_row, k_head,
-                                    v.data_ptr(), v_row, v_head, ws.data_ptr(), ws.numel(), _stream()))
+                                    v.data_ptr(), v_row, v_head, ws.data_ptr(), ws.numel(), stream))
 
 
 def trellis_kv4_read(cache: KV4Cache, layer: int, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, rows: int,
@@ -701,19 +725,33 @@ def trellis_kv4_read(cache: KV4Cache, layer: int, table: torch.Tensor, lens: tor
     shape = (rows, cache.n_kv_heads, cache.head_dim)
     k, v = (_out(o, shape, cache.device, dtype, n) for o, n in zip(out if out is not None else (None, None), ("k", "v")))
     b = _kv4_batch(cache, table, lens, cu, slots, rows)
-    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, _kv4_ws_bytes(), cache.device, stream)
     _check(lib().trellis_kv4_read(cache._ref, layer, ctypes.byref(b), _KV4_DTYPE[dtype], k.data_ptr(), v.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), _stream()))
+                                  ws.data_ptr(), ws.numel(), stream))
     return k, v
 
 
 def trellis_kv4_attn_workspace_bytes(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
                                      rows: int, n_q_heads: int, slots: Optional[torch.Tensor] = None) -> int:
     """Workspace bytes of trellis_kv4_attn for these sizes."""
-    b = _kv4_batch(cache, table, lens, cu, slots, rows)
-    nb = lib().trellis_kv4_attn_workspace_bytes(cache._ref, ctypes.byref(b), n_q_heads)
-    if nb == 0:
-        raise TrellisError(-1, lib().trellis_last_error().decode())
+    return _kv4_attn_bytes(cache, _kv4_batch(cache, table, lens, cu, slots, rows), n_q_heads)
+
+
+# Workspace sizes of attention by the sizes they follow from (not by tensors).
+_kv4_attn_nb: Dict[Tuple[int, ...], int] = {}
+
+
+def _kv4_attn_bytes(cache: KV4Cache, b: CKV4Batch, n_q_heads: int) -> int:
+    key = (cache.page_size, cache.n_kv_heads, cache.head_dim, b.max_pages, b.n_seq, b.rows, n_q_heads, cache.device.index)
+    nb = _kv4_attn_nb.get(key)
+    if nb is None:
+        nb = lib().trellis_kv4_attn_workspace_bytes(cache._ref, ctypes.byref(b), n_q_heads)
+        if nb == 0:
+            raise TrellisError(-1, lib().trellis_last_error().decode())
+        if len(_kv4_attn_nb) >= 4096:  # (a long-running server sees many row counts)
+            _kv4_attn_nb.clear()
+        _kv4_attn_nb[key] = nb
     return nb
 
 
@@ -733,28 +771,25 @@ def trellis_kv4_attn(cache: KV4Cache, layer: int, table: torch.Tensor, lens: tor
     if lse is not None:
         _out(lse, (rows, heads), cache.device, torch.float32, "lse")
     b = _kv4_batch(cache, table, lens, cu, slots, rows)
-    bref = ctypes.byref(b)
-    nb = lib().trellis_kv4_attn_workspace_bytes(cache._ref, bref, heads)
-    if nb == 0:
-        raise TrellisError(-1, lib().trellis_last_error().decode())
-    ws = _ws_arg(ws, nb, cache.device)
-    _check(lib().trellis_kv4_attn(cache._ref, layer, bref, _KV4_DTYPE[q.dtype], q.data_ptr(), q_row, q_head, heads,
-                                  cache.head_dim ** -0.5 if scale is None else scale, window, sinks, max_q,
-                                  out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream()))
+    stream = _stream()
+    ws = _kv4_ws(ws, _kv4_attn_bytes(cache, b, heads), cache.device, stream)
+    _check(lib().trellis_kv4_attn(cache._ref, layer, ctypes.byref(b), _KV4_DTYPE[q.dtype], q.data_ptr(), q_row, q_head,
+                                  heads, cache.head_dim ** -0.5 if scale is None else scale, window, sinks, max_q,
+                                  out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), stream))
     return out
 
 
 def _kv4_pages(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, **lists) -> int:
     """Checks the page operations' tensors; the number of items (the first list's length)."""
     _kv4_state(cache, table, lens)
-    _req(ref, torch.int32, "ref", cache.device)
+    _kv4_int(ref, "ref", cache.device)
     if ref.numel() != cache.n_pages:
         raise ValueError(f"ref must have one count per page ({cache.n_pages}), got {ref.numel()}")
     n = None
     for name, (t, extra) in lists.items():
         if t is None:
             continue
-        _req(t, torch.int32, name, cache.device)
+        _kv4_int(t, name, cache.device)
         if n is None:
             n = t.numel()
         elif t.numel() != n + extra:
@@ -767,9 +802,10 @@ def trellis_kv4_reserve(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor
     """lens[slots[i]] += add[i] (slots None: slot i) with the pages that takes, lowest first.
     If there are not enough, nothing changes and bit 8 of the error word is set."""
     n = _kv4_pages(cache, table, lens, ref, add=(add, 0), slots=(slots, 0))
-    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device, stream)
     _check(lib().trellis_kv4_reserve(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
-                                     ref.data_ptr(), _ptr(slots), add.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
+                                     ref.data_ptr(), _ptr(slots), add.data_ptr(), n, ws.data_ptr(), ws.numel(), stream))
 
 
 def trellis_kv4_fork(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, src: torch.Tensor,
@@ -777,9 +813,10 @@ def trellis_kv4_fork(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, r
     """Slot dst[i] becomes a copy of slot src[i]: full pages shared, a partly filled last page
     copied.  What dst held is released."""
     n = _kv4_pages(cache, table, lens, ref, src=(src, 0), dst=(dst, 0))
-    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device, stream)
     _check(lib().trellis_kv4_fork(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
-                                  ref.data_ptr(), src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
+                                  ref.data_ptr(), src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), ws.numel(), stream))
 
 
 def trellis_kv4_compact(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, src: torch.Tensor,
@@ -789,19 +826,21 @@ def trellis_kv4_compact(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor
     packed into new pages; dst[i] may be src[i].  What dst held is released."""
     n = _kv4_pages(cache, table, lens, ref, src=(src, 0), dst=(dst, 0), keep_cu=(keep_cu, 1))
     _req(keep, torch.int32, "keep", cache.device)
-    ws = _ws_arg(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, lib().trellis_kv4_pages_workspace_bytes(cache._ref, n), cache.device, stream)
     _check(lib().trellis_kv4_compact(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
                                      ref.data_ptr(), src.data_ptr(), dst.data_ptr(), n, keep.data_ptr(),
-                                     keep_cu.data_ptr(), keep.numel(), ws.data_ptr(), ws.numel(), _stream()))
+                                     keep_cu.data_ptr(), keep.numel(), ws.data_ptr(), ws.numel(), stream))
 
 
 def trellis_kv4_free(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor, slots: torch.Tensor,
                      ws: Optional[torch.Tensor] = None) -> None:
     """Release slots: their pages' counts drop, their lengths become 0."""
     n = _kv4_pages(cache, table, lens, ref, slots=(slots, 0))
-    ws = _ws_arg(ws, lib().trellis_kv4_workspace_bytes(), cache.device)
+    stream = _stream()
+    ws = _kv4_ws(ws, _kv4_ws_bytes(), cache.device, stream)
     _check(lib().trellis_kv4_free(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
-                                  ref.data_ptr(), slots.data_ptr(), n, ws.data_ptr(), ws.numel(), _stream()))
+                                  ref.data_ptr(), slots.data_ptr(), n, ws.data_ptr(), ws.numel(), stream))
 
 
 # ---------------------------------------------------------------------------------------

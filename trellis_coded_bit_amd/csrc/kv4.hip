@@ -269,13 +269,14 @@ __device__ __forceinline__ void release_pages(const Kv4Pages &p, int slot, int l
   }
 }
 
-// Copies `rows` tokens' codes and scales, both of keys and values and every block of one
-// (layer, head), between pages: a wave takes one contiguous code part and its scales.
-// Grid: x = item, y = shares of the (layer, head, part) units; workgroup y = 0 also writes the
-// child's table row and counts.
+// A child's table row and counts (workgroup y = 0), and its last page: a wave copies the rows that
+// are filled of one (layer, head) at a time, codes and scales of keys and values together, so that
+// four to twelve loads are in flight before the first store.  HBM bounds it.
+// Grid: x = item, y = shares of the (layer, head) units.
+template <int NB>
 __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {
   if (plan.status[0] != 1) return;
-  const int i = blockIdx.x, T = p.c.page_size, NB = p.c.head_dim >> 7;
+  const int i = blockIdx.x, T = p.c.page_size;
   const int s = p.src[i], d = p.dst[i], len = p.lens[s];
   const int full = len / T, part = len % T;
   const int32_t *from = p.table + (size_t)s * p.max_pages;
@@ -307,64 +308,89 @@ __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan pla
     if (blockIdx.y == 0 && threadIdx.x == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, parts = 2 * NB;
-  const int units = p.c.n_layers * p.c.n_kv_heads * parts;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int units = p.c.n_layers * p.c.n_kv_heads;
   for (int u = blockIdx.y * 4 + wave; u < units; u += gridDim.y * 4) {
-    const int q = u % parts, head = (u / parts) % p.c.n_kv_heads, layer = u / (parts * p.c.n_kv_heads);
+    const int head = u % p.c.n_kv_heads, layer = u / p.c.n_kv_heads;
     const char *x = kv4_chunk(p.c, layer, a, head);
     char *y = kv4_chunk(p.c, layer, z, head);
-    const int code = q * T * 64, scale = 128 * NB * T + q * T * 2;
-    for (int o = lane * 16; o < part * 64; o += 1024)
-      *reinterpret_cast<u32x4 *>(y + code + o) = ldg(reinterpret_cast<const u32x4 *>(x + code + o));
-    for (int t = lane; t < part; t += 64)
-      *reinterpret_cast<uint16_t *>(y + scale + 2 * t) = ldg(reinterpret_cast<const uint16_t *>(x + scale + 2 * t));
+    const char *xs = x + 128 * NB * T;
+    char *ys = y + 128 * NB * T;
+    for (int r0 = 0; r0 < part; r0 += 64) {  // 64 rows: four loads a part and a scale
+      u32x4 v[2 * NB][4];
+      uint16_t s[2 * NB];
+#pragma unroll
+      for (int q = 0; q < 2 * NB; ++q) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int o = r0 * 64 + k * 1024 + lane * 16;
+          if (o < part * 64) v[q][k] = ldg(reinterpret_cast<const u32x4 *>(x + q * T * 64 + o));
+        }
+        if (r0 + lane < part) s[q] = ldg(reinterpret_cast<const uint16_t *>(xs + (q * T + r0 + lane) * 2));
+      }
+#pragma unroll
+      for (int q = 0; q < 2 * NB; ++q) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int o = r0 * 64 + k * 1024 + lane * 16;
+          if (o < part * 64) *reinterpret_cast<u32x4 *>(y + q * T * 64 + o) = v[q][k];
+        }
+        if (r0 + lane < part) *reinterpret_cast<uint16_t *>(ys + (q * T + r0 + lane) * 2) = s[q];
+      }
+    }
   }
 }
 
 // Compaction's copy: a wave takes 16 kept rows (four lanes a row, 16 bytes a lane) and its share
-// of the (layer, head, part) units; a row's pages are looked up once.
+// of the (layer, head, part) units, four at a time so that their loads are in flight together; a
+// row's pages are looked up once for all units.
 __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {
   if (plan.status[0] != 1) return;
   const int T = p.c.page_size, NB = p.c.head_dim >> 7;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = blockIdx.x * 16;
-  // 16 lanes find a row's item together; rows are then handed to their four lanes
-  int mine = -1;
-  {
-    const int group = threadIdx.x >> 4;  // 16 groups, one row each
-    const int row = r16 + group;
-    int src_page = -1, src_at = 0, dst_page = -1, dst_at = 0;
+  __shared__ int4 rows[16];
+  {  // 16 lanes find a row's item together
+    const int group = threadIdx.x >> 4, row = r16 + group;
+    int4 t = make_int4(-1, 0, -1, 0);  // page and place of the source, of the destination
     if (row < p.n_keep) {
       const int i = kv4_seq_of(p.keep_cu, p.n, row, threadIdx.x & 15);
       if (i < p.n && row >= p.keep_cu[i]) {
         const int s = p.src[i], pos = p.keep[row], j = row - p.keep_cu[i];
-        if (pos >= 0 && pos < p.lens[s]) {
-          src_page = p.table[(size_t)s * p.max_pages + pos / T];
-          src_at = pos % T;
-          dst_page = plan.list[plan.first[i] + j / T];
-          dst_at = j % T;
-        }
+        if (pos >= 0 && pos < p.lens[s])
+          t = make_int4(p.table[(size_t)s * p.max_pages + pos / T], pos % T, plan.list[plan.first[i] + j / T], j % T);
       }
     }
-    __shared__ int4 rows[16];
-    if ((threadIdx.x & 15) == 0) rows[group] = make_int4(src_page, src_at, dst_page, dst_at);
-    __syncthreads();
-    const int4 t = rows[lane >> 2];
-    if ((uint32_t)t.x < (uint32_t)p.c.n_pages && t.z >= 0) mine = lane >> 2;
-    else if (wave == 0 && blockIdx.y == 0 && (lane & 3) == 0 && r16 + (lane >> 2) < p.n_keep) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
-    if (mine < 0) return;  // (no barrier follows)
-    const int c = lane & 3, parts = 2 * NB, units = p.c.n_layers * p.c.n_kv_heads * parts;
-    const int stride = gridDim.y * 4;
-#pragma unroll 4
-    for (int u = blockIdx.y * 4 + wave; u < units; u += stride) {
-      const int q = u % parts, head = (u / parts) % p.c.n_kv_heads, layer = u / (parts * p.c.n_kv_heads);
-      const char *x = kv4_chunk(p.c, layer, t.x, head);
-      char *y = kv4_chunk(p.c, layer, t.z, head);
-      *reinterpret_cast<u32x4 *>(y + (q * T + t.w) * 64 + 16 * c) =
-          ldg(reinterpret_cast<const u32x4 *>(x + (q * T + t.y) * 64 + 16 * c));
-      const int scale = 128 * NB * T + q * T * 2;
-      if (c == 0)
-        *reinterpret_cast<uint16_t *>(y + scale + 2 * t.w) = ldg(reinterpret_cast<const uint16_t *>(x + scale + 2 * t.y));
+    if ((threadIdx.x & 15) == 0) rows[group] = t;
+  }
+  __syncthreads();
+  const int4 t = rows[lane >> 2];
+  if ((uint32_t)t.x >= (uint32_t)p.c.n_pages || t.z < 0) {
+    if (wave == 0 && blockIdx.y == 0 && (lane & 3) == 0 && r16 + (lane >> 2) < p.n_keep) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
+    return;
+  }
+  const int c = lane & 3, shift = NB == 1 ? 1 : 2;  // log2 of the parts
+  const int units = (p.c.n_layers * p.c.n_kv_heads) << shift, stride = gridDim.y * 4;
+  for (int u0 = blockIdx.y * 4 + wave; u0 < units; u0 += 4 * stride) {
+    u32x4 v[4];
+    uint16_t s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * stride, q = u & ((1 << shift) - 1), h = u >> shift;
+      if (u < units) {
+        const char *x = kv4_chunk(p.c, h / p.c.n_kv_heads, t.x, h % p.c.n_kv_heads);
+        v[k] = ldg(reinterpret_cast<const u32x4 *>(x + (q * T + t.y) * 64 + 16 * c));
+        if (c == 0) s[k] = ldg(reinterpret_cast<const uint16_t *>(x + 128 * NB * T + (q * T + t.y) * 2));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = u0 + k * stride, q = u & ((1 << shift) - 1), h = u >> shift;
+      if (u < units) {
+        char *y = kv4_chunk(p.c, h / p.c.n_kv_heads, t.z, h % p.c.n_kv_heads);
+        *reinterpret_cast<u32x4 *>(y + (q * T + t.w) * 64 + 16 * c) = v[k];
+        if (c == 0) *reinterpret_cast<uint16_t *>(y + 128 * NB * T + (q * T + t.w) * 2) = s[k];
+      }
     }
   }
 }
@@ -433,8 +459,10 @@ hipError_t launch_kv4_fork(const Kv4Pages &p, void *ws, hipStream_t stream) {
   const PagesPlan plan = plan_of(ws, p.n);
   uint32_t *err = static_cast<uint32_t *>(ws);
   kv4_plan_kernel<kFork><<<1, kPlanThreads, bits_bytes(p.n_slots), stream>>>(p, plan, err);
-  const int units = p.c.n_layers * p.c.n_kv_heads * 2 * (p.c.head_dim / 128);
-  kv4_fork_kernel<<<dim3(p.n, (units + 3) / 4 < 4096 ? (units + 3) / 4 : 4096), 256, 0, stream>>>(p, plan, err);
+  const int units = p.c.n_layers * p.c.n_kv_heads;
+  const dim3 grid(p.n, (units + 3) / 4 < 4096 ? (units + 3) / 4 : 4096);
+  if (p.c.head_dim == 128) kv4_fork_kernel<1><<<grid, 256, 0, stream>>>(p, plan, err);
+  else kv4_fork_kernel<2><<<grid, 256, 0, stream>>>(p, plan, err);
   return hipGetLastError();
 }
 

@@ -10,92 +10,115 @@ namespace {
 // ---------------------------------------------------------------------------------------
 //
 // Sixteen lanes hold one 128-block, eight elements a lane: one 16-byte load or store of 16-bit
-// values, one word of codes.  A workgroup takes 16 consecutive rows of one (keys or values,
-// head, block), so its 64-byte code rows fall next to each other in a page.  HBM bounds long
-// calls (16-bit values in, a quarter of it out); a few rows are bound by the chain of loads
-// cu -> slot, length -> table before the store, which the row's own load overlaps.
+// values, one word of codes.  A workgroup takes 16 consecutive rows and N of the (keys or values,
+// head, block) kinds, so the 64-byte code rows of a kind fall next to each other in a page, and a
+// row's page is looked up once for N blocks.  HBM bounds long calls (16-bit values in, a quarter of
+// it out); a few rows are bound by the chain of loads cu -> slot, length -> table before the store,
+// which the rows' own loads overlap.  N = 4 where that still fills the card, else 1 (8901 rows of 8
+// heads: 25.5 us a call at N = 1; MEASURED_N).
 
-template <bool BF>
+template <bool BF, int N>
 __global__ __launch_bounds__(256) void kv4_append_kernel(trellis_kv4_cache c, int layer, trellis_kv4_batch b, Kv4Rows k,
                                                          Kv4Rows v, uint32_t *errword) {
-  const int NB = c.head_dim >> 7;
+  const int NB = c.head_dim >> 7, kinds = 2 * c.n_kv_heads * NB;
   const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
   if (row >= b.rows) return;  // (whole 16-lane groups leave together)
   const int i = threadIdx.x & 15, lane = threadIdx.x & 63;
-  const int kind = blockIdx.y, nb = kind % NB, head = (kind / NB) % c.n_kv_heads, is_v = kind / (NB * c.n_kv_heads);
-  const Kv4Rows src = is_v ? v : k;
-  const uint16_t *p = static_cast<const uint16_t *>(src.p) + row * src.row_stride + head * src.head_stride + nb * 128 + 8 * i;
-  const u32x4 raw = ldg(reinterpret_cast<const u32x4 *>(p));
+  u32x4 raw[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
+    const Kv4Rows src = kind >= kinds / 2 ? v : k;
+    if (kind < kinds)
+      raw[n] = ldg(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(src.p) + row * src.row_stride +
+                                                   head * src.head_stride + nb * 128 + 8 * i));
+  }
   const Kv4Place at = kv4_place(c, b, row, i);
   if (at.page < 0) {
-    if (i == 0 && kind == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
+    if (i == 0 && blockIdx.y == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
     return;
   }
-  float x[8];
-  kv4_unpack8<BF>(raw, x);
-  kv4_fwht16(x, lane);
-  float top = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    x[t] *= kRsqrt128;
-    top = fmaxf(top, fabsf(x[t]));
-    finite &= fabsf(x[t]) <= 3.4028234e38f;  // false for NaN
-  }
-  // a NaN or infinity anywhere in the block reaches every lane as an infinite maximum
-  if (!finite) top = __builtin_inff();
-  top = fmaxf(top, lane_xor<1>(top));
-  top = fmaxf(top, lane_xor<2>(top));
-  top = fmaxf(top, lane_xor<4>(top));
-  top = fmaxf(top, lane_xor<8>(top));
-  // the scale is rounded to bf16 first and the codes are taken against the rounded one
-  uint16_t s = kv4_narrow<true>(top * (1.f / 6.f));
-  const float sf = kv4_widen<true>(s);
-  uint32_t w = 0;
-  if (!(top <= 3.4028234e38f)) {
-    s = 0x7FC0;
-  } else if (sf < 1.17549435e-38f) {
-    s = 0;
-  } else {
-    const float inv = 1.f / sf;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.0f, 3);
-  }
   const Kv4Chunk ch{c.page_size, NB};
-  char *base = kv4_chunk(c, layer, at.page, head);
-  *reinterpret_cast<uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i) = w;
-  if (i == 0) *reinterpret_cast<uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at))) = s;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
+    const bool is_v = kind >= kinds / 2;
+    if (kind >= kinds) break;
+    float x[8];
+    kv4_unpack8<BF>(raw[n], x);
+    kv4_fwht16(x, lane);
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      x[t] *= kRsqrt128;
+      top = fmaxf(top, fabsf(x[t]));
+      finite &= fabsf(x[t]) <= 3.4028234e38f;  // false for NaN
+    }
+    // a NaN or infinity anywhere in the block reaches every lane as an infinite maximum
+    if (!finite) top = __builtin_inff();
+    top = fmaxf(top, lane_xor<1>(top));
+    top = fmaxf(top, lane_xor<2>(top));
+    top = fmaxf(top, lane_xor<4>(top));
+    top = fmaxf(top, lane_xor<8>(top));
+    // the scale is rounded to bf16 first and the codes are taken against the rounded one
+    uint16_t s = kv4_narrow<true>(top * (1.f / 6.f));
+    const float sf = kv4_widen<true>(s);
+    uint32_t w = 0;
+    if (!(top <= 3.4028234e38f)) {
+      s = 0x7FC0;
+    } else if (sf < 1.17549435e-38f) {
+      s = 0;
+    } else {
+      const float inv = 1.f / sf;
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.0f, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.0f, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.0f, 2);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.0f, 3);
+    }
+    char *base = kv4_chunk(c, layer, at.page, head);
+    *reinterpret_cast<uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i) = w;
+    if (i == 0) *reinterpret_cast<uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at))) = s;
+  }
 }
 
-template <bool BF>
+template <bool BF, int N>
 __global__ __launch_bounds__(256) void kv4_read_kernel(trellis_kv4_cache c, int layer, trellis_kv4_batch b, uint16_t *k,
                                                        uint16_t *v, uint32_t *errword) {
-  const int NB = c.head_dim >> 7;
+  const int NB = c.head_dim >> 7, kinds = 2 * c.n_kv_heads * NB;
   const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
   if (row >= b.rows) return;
   const int i = threadIdx.x & 15, lane = threadIdx.x & 63;
-  const int kind = blockIdx.y, nb = kind % NB, head = (kind / NB) % c.n_kv_heads, is_v = kind / (NB * c.n_kv_heads);
   const Kv4Place at = kv4_place(c, b, row, i);
-  float x[8];
+  if (at.page < 0 && i == 0 && blockIdx.y == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
+  const Kv4Chunk ch{c.page_size, NB};
+  uint32_t w[N];
+  uint16_t s[N];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) x[t] = 0.f;
-  if (at.page >= 0) {
-    const Kv4Chunk ch{c.page_size, NB};
-    const char *base = kv4_chunk(c, layer, at.page, head);
-    const uint32_t w = ldg(reinterpret_cast<const uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i));
-    const float s = kv4_widen<true>(ldg(reinterpret_cast<const uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at)))));
-    kv4_values8(w, x);
+  for (int n = 0; n < N; ++n) {
+    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
+    const bool is_v = kind >= kinds / 2;
+    w[n] = 0;
+    s[n] = 0;
+    if (kind < kinds && at.page >= 0) {
+      const char *base = kv4_chunk(c, layer, at.page, head);
+      w[n] = ldg(reinterpret_cast<const uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i));
+      s[n] = ldg(reinterpret_cast<const uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at))));
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
+    if (kind >= kinds) break;
+    float x[8];
+    kv4_values8(w[n], x);
     kv4_fwht16(x, lane);
-    const float f = s * kRsqrt128;
+    const float f = kv4_widen<true>(s[n]) * kRsqrt128;
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
-  } else if (i == 0 && kind == 0) {
-    kv4_error(errword, TRELLIS_KV4_ERR_BAD);
+    uint16_t *y = (kind >= kinds / 2 ? v : k) + ((size_t)row * c.n_kv_heads + head) * c.head_dim + nb * 128 + 8 * i;
+    *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(x);
   }
-  uint16_t *y = (is_v ? v : k) + ((size_t)row * c.n_kv_heads + head) * c.head_dim + nb * 128 + 8 * i;
-  *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(x);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -271,7 +294,8 @@ __device__ __forceinline__ void release_pages(const Kv4Pages &p, int slot, int l
 
 // A child's table row and counts (workgroup y = 0), and its last page: a wave copies the rows that
 // are filled of one (layer, head) at a time, codes and scales of keys and values together, so that
-// four to twelve loads are in flight before the first store.  HBM bounds it.
+// up to 20 loads are in flight before the first store.  HBM bounds it; the stores bypass the caches,
+// which keep the parents' pages (192 children of 48 parents, 32 layers: 126 -> 59 us).
 // Grid: x = item, y = shares of the (layer, head) units.
 template <int NB>
 __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {
@@ -333,7 +357,7 @@ __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan pla
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int o = r0 * 64 + k * 1024 + lane * 16;
-          if (o < part * 64) *reinterpret_cast<u32x4 *>(y + q * T * 64 + o) = v[q][k];
+          if (o < part * 64) __builtin_nontemporal_store(v[q][k], reinterpret_cast<u32x4 *>(y + q * T * 64 + o));
         }
         if (r0 + lane < part) *reinterpret_cast<uint16_t *>(ys + (q * T + r0 + lane) * 2) = s[q];
       }
@@ -343,7 +367,9 @@ __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan pla
 
 // Compaction's copy: a wave takes 16 kept rows (four lanes a row, 16 bytes a lane) and its share
 // of the (layer, head, part) units, four at a time so that their loads are in flight together; a
-// row's pages are looked up once for all units.
+// row's pages are looked up once for all units.  HBM bounds it: rows are 64 bytes, so where about half
+// are kept most 128-byte lines are read for one of their two (12 x 55% of up to 4000 tokens, 16 layers:
+// 300 MB kept, 174 us with ordinary accesses, 156 with ones that bypass the caches).
 __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {
   if (plan.status[0] != 1) return;
   const int T = p.c.page_size, NB = p.c.head_dim >> 7;
@@ -379,7 +405,7 @@ __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, Pages
       const int u = u0 + k * stride, q = u & ((1 << shift) - 1), h = u >> shift;
       if (u < units) {
         const char *x = kv4_chunk(p.c, h / p.c.n_kv_heads, t.x, h % p.c.n_kv_heads);
-        v[k] = ldg(reinterpret_cast<const u32x4 *>(x + (q * T + t.y) * 64 + 16 * c));
+        v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + (q * T + t.y) * 64 + 16 * c));
         if (c == 0) s[k] = ldg(reinterpret_cast<const uint16_t *>(x + 128 * NB * T + (q * T + t.y) * 2));
       }
     }
@@ -388,7 +414,7 @@ __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, Pages
       const int u = u0 + k * stride, q = u & ((1 << shift) - 1), h = u >> shift;
       if (u < units) {
         char *y = kv4_chunk(p.c, h / p.c.n_kv_heads, t.z, h % p.c.n_kv_heads);
-        *reinterpret_cast<u32x4 *>(y + (q * T + t.w) * 64 + 16 * c) = v[k];
+        __builtin_nontemporal_store(v[k], reinterpret_cast<u32x4 *>(y + (q * T + t.w) * 64 + 16 * c));
         if (c == 0) *reinterpret_cast<uint16_t *>(y + 128 * NB * T + (q * T + t.w) * 2) = s[k];
       }
     }
@@ -429,20 +455,33 @@ size_t bits_bytes(int n_slots) { return (size_t)((n_slots + 31) / 32) * 4; }
 
 }  // namespace
 
+namespace {
+// Kinds a workgroup takes: four where 2048 workgroups (eight a CU) remain.
+int kinds_each(const trellis_kv4_cache &c, const trellis_kv4_batch &b) {
+  const long long groups = (long long)((b.rows + 15) / 16) * 2 * c.n_kv_heads * (c.head_dim / 128);
+  return groups >= 4 * 2048 ? 4 : 1;
+}
+}  // namespace
+
 hipError_t launch_kv4_append(const trellis_kv4_cache &c, int layer, const trellis_kv4_batch &b, int dtype,
                              const Kv4Rows &k, const Kv4Rows &v, uint32_t *errword, hipStream_t stream) {
-  const dim3 grid((b.rows + 15) / 16, 2 * c.n_kv_heads * (c.head_dim / 128));
-  if (dtype == TRELLIS_KV4_BF16) kv4_append_kernel<true><<<grid, 256, 0, stream>>>(c, layer, b, k, v, errword);
-  else kv4_append_kernel<false><<<grid, 256, 0, stream>>>(c, layer, b, k, v, errword);
+  const int n = kinds_each(c, b), kinds = 2 * c.n_kv_heads * (c.head_dim / 128);
+  const dim3 grid((b.rows + 15) / 16, (kinds + n - 1) / n);
+  const bool bf = dtype == TRELLIS_KV4_BF16;
+  const auto kernel = n == 4 ? (bf ? kv4_append_kernel<true, 4> : kv4_append_kernel<false, 4>)
+                             : (bf ? kv4_append_kernel<true, 1> : kv4_append_kernel<false, 1>);
+  kernel<<<grid, 256, 0, stream>>>(c, layer, b, k, v, errword);
   return hipGetLastError();
 }
 
 hipError_t launch_kv4_read(const trellis_kv4_cache &c, int layer, const trellis_kv4_batch &b, int dtype, void *k,
                            void *v, uint32_t *errword, hipStream_t stream) {
-  const dim3 grid((b.rows + 15) / 16, 2 * c.n_kv_heads * (c.head_dim / 128));
-  uint16_t *ko = static_cast<uint16_t *>(k), *vo = static_cast<uint16_t *>(v);
-  if (dtype == TRELLIS_KV4_BF16) kv4_read_kernel<true><<<grid, 256, 0, stream>>>(c, layer, b, ko, vo, errword);
-  else kv4_read_kernel<false><<<grid, 256, 0, stream>>>(c, layer, b, ko, vo, errword);
+  const int n = kinds_each(c, b), kinds = 2 * c.n_kv_heads * (c.head_dim / 128);
+  const dim3 grid((b.rows + 15) / 16, (kinds + n - 1) / n);
+  const bool bf = dtype == TRELLIS_KV4_BF16;
+  const auto kernel = n == 4 ? (bf ? kv4_read_kernel<true, 4> : kv4_read_kernel<false, 4>)
+                             : (bf ? kv4_read_kernel<true, 1> : kv4_read_kernel<false, 1>);
+  kernel<<<grid, 256, 0, stream>>>(c, layer, b, static_cast<uint16_t *>(k), static_cast<uint16_t *>(v), errword);
   return hipGetLastError();
 }
 

@@ -17,21 +17,31 @@ namespace {
 // which the rows' own loads overlap.  N = 4 where that still fills the card, else 1 (8901 rows of 8
 // heads: 25.5 us a call at N = 1; MEASURED_N).
 
+// The largest of 16 lanes' numbers.
+__device__ __forceinline__ uint32_t kv4_max16(uint32_t v) {
+  const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));
+  return up(v, __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true));
+}
+
 template <bool BF, int N>
 __global__ __launch_bounds__(256) void kv4_append_kernel(trellis_kv4_cache c, int layer, trellis_kv4_batch b, Kv4Rows k,
                                                          Kv4Rows v, uint32_t *errword) {
   const int NB = c.head_dim >> 7, kinds = 2 * c.n_kv_heads * NB;
   const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
   if (row >= b.rows) return;  // (whole 16-lane groups leave together)
-  const int i = threadIdx.x & 15, lane = threadIdx.x & 63;
+  const int i = threadIdx.x & 15, place = kv4_fwht16_place(i);
+  const float sign = kv4_fwht16_sign(i) * kRsqrt128;
   u32x4 raw[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
-    const Kv4Rows src = kind >= kinds / 2 ? v : k;
-    if (kind < kinds)
+    const Kv4Kind kind = kv4_kind(c, blockIdx.y * N + n);
+    const Kv4Rows src = kind.is_v ? v : k;
+    if (blockIdx.y * N + n < kinds)
       raw[n] = ldg(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(src.p) + row * src.row_stride +
-                                                   head * src.head_stride + nb * 128 + 8 * i));
+                                                   kind.head * src.head_stride + kind.nb * 128 + 8 * i));
   }
   const Kv4Place at = kv4_place(c, b, row, i);
   if (at.page < 0) {
@@ -39,45 +49,42 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(trellis_kv4_cache c, in
     return;
   }
   const Kv4Chunk ch{c.page_size, NB};
+  const uint32_t chunk = ch.bytes();  // (a page's bytes fit 32 bits: 1024 heads of 132 * 2 * 256)
+  char *page = kv4_chunk(c, layer, at.page < 0 ? 0 : at.page, 0);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
-    const bool is_v = kind >= kinds / 2;
-    if (kind >= kinds) break;
+    if (blockIdx.y * N + n >= kinds) break;
+    const auto [head, nb, is_v] = kv4_kind(c, blockIdx.y * N + n);
     float x[8];
     kv4_unpack8<BF>(raw[n], x);
-    kv4_fwht16(x, lane);
-    float top = 0.f;
-    bool finite = true;
+    kv4_fwht16_signed(x, i);
+    // the largest magnitude as an integer: infinity is above every number, a NaN above infinity
+    uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      x[t] *= kRsqrt128;
-      top = fmaxf(top, fabsf(x[t]));
-      finite &= fabsf(x[t]) <= 3.4028234e38f;  // false for NaN
+      const uint32_t m = __builtin_bit_cast(uint32_t, x[t]) & 0x7FFFFFFFu;
+      top = m > top ? m : top;
     }
-    // a NaN or infinity anywhere in the block reaches every lane as an infinite maximum
-    if (!finite) top = __builtin_inff();
-    top = fmaxf(top, lane_xor<1>(top));
-    top = fmaxf(top, lane_xor<2>(top));
-    top = fmaxf(top, lane_xor<4>(top));
-    top = fmaxf(top, lane_xor<8>(top));
+    top = kv4_max16(top);
     // the scale is rounded to bf16 first and the codes are taken against the rounded one
-    uint16_t s = kv4_narrow<true>(top * (1.f / 6.f));
+    uint16_t s = kv4_narrow<true>(__builtin_bit_cast(float, top) * kRsqrt128 * (1.f / 6.f));
     const float sf = kv4_widen<true>(s);
     uint32_t w = 0;
-    if (!(top <= 3.4028234e38f)) {
+    if (top >= 0x7F800000u) {
       s = 0x7FC0;
     } else if (sf < 1.17549435e-38f) {
       s = 0;
     } else {
-      const float inv = 1.f / sf;
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.0f, 0);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.0f, 1);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.0f, 2);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.0f, 3);
+      const float inv = 1.f / sf * sign;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) x[t] *= inv;
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], 1.0f, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], 1.0f, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], 1.0f, 2);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], 1.0f, 3);
     }
-    char *base = kv4_chunk(c, layer, at.page, head);
-    *reinterpret_cast<uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i) = w;
+    char *base = page + (uint32_t)head * chunk;
+    *reinterpret_cast<uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * place) = w;
     if (i == 0) *reinterpret_cast<uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at))) = s;
   }
 }
@@ -88,35 +95,37 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(trellis_kv4_cache c, int 
   const int NB = c.head_dim >> 7, kinds = 2 * c.n_kv_heads * NB;
   const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
   if (row >= b.rows) return;
-  const int i = threadIdx.x & 15, lane = threadIdx.x & 63;
+  const int i = threadIdx.x & 15, place = kv4_fwht16_place(i);
+  const float sign = kv4_fwht16_sign(i) * kRsqrt128;
   const Kv4Place at = kv4_place(c, b, row, i);
   if (at.page < 0 && i == 0 && blockIdx.y == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
   const Kv4Chunk ch{c.page_size, NB};
+  const uint32_t chunk = ch.bytes();  // (a page's bytes fit 32 bits: 1024 heads of 132 * 2 * 256)
+  char *page = kv4_chunk(c, layer, at.page < 0 ? 0 : at.page, 0);
   uint32_t w[N];
   uint16_t s[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
-    const bool is_v = kind >= kinds / 2;
+    const auto [head, nb, is_v] = kv4_kind(c, blockIdx.y * N + n);
     w[n] = 0;
     s[n] = 0;
-    if (kind < kinds && at.page >= 0) {
-      const char *base = kv4_chunk(c, layer, at.page, head);
+    if (blockIdx.y * N + n < kinds && at.page >= 0) {
+      const char *base = page + (uint32_t)head * chunk;
       w[n] = ldg(reinterpret_cast<const uint32_t *>(base + (is_v ? ch.v_code(nb, at.at) : ch.k_code(nb, at.at)) + 4 * i));
       s[n] = ldg(reinterpret_cast<const uint16_t *>(base + (is_v ? ch.v_scale(nb, at.at) : ch.k_scale(nb, at.at))));
     }
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int kind = blockIdx.y * N + n, nb = kind % NB, head = (kind / NB) % c.n_kv_heads;
-    if (kind >= kinds) break;
+    if (blockIdx.y * N + n >= kinds) break;
+    const auto [head, nb, is_v] = kv4_kind(c, blockIdx.y * N + n);
     float x[8];
     kv4_values8(w[n], x);
-    kv4_fwht16(x, lane);
-    const float f = kv4_widen<true>(s[n]) * kRsqrt128;
+    kv4_fwht16_signed(x, i);
+    const float f = kv4_widen<true>(s[n]) * sign;
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
-    uint16_t *y = (kind >= kinds / 2 ? v : k) + ((size_t)row * c.n_kv_heads + head) * c.head_dim + nb * 128 + 8 * i;
+    uint16_t *y = (is_v ? v : k) + ((size_t)row * c.n_kv_heads + head) * c.head_dim + nb * 128 + 8 * place;
     *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(x);
   }
 }
@@ -172,7 +181,7 @@ __device__ __forceinline__ long long block_prefix(long long v, long long *lds, l
   return lds[wave] + x - v;
 }
 
-__device__ __forceinline__ int pages_of_len(int len, int T) { return (int)(((long long)len + T - 1) / T); }
+__device__ __forceinline__ int pages_of_len(int len, int T) { return (int)(((long long)len + T - 1) >> kv4_page_log2(T)); }
 
 // What item i needs, or -1 where the call has to be refused.
 template <int MODE>
@@ -372,7 +381,7 @@ __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan pla
 // 300 MB kept, 174 us with ordinary accesses, 156 with ones that bypass the caches).
 __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {
   if (plan.status[0] != 1) return;
-  const int T = p.c.page_size, NB = p.c.head_dim >> 7;
+  const int T = p.c.page_size, log_t = kv4_page_log2(T), NB = p.c.head_dim >> 7;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = blockIdx.x * 16;
   __shared__ int4 rows[16];
@@ -384,7 +393,8 @@ __global__ __launch_bounds__(256) void kv4_compact_copy_kernel(Kv4Pages p, Pages
       if (i < p.n && row >= p.keep_cu[i]) {
         const int s = p.src[i], pos = p.keep[row], j = row - p.keep_cu[i];
         if (pos >= 0 && pos < p.lens[s])
-          t = make_int4(p.table[(size_t)s * p.max_pages + pos / T], pos % T, plan.list[plan.first[i] + j / T], j % T);
+          t = make_int4(p.table[(size_t)s * p.max_pages + (pos >> log_t)], pos & (T - 1), plan.list[plan.first[i] + (j >> log_t)],
+                        j & (T - 1));
       }
     }
     if ((threadIdx.x & 15) == 0) rows[group] = t;

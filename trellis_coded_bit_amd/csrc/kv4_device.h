@@ -24,6 +24,9 @@ __device__ __forceinline__ uint16_t kv4_narrow(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
+// log2 of a page's tokens (16 .. 256): positions are split by shift and mask.
+__device__ __forceinline__ int kv4_page_log2(int page_size) { return __builtin_ctz(page_size); }
+
 // Where one (page, head) chunk's parts lie, in bytes from its start: T tokens, NB blocks.
 struct Kv4Chunk {
   int T, NB;
@@ -67,11 +70,23 @@ __device__ __forceinline__ Kv4Place kv4_place(const trellis_kv4_cache &c, const 
   const int c0 = ldg(b.cu + s), c1 = ldg(b.cu + s + 1);
   const long long pos = (long long)ldg(b.lens + slot) - c1 + row;  // len - (c1 - c0) + (row - c0)
   if (row < c0 || pos < 0 || pos >= (long long)b.max_pages * c.page_size) return r;
-  const int page = ldg(b.table + (size_t)slot * b.max_pages + (int)(pos / c.page_size));
+  const int page = ldg(b.table + (size_t)slot * b.max_pages + ((int)pos >> kv4_page_log2(c.page_size)));
   if ((uint32_t)page >= (uint32_t)c.n_pages) return r;
   r.page = page;
-  r.at = (int)(pos % c.page_size);
+  r.at = (int)pos & (c.page_size - 1);
   return r;
+}
+
+// Kind n of a row's 2 * n_kv_heads * NB blocks: keys' blocks head by head, then the values'.
+struct Kv4Kind {
+  int head, nb;
+  bool is_v;
+};
+__device__ __forceinline__ Kv4Kind kv4_kind(const trellis_kv4_cache &c, int n) {
+  const int log_nb = c.head_dim >> 8, half = c.n_kv_heads << log_nb;
+  const bool is_v = n >= half;
+  const int k = is_v ? n - half : n;
+  return {k >> log_nb, k & log_nb, is_v};
 }
 
 // H_128 (unnormalised) over 16 lanes holding elements 8i .. 8i+7, strides 1, 2, 4 .. 64 in
@@ -96,6 +111,47 @@ __device__ __forceinline__ void kv4_fwht16(float (&v)[8], int lane) {
   for (int t = 0; t < 8; ++t) v[t] = lane_xor<4>(v[t]) + sg4 * v[t];
 #pragma unroll
   for (int t = 0; t < 8; ++t) v[t] = lane_xor<8>(v[t]) + sg8 * v[t];
+}
+
+// The same, up to a sign a lane and the order of the lanes, in one instruction an element and
+// stage across lanes: v + c v', with v' the partner's and c = -1 in a pair's second lane, is the
+// butterfly with that lane's result negated, and all of a later stage's partners carry the same
+// negations.  The third stage pairs i with 7 - i, which one lane pattern reaches and i ^ 4 does
+// not; H_8 over the masks 1, 2, 7 is H_8 over 1, 2, 4 with its outputs in another order.  Lane i
+// ends with elements 8 k .. 8 k + 7, k = kv4_fwht16_place(i), times kv4_fwht16_sign(i).
+__device__ __forceinline__ int kv4_fwht16_place(int i) {
+  const int b2 = (i >> 2) & 1, k0 = (i & 1) ^ b2, k1 = ((i >> 1) & 1) ^ b2;
+  return (i & 8) | ((k0 ^ k1 ^ b2) << 2) | (k1 << 1) | k0;
+}
+__device__ __forceinline__ float kv4_fwht16_sign(int i) { return (__builtin_popcount(i & 15) & 1) ? -1.f : 1.f; }
+__device__ __forceinline__ void kv4_fwht16_signed(float (&v)[8], int i) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if ((t & h) == 0) {
+        const float a = v[t], b = v[t + h];
+        v[t] = a + b;
+        v[t + h] = a - b;
+      }
+  const int b2 = (i >> 2) & 1;
+  const float c1 = ((i & 1) ^ b2) ? -1.f : 1.f, c2 = (((i >> 1) & 1) ^ b2) ? -1.f : 1.f;
+  const float c7 = b2 ? -1.f : 1.f, c8 = (i & 8) ? -1.f : 1.f;
+  // One block: a lane pattern's operand must have been written at least two instructions before
+  // (the leading wait; then every element is eight instructions old).
+  asm("s_nop 4\n\t"
+#define KV4_STAGE(c, pattern)                                                                                          \
+  "v_fmac_f32_dpp %0, %0, " c " " pattern "\n\tv_fmac_f32_dpp %1, %1, " c " " pattern                                  \
+  "\n\tv_fmac_f32_dpp %2, %2, " c " " pattern "\n\tv_fmac_f32_dpp %3, %3, " c " " pattern                            \
+  "\n\tv_fmac_f32_dpp %4, %4, " c " " pattern "\n\tv_fmac_f32_dpp %5, %5, " c " " pattern                            \
+  "\n\tv_fmac_f32_dpp %6, %6, " c " " pattern "\n\tv_fmac_f32_dpp %7, %7, " c " " pattern "\n\t"
+      KV4_STAGE("%8", "quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf bound_ctrl:1")
+      KV4_STAGE("%9", "quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf bound_ctrl:1")
+      KV4_STAGE("%10", "row_half_mirror row_mask:0xf bank_mask:0xf bound_ctrl:1")
+      KV4_STAGE("%11", "row_ror:8 row_mask:0xf bank_mask:0xf bound_ctrl:1")
+#undef KV4_STAGE
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])
+      : "v"(c1), "v"(c2), "v"(c7), "v"(c8));
 }
 
 template <bool BF>

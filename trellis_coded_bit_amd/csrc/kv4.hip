@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(trellis_kv4_cache c, int 
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
     uint16_t *y = (is_v ? v : k) + ((size_t)row * c.n_kv_heads + head) * c.head_dim + nb * 128 + 8 * place;
-    *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(x);
+    __builtin_nontemporal_store(kv4_pack8<BF>(x), reinterpret_cast<u32x4 *>(y));
   }
 }
 

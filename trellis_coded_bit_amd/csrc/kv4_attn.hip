@@ -175,8 +175,7 @@ __device__ __forceinline__ v8i read_values(const WaveLds<NB, R> &lds, int nb, in
   return v8i{a[0], a[1], b[0], b[1], 0, 0, 0, 0};
 }
 
-// Scores of a lane's own keys (own word t's key i), in units of cf[0] (one block) or in powers of
-// two (two blocks).
+// Scores of a lane's own keys (own word t's key i), in powers of two.
 template <int NB, int R>
 __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB, kCols / R> &q, const Column<NB> &col,
                                        const WaveLds<NB, R> &lds, float (&x)[8 / R][4]) {
@@ -194,9 +193,9 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB,
     for (int j = 0; j < 8; ++j) {
       const v8i a = {k[nb][j][0], k[nb][j][1], k[nb][j][2], k[nb][j][3], 0, 0, 0, 0};
       floatx4 s = {0.f, 0.f, 0.f, 0.f};
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 0, 0, scale_byte(0), 0, col.scale[nb]);
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 0, 0, scale_byte(0), 1, col.scale[nb]);
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 0, 0, scale_byte(0), 2, col.scale[nb]);
       constexpr int H = 4 / R;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -208,9 +207,8 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB,
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float z = y[t][i] * scale_of(ks, t, i);
-        if (NB == 1) x[t][i] = z;
-        else x[t][i] = nb ? fmaf(z, col.cf[nb], x[t][i]) : z * col.cf[nb];
+        const float s = scale_of(ks, t, i);
+        x[t][i] = nb ? fmaf(y[t][i], s, x[t][i]) : y[t][i] * s;
       }
   }
 }
@@ -262,8 +260,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
   if (R >= 4) top = fmaxf(top, lane_xor<4>(top));
   if (R >= 2) top = fmaxf(top, lane_xor<8>(top));
   top = max4(top);
-  const float cf = NB == 1 ? col.cf[0] : 1.f;
-  const float m = fmaxf(sum.m, top * cf);
+  const float m = fmaxf(sum.m, top);
   const float mu = m == kNegInf ? 0.f : m;  // nothing seen so far
   const float alpha = __builtin_amdgcn_exp2f(sum.m - mu);
   sum.m = m;
@@ -272,7 +269,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[t][i] = __builtin_amdgcn_exp2f(fmaf(x[t][i], cf, -mu));
+      x[t][i] = __builtin_amdgcn_exp2f(x[t][i] - mu);
       add += x[t][i];
     }
   sum.l = fmaf(sum.l, alpha, add);
@@ -556,7 +553,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       const int cc = lane & (C - 1);
       column.pos = cc < cols ? q.len - q.n + (col0 + cc) / g.group : -1;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) column.cf[nb] = lds.q.cf[nb][cc];
+      for (int nb = 0; nb < NB; ++nb) column.scale[nb] = lds.q.scale[nb][cc];
     }
     // ---- this wave's tiles
     Sums<NB> sum;
@@ -804,7 +801,7 @@ size_t kv4_attn_workspace_bytes(const trellis_kv4_cache &c, const trellis_kv4_ba
 // A sequence of at most this many columns (rows times query heads per key/value head) is the
 // narrow kernel's, whose tiles are 16 columns wide and shared by any number of workgroups; the
 // wide kernel's are 128.  MEASURED_FEW
-constexpr int kFew = 48;
+constexpr int kFew = 96;
 
 hipError_t launch_kv4_attn(const Kv4Attn &a, void *ws, hipStream_t stream) {
   AttnArgs g{};

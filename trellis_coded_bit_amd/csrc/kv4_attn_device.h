@@ -111,12 +111,13 @@ __device__ __forceinline__ float sum4(float v) {
 // Byte of a power of two 2^e as a matrix instruction's scale.
 __device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
 
-// C columns' rotated queries as matrix operands, in shared memory: lane group g of a column's
+// C columns' rotated queries as matrix operands, in shared memory, times the softmax's scale and
+// log2 e: a product with its scales is a score in powers of two.  Lane group g of a column's
 // E4M3 operand holds elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block.
 template <int NB, int C>
 struct QueryLds {
   alignas(16) int part[NB][3][C][4][8];
-  float cf[NB][C];  // score = cf * (sum over parts), in powers of two; > 0, so a hidden score stays minus infinity
+  int scale[NB][C];  // a byte a part: its power of two as the matrix instructions take it
 };
 
 // Sixteen lanes to a column, eight elements each.
@@ -152,6 +153,7 @@ __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> 
     bool finite = true;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
+      x[t] *= g.a.scale * (kLog2e * kRsqrt128);
       top = fmaxf(top, fabsf(x[t]));
       finite &= fabsf(x[t]) <= 3.4028234e38f;
     }
@@ -161,11 +163,10 @@ __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> 
     top = fmaxf(top, lane_xor<4>(top));
     top = fmaxf(top, lane_xor<8>(top));
     // the largest element comes to [128, 256); a column that is not finite becomes NaN
-    const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 8);
-    float f = __builtin_bit_cast(float, (uint32_t)min(261 - e, 254) << 23);
+    const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 16);
+    float f = __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);
     if (top > 3.4028234e38f) f = __builtin_nanf("");
-    if (g.a.scale < 0.f) f = -f;
-    if (i == 0) lds.cf[nb][c] = fmaxf(__builtin_bit_cast(float, (uint32_t)(e - 7) << 23) * (fabsf(g.a.scale) * kLog2e * kRsqrt128), 1e-37f);
+    if (i == 0) lds.scale[nb][c] = (e - 7) | (e - 11) << 8 | (e - 15) << 16;
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
 #pragma unroll
@@ -191,7 +192,7 @@ __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> 
 // What a lane keeps of its column.
 template <int NB>
 struct Column {
-  float cf[NB];
+  int scale[NB];
   int pos;  // the column's position (-1: sees nothing)
 };
 

@@ -122,10 +122,12 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
                                           float (&l)[kColTiles], floatx4 (&o)[kColTiles][NB][8]) {
   constexpr int CT = kColTiles;
   const int lane = opaque_tid() & 63;
+  const float log2f = (float)max(134 - e_run[0], -60);  // (2^-60: weights stay far from the smallest number)
         half8 w[CT][NB][4];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          // ---- scores
+          // ---- scores, from the running maximum (or from 0) as the weights' powers of two
+          const float mu = m[ct] == kNegInf ? 0.f : m[ct], c0 = log2f - mu;
           float y[8][4];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -139,14 +141,12 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
               const v4i kv = *reinterpret_cast<const v4i *>(kp + (j >> 1) * 256 + c * 16);
               const v8i a = {kv[0], kv[1], kv[2], kv[3], 0, 0, 0, 0};
               floatx4 z = {0.f, 0.f, 0.f, 0.f};
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, scale_byte(0));
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-4));
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 0, scale_byte(-8));
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, col[ct].scale[nb]);
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 1, col[ct].scale[nb]);
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 2, col[ct].scale[nb]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float u = z[i] * ks[key32(j, i)];
-                if (NB == 1) y[j][i] = u;
-                else y[j][i] = nb ? fmaf(u, col[ct].cf[nb], y[j][i]) : u * col[ct].cf[nb];
+                y[j][i] = fmaf(z[i], ks[key32(j, i)], nb ? y[j][i] : c0);
               }
             }
           }
@@ -165,36 +165,32 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
         }
     }
     // The running maximum stays until a lane's weights outgrow 2^7 together: most tiles then need
-    // neither a maximum nor a rescaling.  (A column that has seen nothing has m = -inf and comes here
-    // with infinite or NaN weights.)  The power of two f[0] is taken into the exponent.
-    const float cf = NB == 1 ? col[ct].cf[0] : 1.f;
-    const float log2f = (float)(134 - e_run[0]);
-    float x[8][4], add = 0.f, alpha = 1.f;
-    {
-      const float c0 = log2f - m[ct];
+    // neither a maximum nor a rescaling.  The power of two f[0] is taken into the exponent.
+    float add = 0.f, alpha = 1.f;
+    float x[8][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[j][i] = __builtin_amdgcn_exp2f(fmaf(y[j][i], cf, c0));
-          add += x[j][i];
-        }
-    }
-    if (__any(!(add <= 128.f * f[0]))) {
+      for (int i = 0; i < 4; ++i) {
+        x[j][i] = __builtin_amdgcn_exp2f(y[j][i]);
+        add += x[j][i];
+      }
+    const float one = __builtin_amdgcn_exp2f(log2f);  // a weight of 1
+    if (__any(!(add <= 128.f * one) | (m[ct] == kNegInf))) {
       float top = kNegInf;
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
       top = max4(top);
-      const float m2 = fmaxf(m[ct], top * cf);
-      const float mu = m2 == kNegInf ? 0.f : m2;  // nothing seen so far
-      alpha = __builtin_amdgcn_exp2f(m[ct] - mu);
-      m[ct] = m2;
+      // by how much the maximum grows (where there was none, from 0)
+      const float by = m[ct] == kNegInf ? top - log2f : fmaxf(top - log2f, 0.f), up = by == kNegInf ? 0.f : by;
+      alpha = m[ct] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(-up);
+      m[ct] = m[ct] == kNegInf ? by : m[ct] + up;
       add = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[j][i] = __builtin_amdgcn_exp2f(fmaf(y[j][i], cf, log2f - mu));
+          x[j][i] = __builtin_amdgcn_exp2f(y[j][i] - up);
           add += x[j][i];
         }
     }
@@ -205,6 +201,12 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
     for (int nb = 0; nb < NB; ++nb) {
       float vs[32];
       read_scales32(lds.vs[buf][nb], vs);
+      if (nb == 0 && e_run[0] > 194) {  // what the exponent's bound left
+        asm volatile("");
+        const float rest = f[0] * __builtin_amdgcn_exp2f(-log2f);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) vs[k] *= rest;
+      }
       if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
         asm volatile("");
 #pragma unroll
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     col[ct].pos = c < col0 + cols ? q.len - q.n + c / g.group : -1;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      col[ct].cf[nb] = lds.q[wave].cf[nb][lane & 15];
+      col[ct].scale[nb] = lds.q[wave].scale[nb][lane & 15];
 #pragma unroll
       for (int k = 0; k < 3; ++k) part[ct][nb][k] = read8(lds.q[wave].part[nb][k][lane & 15][lane >> 4]);
     }
@@ -487,7 +489,7 @@ int wide_splits(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_
   const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? wide_waves<1>() : wide_waves<2>());
   const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
   long long n = room / segs;
-  if (n > tiles / 8) n = tiles / 8;
+  if (n > tiles / 4) n = tiles / 4;
   return n < 1 ? 1 : n > 64 ? 64 : (int)n;
 }
 

@@ -17,15 +17,6 @@ namespace {
 // which the rows' own loads overlap.  N = 4 where that still fills the card, else 1 (8901 rows of 8
 // heads: 25.5 us a call at N = 1; MEASURED_N).
 
-// The largest of 16 lanes' numbers.
-__device__ __forceinline__ uint32_t kv4_max16(uint32_t v) {
-  const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));
-  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));
-  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));
-  return up(v, __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true));
-}
-
 template <bool BF, int N>
 __global__ __launch_bounds__(256) void kv4_append_kernel(trellis_kv4_cache c, int layer, trellis_kv4_batch b, Kv4Rows k,
                                                          Kv4Rows v, uint32_t *errword) {

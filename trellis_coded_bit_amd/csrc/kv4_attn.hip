@@ -505,7 +505,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     if (lane < 8) mine.w[4 * C * 3][lane] = 0;
   }
   Tile<NB> x;
-  QueryRaw<NB> query = load_query<NB, C>(g, c.q, c.head, c.col0);
+  QueryRaw<NB> query = load_query<NB, C>(g, c.q, c.head, column_base(g, c.col0), 0);
   const char *base = kv4_chunk(g.a.c, g.a.layer, 0, c.head);
   {
     const int t = c.t0 + wave;
@@ -541,17 +541,18 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       n.t1 = (int)min((long long)n.q.tiles, u1 - n.begin);
       first_n = wave < n.t1 && n.q.len > 0;
       if (first_n) entry_n = tile_entry(g, n.q, tile_at(n.q, wave));
-      query_n = load_query<NB, C>(g, n.q, n.head, n.col0);
+      query_n = load_query<NB, C>(g, n.q, n.head, column_base(g, n.col0), 0);
     }
     const char *base_n = kv4_chunk(g.a.c, g.a.layer, 0, n.head);
     put_query<BF, NB, C>(g, query, lds.q);
     __syncthreads();
     const int cols = (int)min((long long)C, (long long)q.n * g.group - col0);
-    const int pos0 = q.len - q.n + col0 / g.group, pos1 = q.len - q.n + (col0 + cols - 1) / g.group;
+    const ColumnBase from = column_base(g, col0);
+    const int pos0 = q.len - q.n + from.row, pos1 = q.len - q.n + column_at(g, from, cols - 1).row;
     Column<NB> column;
     {
       const int cc = lane & (C - 1);
-      column.pos = cc < cols ? q.len - q.n + (col0 + cc) / g.group : -1;
+      column.pos = cc < cols ? q.len - q.n + column_at(g, from, cc).row : -1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) column.scale[nb] = lds.q.scale[nb][cc];
     }
@@ -640,7 +641,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     if (w0 == w1) {
       if ((tid >> 4) < cols)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + col, nb, v[nb], M, L);
+        for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, column_at(g, from, col), nb, v[nb], M, L);
     } else {
       // ---- this workgroup's part, then the join by whoever arrives last
       const long long region = (long long)gridDim.x * 2 * kPart * 4;
@@ -736,7 +737,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
               for (int e = 0; e < 8; ++e) acc[nb][e] = acc[nb][e] * fa + from[nb * 8 + e] * fb;
           }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + cc, nb, acc[nb], m, l2);
+          for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, column_at(g, from, cc), nb, acc[nb], m, l2);
         }
       }
     }
@@ -812,6 +813,7 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, void *ws, hipStream_t stream) {
   g.counters = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kWsHeaderBytes);
   g.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + kWsReserved);
   g.group = a.n_q_heads / a.c.n_kv_heads;
+  g.per_group = 65536 / g.group + 1;
   for (g.page_shift = 4; (1 << g.page_shift) < a.c.page_size;) ++g.page_shift;
   g.page_stride = (uint32_t)trellis_kv4_page_bytes(a.c.page_size, a.c.n_kv_heads, a.c.head_dim);
   // Which kernels: one where every sequence is known to be its kind (that kernel then takes whatever

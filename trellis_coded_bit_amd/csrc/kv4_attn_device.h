@@ -23,6 +23,7 @@ struct AttnArgs {
   int splits;          // wide: workgroups that share a segment
   float *parts;        // [workgroups][2][C][D + 8]: unnormalised sums, then maximum, sum of weights
   int group;           // query heads per key/value head
+  uint32_t per_group;  // 65536 / group + 1: x * per_group >> 16 is x / group up to x = 255
   int page_shift;      // log2 of the page size
   uint32_t page_stride;  // bytes from page to page of a layer
 };
@@ -111,6 +112,20 @@ __device__ __forceinline__ float sum4(float v) {
 // Byte of a power of two 2^e as a matrix instruction's scale.
 __device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
 
+// A column is a row and one of the key/value head's query heads.  Columns are counted from a uniform
+// one, up to 63 on, so that only that one is divided.
+struct ColumnBase {
+  int row, head;
+};
+__device__ __forceinline__ ColumnBase column_base(const AttnArgs &g, int col0) {
+  const int row = __builtin_amdgcn_readfirstlane(col0 / g.group);
+  return {row, col0 - row * g.group};
+}
+__device__ __forceinline__ ColumnBase column_at(const AttnArgs &g, const ColumnBase &from, int i) {
+  const uint32_t x = from.head + i, r = __umul24(x, g.per_group) >> 16;
+  return {from.row + (int)r, (int)(x - __umul24(r, g.group))};
+}
+
 // C columns' rotated queries as matrix operands, in shared memory, times the softmax's scale and
 // log2 e: a product with its scales is a score in powers of two.  Lane group g of a column's
 // E4M3 operand holds elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block.
@@ -120,18 +135,18 @@ struct QueryLds {
   int scale[NB][C];  // a byte a part: its power of two as the matrix instructions take it
 };
 
-// Sixteen lanes to a column, eight elements each.
+// Sixteen lanes to a column, eight elements each: C columns from `first` after `from` on.
 template <int NB>
 struct QueryRaw {
   u32x4 x[NB];
 };
 template <int NB, int C>
-__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, int col0) {
+__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, const ColumnBase &from, int first) {
   QueryRaw<NB> r;
-  const int c = col0 + (threadIdx.x >> 4);
-  const bool ok = (int)(threadIdx.x >> 4) < C && c < (long long)q.n * g.group;
+  const ColumnBase c = column_at(g, from, first + (threadIdx.x >> 4));
+  const bool ok = (int)(threadIdx.x >> 4) < C && c.row < q.n;
   const uint16_t *p = static_cast<const uint16_t *>(g.a.q.p);
-  if (ok) p += (int64_t)(q.c0 + c / g.group) * g.a.q.row_stride + (head * g.group + c % g.group) * g.a.q.head_stride + 8 * (threadIdx.x & 15);
+  if (ok) p += (int64_t)(q.c0 + c.row) * g.a.q.row_stride + (head * g.group + c.head) * g.a.q.head_stride + 8 * (threadIdx.x & 15);
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     r.x[nb] = u32x4{0, 0, 0, 0};
@@ -142,30 +157,26 @@ __device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq 
 
 template <bool BF, int NB, int C>
 __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> &raw, QueryLds<NB, C> &lds) {
-  const int c = threadIdx.x >> 4, i = threadIdx.x & 15;
+  const int c = threadIdx.x >> 4, i = threadIdx.x & 15, k = kv4_fwht16_place(i);  // elements 8 k .. 8 k + 7
+  const float factor = g.a.scale * (kLog2e * kRsqrt128) * kv4_fwht16_sign(i);
   if (c >= C) return;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     float x[8];
     kv4_unpack8<BF>(raw.x[nb], x);
-    kv4_fwht16(x, threadIdx.x & 63);
-    float top = 0.f;
-    bool finite = true;
+    kv4_fwht16_signed(x, i);
+    // the largest magnitude as an integer: infinity is above every number, a NaN above infinity
+    uint32_t top = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      x[t] *= g.a.scale * (kLog2e * kRsqrt128);
-      top = fmaxf(top, fabsf(x[t]));
-      finite &= fabsf(x[t]) <= 3.4028234e38f;
+      x[t] *= factor;
+      const uint32_t w = __builtin_bit_cast(uint32_t, x[t]) & 0x7FFFFFFFu;
+      top = w > top ? w : top;
     }
-    top = finite ? top : __builtin_inff();
-    top = fmaxf(top, lane_xor<1>(top));
-    top = fmaxf(top, lane_xor<2>(top));
-    top = fmaxf(top, lane_xor<4>(top));
-    top = fmaxf(top, lane_xor<8>(top));
+    top = kv4_max16(top);
     // the largest element comes to [128, 256); a column that is not finite becomes NaN
-    const int e = max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 16);
-    float f = __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);
-    if (top > 3.4028234e38f) f = __builtin_nanf("");
+    const int e = max((int)(top >> 23), 16);
+    const float f = top >= 0x7F800000u ? __builtin_nanf("") : __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);
     if (i == 0) lds.scale[nb][c] = (e - 7) | (e - 11) << 8 | (e - 15) << 16;
 #pragma unroll
     for (int t = 0; t < 8; ++t) x[t] *= f;
@@ -184,7 +195,7 @@ __device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> 
         x[4 * w + 2] = (x[4 * w + 2] - b[0]) * 16.f;
         x[4 * w + 3] = (x[4 * w + 3] - b[1]) * 16.f;
       }
-      *reinterpret_cast<v2i *>(&lds.part[nb][s][c][(i & 7) >> 1][(i >> 3) * 4 + (i & 1) * 2]) = o;
+      *reinterpret_cast<v2i *>(&lds.part[nb][s][c][(k & 7) >> 1][(k >> 3) * 4 + (k & 1) * 2]) = o;
     }
   }
 }
@@ -218,18 +229,18 @@ __device__ __forceinline__ void clear_rest(const AttnArgs &g) {
 // Writes one column block's result: 16 lanes, eight elements each, still rotated and not
 // normalised.
 template <bool BF>
-__device__ __forceinline__ void write_block(const AttnArgs &g, const Seq &q, int head, int c, int nb, float (&v)[8], float m,
-                                            float l) {
+__device__ __forceinline__ void write_block(const AttnArgs &g, const Seq &q, int head, const ColumnBase &c, int nb, float (&v)[8],
+                                            float m, float l) {
   const int i = threadIdx.x & 15;
-  kv4_fwht16(v, threadIdx.x & 63);
-  const float f = l == 0.f ? 0.f : kRsqrt128 / l;  // (nothing seen: zero)
+  kv4_fwht16_signed(v, i);
+  const float f = l == 0.f ? 0.f : kv4_fwht16_sign(i) * kRsqrt128 / l;  // (nothing seen: zero)
 #pragma unroll
   for (int t = 0; t < 8; ++t) v[t] *= f;
   if (l == 0.f)
 #pragma unroll
     for (int t = 0; t < 8; ++t) v[t] = 0.f;
-  const size_t at = (size_t)(q.c0 + c / g.group) * g.a.n_q_heads + head * g.group + c % g.group;
-  uint16_t *y = static_cast<uint16_t *>(g.a.y) + at * g.a.c.head_dim + nb * 128 + 8 * i;
+  const size_t at = (size_t)(q.c0 + c.row) * g.a.n_q_heads + head * g.group + c.head;
+  uint16_t *y = static_cast<uint16_t *>(g.a.y) + at * g.a.c.head_dim + nb * 128 + 8 * kv4_fwht16_place(i);
   *reinterpret_cast<u32x4 *>(y) = kv4_pack8<BF>(v);
   if (g.a.lse && nb == 0 && i == 0) g.a.lse[at] = l == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }

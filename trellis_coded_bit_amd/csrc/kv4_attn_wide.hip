@@ -301,7 +301,8 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   if (s < 0) return;
   const int col0 = (q.col_tiles - 1 - item) * kWideCols;
   const int cols = (int)min((long long)kWideCols, (long long)q.n * g.group - col0);
-  const int p0 = q.len - q.n + col0 / g.group, p1 = q.len - q.n + (col0 + cols - 1) / g.group;  // positions
+  const ColumnBase from = column_base(g, col0);
+  const int p0 = q.len - q.n + from.row, p1 = q.len - q.n + column_at(g, from, cols - 1).row;  // positions
   // the key tiles of these rows
   q.lo = g.a.window ? max(p0 - g.a.window + 1, 0) : 0;
   q.first = q.lo / kTile;
@@ -320,14 +321,14 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   for (int ct = 0; ct < CT; ++ct) {
     QueryRaw<NB> r[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) r[w] = load_query<NB, kCols>(g, q, head, col0 + (w * CT + ct) * kCols);
+    for (int w = 0; w < 4; ++w) r[w] = load_query<NB, kCols>(g, q, head, from, (w * CT + ct) * kCols);
     if (ct == 0 && t0 < t1) load_share(g, q.lo, base, tile_at(q, t0), entry, x);
     if (ct) __syncthreads();
 #pragma unroll
     for (int w = 0; w < 4; ++w) put_query<BF, NB, kCols>(g, r[w], lds.q[w]);
     __syncthreads();
-    const int c = col0 + (wave * CT + ct) * kCols + (lane & 15);
-    col[ct].pos = c < col0 + cols ? q.len - q.n + c / g.group : -1;
+    const int c = (wave * CT + ct) * kCols + (lane & 15);
+    col[ct].pos = c < cols ? q.len - q.n + column_at(g, from, c).row : -1;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       col[ct].scale[nb] = lds.q[wave].scale[nb][lane & 15];
@@ -354,8 +355,8 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     put_share(g, q, tile_at(q, t0), x, lds.t, 0);
     if (t0 + 1 < t1) load_share(g, q.lo, base, tile_at(q, t0 + 1), entry2, x);
   }
-  const int wp0 = q.len - q.n + min(col0 + wave * CT * kCols, col0 + cols - 1) / g.group;
-  const int wp1 = q.len - q.n + min(col0 + (wave + 1) * CT * kCols, col0 + cols) / g.group;  // (one more at most)
+  const int wp0 = q.len - q.n + column_at(g, from, min(wave * CT * kCols, cols - 1)).row;
+  const int wp1 = q.len - q.n + column_at(g, from, min((wave + 1) * CT * kCols, cols)).row;  // (one more at most)
   const bool idle = wave * CT * kCols >= cols;  // no column of this wave's
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1, tile = tile_at(q, t), k0 = tile * kTile;
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
         const floatx4 b = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i + 4]);
         float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         if (g.splits == 1) {
-          write_block<BF>(g, q, head, col0 + at, nb, v, mm, ll);
+          write_block<BF>(g, q, head, column_at(g, from, at), nb, v, mm, ll);
         } else {
           const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)(blockIdx.x / g.splits) * g.splits * kWideCols * (D + 8),
                                                         (long long)g.splits * kWideCols * (D + 8) * 4);
@@ -474,7 +475,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
       }
     }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, col0 + c, nb, acc[nb], mm, ll);
+    for (int nb = 0; nb < NB; ++nb) write_block<BF>(g, q, head, column_at(g, from, c), nb, acc[nb], mm, ll);
   }
 }
 

@@ -89,32 +89,9 @@ __device__ __forceinline__ Kv4Kind kv4_kind(const trellis_kv4_cache &c, int n) {
   return {k >> log_nb, k & log_nb, is_v};
 }
 
-// H_128 (unnormalised) over 16 lanes holding elements 8i .. 8i+7, strides 1, 2, 4 .. 64 in
-// ascending order.
-__device__ __forceinline__ void kv4_fwht16(float (&v)[8], int lane) {
-#pragma unroll
-  for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if ((t & h) == 0) {
-        const float a = v[t], b = v[t + h];
-        v[t] = a + b;
-        v[t + h] = a - b;
-      }
-  const float sg1 = (lane & 1) ? -1.f : 1.f, sg2 = (lane & 2) ? -1.f : 1.f;
-  const float sg4 = (lane & 4) ? -1.f : 1.f, sg8 = (lane & 8) ? -1.f : 1.f;
-#pragma unroll
-  for (int t = 0; t < 8; ++t) v[t] = lane_xor<1>(v[t]) + sg1 * v[t];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) v[t] = lane_xor<2>(v[t]) + sg2 * v[t];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) v[t] = lane_xor<4>(v[t]) + sg4 * v[t];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) v[t] = lane_xor<8>(v[t]) + sg8 * v[t];
-}
-
-// The same, up to a sign a lane and the order of the lanes, in one instruction an element and
-// stage across lanes: v + c v', with v' the partner's and c = -1 in a pair's second lane, is the
+// H_128 (unnormalised) over 16 lanes holding elements 8i .. 8i+7, strides 1, 2, 4 .. 64, up to a
+// sign a lane and the order of the lanes, in one instruction an element and stage across lanes:
+// v + c v', with v' the partner's and c = -1 in a pair's second lane, is the
 // butterfly with that lane's result negated, and all of a later stage's partners carry the same
 // negations.  The third stage pairs i with 7 - i, which one lane pattern reaches and i ^ 4 does
 // not; H_8 over the masks 1, 2, 7 is H_8 over 1, 2, 4 with its outputs in another order.  Lane i
@@ -152,6 +129,15 @@ __device__ __forceinline__ void kv4_fwht16_signed(float (&v)[8], int i) {
 #undef KV4_STAGE
       : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])
       : "v"(c1), "v"(c2), "v"(c7), "v"(c8));
+}
+
+// The largest of 16 lanes' numbers.
+__device__ __forceinline__ uint32_t kv4_max16(uint32_t v) {
+  const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));
+  v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));
+  return up(v, __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true));
 }
 
 template <bool BF>

@@ -131,23 +131,53 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
           float y[8][4];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            float ks[32];
-            read_scales32(lds.ks[buf][nb], ks);
+            // Products j = 2 p, 2 p + 1 together.  The order is kept as written: the next two's keys are
+            // on their way during the products, and two chains of three products alternate; left to
+            // itself the compiler waits for every load and every product.
             const int row = lane & 15, sub = row >> 1;
             const char *kp = lds.k[buf][nb] + sub * 1024;
+            const float *sp = lds.ks[buf][nb] + (lane >> 4) * 32;
+            v4i kv[2][2];
+            floatx4 s4[2][2], z[2][2];
+            const auto load = [&](int p) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int c = (8 * (j & 1) + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
-              const v4i kv = *reinterpret_cast<const v4i *>(kp + (j >> 1) * 256 + c * 16);
-              const v8i a = {kv[0], kv[1], kv[2], kv[3], 0, 0, 0, 0};
-              floatx4 z = {0.f, 0.f, 0.f, 0.f};
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][0], z, 4, 0, 0, scale_byte(0), 0, col[ct].scale[nb]);
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][1], z, 4, 0, 0, scale_byte(0), 1, col[ct].scale[nb]);
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[ct][nb][2], z, 4, 0, 0, scale_byte(0), 2, col[ct].scale[nb]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                y[j][i] = fmaf(z[i], ks[key32(j, i)], nb ? y[j][i] : c0);
+              for (int h = 0; h < 2; ++h) {
+                const int c = (8 * h + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
+                kv[p & 1][h] = *reinterpret_cast<const v4i *>(kp + p * 256 + c * 16);
               }
+            };
+            load(0);
+#pragma unroll
+            for (int p = 0; p < 5; ++p) {
+              const int at = p & 1;
+              if (p < 4) {
+                if (p < 3) load(p + 1);
+                // keys 4 p .. + 3 and 16 + 4 p .. + 3 of the lane's
+                s4[at][0] = *reinterpret_cast<const floatx4 *>(sp + 4 * p);
+                s4[at][1] = *reinterpret_cast<const floatx4 *>(sp + 16 + 4 * p);
+                __builtin_amdgcn_sched_barrier(0);
+                const v8i a0 = {kv[at][0][0], kv[at][0][1], kv[at][0][2], kv[at][0][3], 0, 0, 0, 0};
+                const v8i a1 = {kv[at][1][0], kv[at][1][1], kv[at][1][2], kv[at][1][3], 0, 0, 0, 0};
+                const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+                const int scale = col[ct].scale[nb];
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][0], zero, 4, 0, 0, scale_byte(0), 0, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][0], zero, 4, 0, 0, scale_byte(0), 0, scale);
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][1], z[at][0], 4, 0, 0, scale_byte(0), 1, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][1], z[at][1], 4, 0, 0, scale_byte(0), 1, scale);
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][2], z[at][0], 4, 0, 0, scale_byte(0), 2, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][2], z[at][1], 4, 0, 0, scale_byte(0), 2, scale);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+              if (p > 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    float &to = y[2 * (p - 1) + h][i];
+                    to = fmaf(z[at ^ 1][h][i], s4[at ^ 1][i >> 1][2 * h + (i & 1)], nb ? to : c0);
+                  }
+              }
+              __builtin_amdgcn_sched_barrier(0);
             }
           }
           // ---- softmax
@@ -236,23 +266,41 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
           const int row = lane & 15, sub = 2 * (lane >> 4);
           const char *vp = lds.v[buf][nb] + sub * 1024 + row * 64;
           typedef __attribute__((address_space(3))) v2i lds_v2i;
+          // Elements' tiles dt = 2 p, 2 p + 1 together, and the next word's codes turned to fp16 during
+          // a word's products.
+          v2i codes[2][2][2];
+          const auto load = [&](int p) {
 #pragma unroll
-          for (int dt = 0; dt < 8; ++dt) {
-            const char *at = vp + (((dt >> 1) ^ (row >> 2)) * 16) + (((dt & 1) ^ ((lane >> 4) & 1)) * 8);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const v2i codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + h * 1024));
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t c = codes[k];
-                const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
-                const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
-                const half8 a = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                  o[ct][nb][dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[ct][nb][2 * h + k], o[ct][nb][dt], 0, 0, 0);
-              }
+            for (int d = 0; d < 2; ++d) {
+              const char *at = vp + ((p ^ (row >> 2)) * 16) + ((d ^ ((lane >> 4) & 1)) * 8);
+              codes[p & 1][d][0] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)at);
+              codes[p & 1][d][1] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + 1024));
             }
+          };
+          half8 a[2][2];
+          const auto unpack = [&](int step) {  // word step & 3 of pair step >> 2
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const uint32_t c = codes[(step >> 2) & 1][d][(step >> 1) & 1][step & 1];
+              const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
+              const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
+              a[step & 1][d] = half8{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+            }
+          };
+          load(0);
+          unpack(0);
+#pragma unroll
+          for (int step = 0; step < 16; ++step) {
+            const int p = step >> 2;
+            if ((step & 3) == 0 && p < 3) load(p + 1);
+            if (step < 15) unpack(step + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct)
+                o[ct][nb][2 * p + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[step & 1][d], w[ct][nb][step & 3], o[ct][nb][2 * p + d], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
 }

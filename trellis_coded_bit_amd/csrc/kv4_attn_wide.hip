@@ -34,60 +34,62 @@ union WideLds {
   int last;
 };
 
-// A thread's share of a tile on its way to shared memory: 32 lanes have a subtile, 16 bytes twice.
-template <int NB>
+// A tile's way to shared memory: each wave copies two of its eight subtiles of 16 tokens, 1024
+// contiguous bytes of keys and of values for each block, with copies that pass by the registers.
+// The scales go through registers, where those of keys that no row sees become zero: half a
+// wave has a subtile's, two tokens a lane.
 struct Share {
-  v4i k[NB][2], v[NB][2];
-  uint32_t s;  // two tokens' scales: lanes 0..7 of a subtile key scales, 8..15 value scales (16..31: block 1)
+  uint32_t s;  // lanes 0..7 of a subtile key scales, 8..15 value scales (16..31: block 1)
   int page;
 };
 
+constexpr int kNoPage = -0x7FFFFFFF - 1;  // past the length
 __device__ __forceinline__ int share_entry(const AttnArgs &g, const Seq &q, int tile) {
   const int tok = tile * kTile + 16 * (threadIdx.x >> 5);
-  int e = -0x7FFFFFFF - 1;
+  int e = kNoPage;
   if (tok < q.len) e = ldg(g.a.b.table + (size_t)q.slot * g.a.b.max_pages + (tok >> g.page_shift));
   return e;
 }
 
-template <int NB>
-__device__ __forceinline__ void load_share(const AttnArgs &g, int lo, const char *base, int tile, int entry, Share<NB> &x) {
-  const int T = g.a.c.page_size, i = threadIdx.x & 31;
-  const int tok = tile * kTile + 16 * (threadIdx.x >> 5), at = tok & (T - 1);
-  x.page = (uint32_t)entry < (uint32_t)g.a.c.n_pages ? entry : -1;
-  if (x.page < 0 && entry != -0x7FFFFFFF - 1 && (tok + 15 >= lo || tok < g.a.sinks))
-    kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
-  const char *chunk = base + (uint64_t)(uint32_t)max(x.page, 0) * g.page_stride;
-  const char *p = chunk + at * 64 + i * 16;
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x.k[nb][h] = ldg(reinterpret_cast<const v4i *>(p + nb * T * 64 + h * 512));
-      x.v[nb][h] = ldg(reinterpret_cast<const v4i *>(p + (NB + nb) * T * 64 + h * 512));
-    }
-  x.s = 0;
-  const int nb = i >> 4, kind = (i >> 3) & 1;
-  if (nb < NB) x.s = ldg(reinterpret_cast<const uint32_t *>(chunk + 128 * NB * T + ((kind * NB + nb) * T + at + 2 * (i & 7)) * 2));
-}
-
 // The 16-byte parts of a tile in shared memory are permuted so that the products' reads spread over
 // the banks: key parts by their subtile (a product reads two tokens of each subtile), value parts by
-// bits 2 and 3 of their token, and a part's halves by the subtile's pair.
+// bits 2 and 3 of their token.
 __device__ __forceinline__ int key_swizzle(int subtile) { return (subtile & 3) | ((subtile & 4) << 1); }
 
+// (A subtile without a page copies page 0's, whose scales become zero.)  The copies are not waited
+// for by anything but an explicit wait.
 template <int NB>
-__device__ __forceinline__ void put_share(const AttnArgs &g, const Seq &q, int tile, const Share<NB> &x, WideTiles<NB> &lds, int buf) {
-  const int s = threadIdx.x >> 5, i = threadIdx.x & 31;
-  const bool swap = (s >> 1) & 1;
+__device__ __forceinline__ void load_share(const AttnArgs &g, int lo, const char *base, int tile, int entry, WideTiles<NB> &lds, int buf,
+                                           Share &x) {
+  const int T = g.a.c.page_size, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  {
+    const int tok = tile * kTile + 16 * (threadIdx.x >> 5), i = threadIdx.x & 31;
+    x.page = (uint32_t)entry < (uint32_t)g.a.c.n_pages ? entry : -1;
+    if (x.page < 0 && entry != kNoPage && (tok + 15 >= lo || tok < g.a.sinks)) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
+    const char *chunk = base + (uint64_t)(uint32_t)max(x.page, 0) * g.page_stride;
+    x.s = 0;
+    const int nb = i >> 4, kind = (i >> 3) & 1, at = tok & (T - 1);
+    if (nb < NB) x.s = ldg(reinterpret_cast<const uint32_t *>(chunk + 128 * NB * T + ((kind * NB + nb) * T + at + 2 * (i & 7)) * 2));
+  }
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+  for (int h = 0; h < 2; ++h) {
+    const int sub = 2 * wave + h, at = (tile * kTile + 16 * sub) & (T - 1);
+    const int page = max(__builtin_amdgcn_readlane(x.page, 32 * h), 0);
+    const char *p = base + (uint64_t)(uint32_t)page * g.page_stride + at * 64;
+    typedef __attribute__((address_space(1))) const void gbl_void;
+    typedef __attribute__((address_space(3))) void lds_void;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = h * 32 + i;  // part c & 3 of token c >> 2
-      *reinterpret_cast<v4i *>(lds.k[buf][nb] + s * 1024 + (c ^ key_swizzle(s)) * 16) = x.k[nb][h];
-      const v4i v = x.v[nb][h];
-      *reinterpret_cast<v4i *>(lds.v[buf][nb] + s * 1024 + (c ^ ((c >> 4) & 3)) * 16) = swap ? v4i{v[2], v[3], v[0], v[1]} : v;
+    for (int nb = 0; nb < NB; ++nb) {
+      const char *k = p + nb * T * 64 + (lane ^ key_swizzle(sub)) * 16, *v = p + (NB + nb) * T * 64 + (lane ^ ((lane >> 4) & 3)) * 16;
+      __builtin_amdgcn_global_load_lds((gbl_void *)k, (lds_void *)(lds.k[buf][nb] + sub * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((gbl_void *)v, (lds_void *)(lds.v[buf][nb] + sub * 1024), 16, 0, 0);
     }
+  }
+}
+
+template <int NB>
+__device__ __forceinline__ void put_share(const AttnArgs &g, const Seq &q, int tile, const Share &x, WideTiles<NB> &lds, int buf) {
+  const int s = threadIdx.x >> 5, i = threadIdx.x & 31;
   const int nb = i >> 4, kind = (i >> 3) & 1, at = 16 * s + 2 * (i & 7), tok = tile * kTile + at;
   if (nb < NB) {
     const bool here = x.page >= 0;
@@ -272,7 +274,7 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
           const auto load = [&](int p) {
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              const char *at = vp + ((p ^ (row >> 2)) * 16) + ((d ^ ((lane >> 4) & 1)) * 8);
+              const char *at = vp + ((p ^ (row >> 2)) * 16) + d * 8;
               codes[p & 1][d][0] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)at);
               codes[p & 1][d][1] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + 1024));
             }
@@ -359,10 +361,9 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   const int t0 = (int)((long long)q.tiles * split / g.splits), t1 = (int)((long long)q.tiles * (split + 1) / g.splits);
   const char *base = kv4_chunk(g.a.c, g.a.layer, 0, head);
   // ---- queries: four column tiles at a time, then each wave takes its own into registers
-  Share<NB> x;
-  int entry = 0, entry2 = 0;
+  Share x;
+  int entry = 0;
   if (t0 < t1) entry = share_entry(g, q, tile_at(q, t0));
-  if (t0 + 1 < t1) entry2 = share_entry(g, q, tile_at(q, t0 + 1));
   v8i part[CT][NB][3];
   Column<NB> col[CT];
 #pragma unroll
@@ -370,7 +371,6 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     QueryRaw<NB> r[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) r[w] = load_query<NB, kCols>(g, q, head, from, (w * CT + ct) * kCols);
-    if (ct == 0 && t0 < t1) load_share(g, q.lo, base, tile_at(q, t0), entry, x);
     if (ct) __syncthreads();
 #pragma unroll
     for (int w = 0; w < 4; ++w) put_query<BF, NB, kCols>(g, r[w], lds.q[w]);
@@ -399,17 +399,18 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) e_run[nb] = 127;
-  if (t0 < t1) {
-    put_share(g, q, tile_at(q, t0), x, lds.t, 0);
-    if (t0 + 1 < t1) load_share(g, q.lo, base, tile_at(q, t0 + 1), entry2, x);
-  }
+  if (t0 < t1) load_share(g, q.lo, base, tile_at(q, t0), entry, lds.t, 0, x);
+  if (t0 + 1 < t1) entry = share_entry(g, q, tile_at(q, t0 + 1));
   const int wp0 = q.len - q.n + column_at(g, from, min(wave * CT * kCols, cols - 1)).row;
   const int wp1 = q.len - q.n + column_at(g, from, min((wave + 1) * CT * kCols, cols)).row;  // (one more at most)
   const bool idle = wave * CT * kCols >= cols;  // no column of this wave's
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1, tile = tile_at(q, t), k0 = tile * kTile;
+    put_share(g, q, tile, x, lds.t, buf);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies have arrived
+    __syncthreads();                     // this tile is complete, and the one before it is read
+    if (t + 1 < t1) load_share(g, q.lo, base, tile_at(q, t + 1), entry, lds.t, buf ^ 1, x);
     if (t + 2 < t1) entry = share_entry(g, q, tile_at(q, t + 2));
-    __syncthreads();  // this tile is complete, and the one before it is read
     if (!idle && k0 <= wp1) {
       const uint32_t bad = (uint32_t)__ballot(lane < 8 && lds.t.bad[buf][lane & 7]);
       const bool mask = !(k0 + kTile - 1 <= wp0 && bad == 0 &&
@@ -441,8 +442,6 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
       }
       wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, part, col, f, keep, e_run, m, l, o);
     }
-    if (t + 1 < t1) put_share(g, q, tile_at(q, t + 1), x, lds.t, buf ^ 1);
-    if (t + 2 < t1) load_share(g, q.lo, base, tile_at(q, t + 2), entry, x);
   }
   // ---- results: back to the values' units, through shared memory, 16 lanes a column
 #pragma unroll

@@ -505,7 +505,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     if (lane < 8) mine.w[4 * C * 3][lane] = 0;
   }
   Tile<NB> x;
-  QueryRaw<NB> query = load_query<NB, C>(g, c.q, c.head, column_base(g, c.col0), 0);
+  QueryRaw<NB> query = load_query<NB>(g, c.q, c.head, column_base(g, c.col0), tid >> 4);
   const char *base = kv4_chunk(g.a.c, g.a.layer, 0, c.head);
   {
     const int t = c.t0 + wave;
@@ -541,7 +541,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       n.t1 = (int)min((long long)n.q.tiles, u1 - n.begin);
       first_n = wave < n.t1 && n.q.len > 0;
       if (first_n) entry_n = tile_entry(g, n.q, tile_at(n.q, wave));
-      query_n = load_query<NB, C>(g, n.q, n.head, column_base(g, n.col0), 0);
+      query_n = load_query<NB>(g, n.q, n.head, column_base(g, n.col0), tid >> 4);
     }
     const char *base_n = kv4_chunk(g.a.c, g.a.layer, 0, n.head);
     put_query<BF, NB, C>(g, query, lds.q);

@@ -109,6 +109,14 @@ __device__ __forceinline__ float sum4(float v) {
   return a + b;
 }
 
+__device__ __forceinline__ uint32_t max4u(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t x = a[0], y = a[1], w = x > y ? x : y;
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const uint32_t s = b[0], t = b[1];
+  return s > t ? s : t;
+}
+
 // Byte of a power of two 2^e as a matrix instruction's scale.
 __device__ __forceinline__ constexpr int scale_byte(int e) { return 127 + e; }
 
@@ -135,16 +143,16 @@ struct QueryLds {
   int scale[NB][C];  // a byte a part: its power of two as the matrix instructions take it
 };
 
-// Sixteen lanes to a column, eight elements each: C columns from `first` after `from` on.
+// Sixteen lanes to a column (the `col`-th from `from` on), eight elements each.
 template <int NB>
 struct QueryRaw {
   u32x4 x[NB];
 };
-template <int NB, int C>
-__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, const ColumnBase &from, int first) {
+template <int NB>
+__device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq &q, int head, const ColumnBase &from, int col) {
   QueryRaw<NB> r;
-  const ColumnBase c = column_at(g, from, first + (threadIdx.x >> 4));
-  const bool ok = (int)(threadIdx.x >> 4) < C && c.row < q.n;
+  const ColumnBase c = column_at(g, from, col);
+  const bool ok = c.row < q.n;
   const uint16_t *p = static_cast<const uint16_t *>(g.a.q.p);
   if (ok) p += (int64_t)(q.c0 + c.row) * g.a.q.row_stride + (head * g.group + c.head) * g.a.q.head_stride + 8 * (threadIdx.x & 15);
 #pragma unroll

@@ -29,8 +29,7 @@ struct WideTiles {
 template <int NB>
 union WideLds {
   WideTiles<NB> t;
-  QueryLds<NB, kCols> q[4];           // before the tiles: one column tile a wave
-  float o[4][NB][kCols][kRowF];       // after them
+  float o[4][NB][kCols][kRowF];       // before the tiles queries, after them sums: one column tile a wave
   int last;
 };
 
@@ -115,11 +114,81 @@ __device__ __forceinline__ void read_scales32(const float *s, float (&w)[32]) {
 // Key (j, i) of the products' results is key 16 (i >> 1) + 2 j + (i & 1) of the lane's.
 __device__ __forceinline__ constexpr int key32(int j, int i) { return 16 * (i >> 1) + 2 * j + (i & 1); }
 
+// A wave's 16 columns as matrix operands.  Lane (n, g) has elements 32 g .. 32 g + 31 of column n as
+// three E2M3 parts.
+template <int NB>
+struct Query {
+  v8i part[NB][3];  // (six registers each)
+  int scale[NB];    // a byte a part: its power of two
+  float add;        // NaN where the column is not finite: no E2M3 number says so
+};
+
+// Rotates the wave's columns, 16 lanes a column, into shared memory, four columns a step; even elements
+// of each 32 first, as the conversion takes them.
+template <bool BF, int NB>
+__device__ __forceinline__ void stage_query(const AttnArgs &g, const QueryRaw<NB> &raw, int step, float (&to)[NB][kCols][kRowF]) {
+  const int c = 4 * step + ((threadIdx.x & 63) >> 4), i = threadIdx.x & 15, k = kv4_fwht16_place(i);
+  const float factor = g.a.scale * (kLog2e * kRsqrt128) * kv4_fwht16_sign(i);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float x[8];
+    kv4_unpack8<BF>(raw.x[nb], x);
+    kv4_fwht16_signed(x, i);
+    float *at = to[nb][c] + 32 * (k >> 2) + 4 * (k & 3);
+    *reinterpret_cast<floatx4 *>(at) = floatx4{x[0], x[2], x[4], x[6]} * factor;
+    *reinterpret_cast<floatx4 *>(at + 16) = floatx4{x[1], x[3], x[5], x[7]} * factor;
+  }
+}
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx32 __attribute__((ext_vector_type(32)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+
+template <int NB>
+__device__ __forceinline__ void take_query(const float (&from)[NB][kCols][kRowF], Query<NB> &q) {
+  const int lane = threadIdx.x & 63;
+  q.add = 0.f;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const floatx4 *p = reinterpret_cast<const floatx4 *>(from[nb][lane & 15] + 32 * (lane >> 4));
+    floatx16 x[2];  // elements 2 j, 2 j + 1
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const floatx4 v = p[t];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = v[e];
+        x[t >> 2][4 * (t & 3) + e] = w;
+        const uint32_t u = __builtin_bit_cast(uint32_t, w) & 0x7FFFFFFFu;
+        top = u > top ? u : top;
+      }
+    }
+    top = max4u(top);
+    if (top >= 0x7F800000u) q.add = __builtin_nanf("");
+    // The largest comes to [3.75, 7.5), so nothing saturates; what a part leaves is at most 0.25, then
+    // 0.125, in its units: the next one's are 16, then 32 times smaller.
+    const int e = max((int)((top + 0x00100000u) >> 23), 24);
+    q.scale[nb] = (e - 2) | (e - 6) << 8 | (e - 11) << 16;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      const float unit = __builtin_bit_cast(float, (uint32_t)(e - (s == 0 ? 2 : s == 1 ? 6 : 11)) << 23);
+      const u32x6 w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x[0], x[1], unit);
+      q.part[nb][s] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], 0, 0};
+      if (s < 2) {
+        const floatx32 back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, unit);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[0][j] -= back[2 * j], x[1][j] -= back[2 * j + 1];
+      }
+    }
+  }
+}
+
 // One tile into a wave's sums.  mask: some row does not see some key; bad: subtiles without a page;
 // odd: some value scale is not finite.
 template <int NB>
 __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB> &lds, int buf, int k0, bool mask, uint32_t bad, bool odd,
-                                          const v8i (&part)[kColTiles][NB][3], const Column<NB> (&col)[kColTiles],
+                                          const Query<NB> (&query)[kColTiles], const int (&pos)[kColTiles],
                                           const float (&f)[NB], const float (&keep)[NB], const int (&e_run)[NB], float (&m)[kColTiles],
                                           float (&l)[kColTiles], floatx4 (&o)[kColTiles][NB][8]) {
   constexpr int CT = kColTiles;
@@ -129,7 +198,7 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           // ---- scores, from the running maximum (or from 0) as the weights' powers of two
-          const float mu = m[ct] == kNegInf ? 0.f : m[ct], c0 = log2f - mu;
+          const float mu = m[ct] == kNegInf ? 0.f : m[ct], c0 = log2f - mu + query[ct].add;
           float y[8][4];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -161,13 +230,13 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
                 const v8i a0 = {kv[at][0][0], kv[at][0][1], kv[at][0][2], kv[at][0][3], 0, 0, 0, 0};
                 const v8i a1 = {kv[at][1][0], kv[at][1][1], kv[at][1][2], kv[at][1][3], 0, 0, 0, 0};
                 const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-                const int scale = col[ct].scale[nb];
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][0], zero, 4, 0, 0, scale_byte(0), 0, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][0], zero, 4, 0, 0, scale_byte(0), 0, scale);
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][1], z[at][0], 4, 0, 0, scale_byte(0), 1, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][1], z[at][1], 4, 0, 0, scale_byte(0), 1, scale);
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, part[ct][nb][2], z[at][0], 4, 0, 0, scale_byte(0), 2, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, part[ct][nb][2], z[at][1], 4, 0, 0, scale_byte(0), 2, scale);
+                const int scale = query[ct].scale[nb];
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][1], z[at][0], 4, 2, 0, scale_byte(0), 1, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][1], z[at][1], 4, 2, 0, scale_byte(0), 1, scale);
+                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][2], z[at][0], 4, 2, 0, scale_byte(0), 2, scale);
+                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][2], z[at][1], 4, 2, 0, scale_byte(0), 2, scale);
                 __builtin_amdgcn_sched_barrier(0);
               }
               if (p > 0) {
@@ -185,7 +254,7 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
           // ---- softmax
           if (mask) {
       asm volatile("");  // (a branch, not 32 selects on every tile)
-      const int kk = k0 + 32 * (lane >> 4), rel = col[ct].pos - kk;
+      const int kk = k0 + 32 * (lane >> 4), rel = pos[ct] - kk;
       const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
       const uint32_t gone = bad >> (2 * (lane >> 4));
 #pragma unroll
@@ -308,7 +377,7 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
 }
 
 template <int NB>
-constexpr int wide_waves() { return NB == 1 ? 3 : 1; }  // a SIMD
+constexpr int wide_waves() { return NB == 1 ? 3 : 2; }  // a SIMD
 
 template <bool BF, int NB>
 __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wide_kernel(AttnArgs g) {
@@ -360,29 +429,24 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   q.tiles = max(q.n_sink + (min(max(p1 + 1, 0), q.len) + kTile - 1) / kTile - q.first, 0);
   const int t0 = (int)((long long)q.tiles * split / g.splits), t1 = (int)((long long)q.tiles * (split + 1) / g.splits);
   const char *base = kv4_chunk(g.a.c, g.a.layer, 0, head);
-  // ---- queries: four column tiles at a time, then each wave takes its own into registers
+  // ---- queries
   Share x;
   int entry = 0;
   if (t0 < t1) entry = share_entry(g, q, tile_at(q, t0));
-  v8i part[CT][NB][3];
-  Column<NB> col[CT];
+  Query<NB> query[CT];
+  int pos[CT];  // of the lane's column, -1: it sees nothing
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
+    const int c0 = (wave * CT + ct) * kCols, c = c0 + (lane & 15);
     QueryRaw<NB> r[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) r[w] = load_query<NB, kCols>(g, q, head, from, (w * CT + ct) * kCols);
-    if (ct) __syncthreads();
+    for (int k = 0; k < 4; ++k) r[k] = load_query<NB>(g, q, head, from, c0 + 4 * k + (lane >> 4));
 #pragma unroll
-    for (int w = 0; w < 4; ++w) put_query<BF, NB, kCols>(g, r[w], lds.q[w]);
-    __syncthreads();
-    const int c = (wave * CT + ct) * kCols + (lane & 15);
-    col[ct].pos = c < cols ? q.len - q.n + column_at(g, from, c).row : -1;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      col[ct].scale[nb] = lds.q[wave].scale[nb][lane & 15];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) part[ct][nb][k] = read8(lds.q[wave].part[nb][k][lane & 15][lane >> 4]);
-    }
+    for (int k = 0; k < 4; ++k) stage_query<BF, NB>(g, r[k], k, lds.o[wave]);
+    __builtin_amdgcn_wave_barrier();
+    take_query<NB>(lds.o[wave], query[ct]);
+    __builtin_amdgcn_wave_barrier();
+    pos[ct] = c < cols ? q.len - q.n + column_at(g, from, c).row : -1;
   }
   __syncthreads();
   floatx4 o[CT][NB][8];
@@ -394,7 +458,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    m[ct] = col[ct].pos < 0 ? 0.f : kNegInf;  // (a column past the last never sees a score)
+    m[ct] = pos[ct] < 0 ? 0.f : kNegInf;  // (a column past the last never sees a score)
     l[ct] = 0.f;
   }
 #pragma unroll
@@ -440,7 +504,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
         }
         f[nb] = __builtin_bit_cast(float, (uint32_t)(261 - e_run[nb]) << 23);
       }
-      wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, part, col, f, keep, e_run, m, l, o);
+      wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, query, pos, f, keep, e_run, m, l, o);
     }
   }
   // ---- results: back to the values' units, through shared memory, 16 lanes a column

@@ -16,7 +16,8 @@ Every timed leg runs at least 50 ms of the same untimed work first (the GPU's cl
 exactly K timed steps; the line's "clock_ramp" says how much ramp work each leg ran.
 
 Prints ONE JSON line (rank 0, N = 1).  --workload selects the other lines (the encoder,
-the standalone entry points, the microbenchmarks) or one of the above alone.
+the standalone entry points, the microbenchmarks, a serving loop over the paged 4-bit
+key/value cache) or one of the above alone.
 """
 from __future__ import annotations
 
@@ -675,13 +676,160 @@ def run_micro(args, torch, tb):
     return out
 
 
+def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, samples=8, page=64, window=0, sinks=0,
+              keep_first=4, keep_last=1020):
+    """A serving program's attention layers end to end: the small-batch workload's qkv (5120 ->
+    48 query, 16 key and 16 value heads of 128) and out products around the paged 4-bit cache.
+    A prompt enters in chunks (trellis_gemm, append, attention), is forked into `samples`
+    sequences that share its pages, these decode one token a step in a HIP graph (reserve, then
+    per layer trellis_gemv, append, attention, trellis_gemv), are cut to their first and last
+    tokens by a compaction, decode on, and are freed.  The last prompt chunk's and the last
+    decoded token's attention of layer 0 are checked against fp32 attention over what the cache
+    reads back.  Every layer gets the same synthetic input."""
+    Hq, Hk, D = 48, 16, 128
+    wl = synth.small_batch(args.seed, batch=samples)
+    base = {n: tb.TrellisLinear.from_host(wl.layers[n]) for n in ("qkv", "out")}
+    layers = _weight_copies(tb, base, n_layers)
+    x1 = torch.from_numpy(wl.xs["qkv"]).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(args.seed)
+    xp = torch.randn((chunk, 5120), generator=gen, device="cuda", dtype=torch.float32).half()
+    steps = args.warmup + args.steps
+    slots = samples
+    max_pages = -(-(prompt + steps + 4) // page) + 1
+    n_pages = -(-prompt // page) + samples * (3 + -(-steps // page) + -(-(keep_first + keep_last) // page))
+    cache = tb.KV4Cache.allocate(n_layers, n_pages, page, Hk, D)
+    table = torch.zeros((slots, max_pages), dtype=torch.int32, device="cuda")
+    lens = torch.zeros(slots, dtype=torch.int32, device="cuda")
+    ref = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    def heads(qkv):
+        h = qkv.view(qkv.shape[0], Hq + 2 * Hk, D)
+        return h[:, :Hq], h[:, Hq:Hq + Hk], h[:, Hq + Hk:]
+
+    def check(q, y, cu, rows, who):
+        """fp32 attention of rows 0..3 and the last over the read-back keys and values."""
+        length = int(lens[who])
+        k, v = tb.trellis_kv4_read(cache, 0, table, lens, ints([0, length]), length, slots=ints([who]))
+        worst = 0.0
+        for r in sorted({0, 1, 2, 3, rows - 1} & set(range(rows))):
+            pos = length - rows + r
+            i = torch.arange(length, device="cuda")
+            seen = (i <= pos) & ((i > pos - window) | (i < sinks) if window else torch.ones_like(i, dtype=torch.bool))
+            kk = k.float().repeat_interleave(Hq // Hk, 1).transpose(0, 1).contiguous()
+            vv = v.float().repeat_interleave(Hq // Hk, 1).transpose(0, 1).contiguous()
+            w = (kk @ q[cu + r].float().unsqueeze(-1)).squeeze(-1) * D ** -0.5
+            w = torch.softmax(w.masked_fill(~seen, float("-inf")), -1)
+            want = (w.unsqueeze(1) @ vv).squeeze(1)
+            worst = max(worst, float((y[cu + r].float() - want).norm() / want.norm()))
+        return worst
+
+    # ---- the prompt, in chunks, into slot 0
+    one, cu_p = ints([0]), ints([0, chunk])
+    add = ints([chunk])
+    qkv_p = torch.empty((chunk, base["qkv"].out_features), dtype=torch.float16, device="cuda")
+    y_p = torch.empty((chunk, Hq, D), dtype=torch.float16, device="cuda")
+    out_p = torch.empty((chunk, base["out"].out_features), dtype=torch.float16, device="cuda")
+
+    def prefill():
+        for _ in range(prompt // chunk):
+            tb.trellis_kv4_reserve(cache, table, lens, ref, add, slots=one)
+            for l in range(n_layers):
+                tb.trellis_gemm(layers[l]["qkv"], xp, out=qkv_p)
+                q, k, v = heads(qkv_p)
+                tb.trellis_kv4_append(cache, l, table, lens, cu_p, k, v, slots=one)
+                tb.trellis_kv4_attn(cache, l, table, lens, cu_p, q, window=window, sinks=sinks, max_q=chunk, slots=one, out=y_p)
+                if l == 0:
+                    kept[0].copy_(q), kept[1].copy_(y_p)
+                tb.trellis_gemm(layers[l]["out"], y_p.view(chunk, Hq * D), out=out_p)
+
+    kept = [torch.empty_like(y_p), torch.empty_like(y_p)]
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    prefill()  # (untimed)
+    tb.trellis_kv4_free(cache, table, lens, ref, one)
+    e0.record()
+    prefill()
+    e1.record()
+    torch.cuda.synchronize()
+    prefill_ms = e0.elapsed_time(e1)
+    err_prompt = check(kept[0], kept[1], 0, chunk, 0)
+
+    # ---- the samples
+    tb.trellis_kv4_fork(cache, table, lens, ref, ints([0] * (samples - 1)), ints(range(1, samples)))
+    cu_d, ones = ints(range(samples + 1)), ints([1] * samples)
+    qkv_d = torch.empty((samples, base["qkv"].out_features), dtype=torch.float16, device="cuda")
+    y_d = [torch.empty((samples, Hq, D), dtype=torch.float16, device="cuda") for _ in range(n_layers)]
+    q_0 = torch.empty((samples, Hq, D), dtype=torch.float16, device="cuda")
+    out_d = torch.empty((samples, base["out"].out_features), dtype=torch.float16, device="cuda")
+    ws = torch.zeros(max(tb.trellis_kv4_attn_workspace_bytes(cache, table, lens, cu_d, samples, Hq),
+                         *(base[n].workspace_bytes(tb.TRELLIS_OP_GEMV, samples) for n in base), 64 << 20),
+                     dtype=torch.uint8, device="cuda")
+
+    def decode():
+        tb.trellis_kv4_reserve(cache, table, lens, ref, ones, ws=ws)
+        for l in range(n_layers):
+            tb.trellis_gemv(layers[l]["qkv"], x1, out=qkv_d, ws=ws)
+            q, k, v = heads(qkv_d)
+            if l == 0:
+                q_0.copy_(q)
+            tb.trellis_kv4_append(cache, l, table, lens, cu_d, k, v, ws=ws)
+            tb.trellis_kv4_attn(cache, l, table, lens, cu_d, q, window=window, sinks=sinks, max_q=1, out=y_d[l], ws=ws)
+            tb.trellis_gemv(layers[l]["out"], y_d[l].view(samples, Hq * D), out=out_d, ws=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            decode()
+    torch.cuda.current_stream().wait_stream(side)
+
+    def replay(n):
+        e0.record()
+        for _ in range(n):
+            graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) * 1e3 / max(n, 1)
+
+    replay(args.warmup)
+    long_us = replay(args.steps - args.steps // 2)
+    # ---- first and last tokens kept, in place; then the rest of the steps
+    length = int(lens[0])
+    keep = [i for i in range(length) if i < keep_first or i >= length - keep_last]
+    everyone = ints(range(samples))
+    e0.record()
+    tb.trellis_kv4_compact(cache, table, lens, ref, everyone, everyone, ints(keep * samples),
+                           ints([len(keep) * i for i in range(samples + 1)]), ws=ws)
+    e1.record()
+    torch.cuda.synchronize()
+    compact_us = e0.elapsed_time(e1) * 1e3
+    short_us = replay(args.steps // 2)
+    err_decode = max(check(q_0, y_d[0], s, 1, s) for s in (0, samples - 1))
+    used = int((ref > 0).sum())
+    tb.trellis_kv4_free(cache, table, lens, ref, everyone, ws=ws)
+    torch.cuda.synchronize()
+    assert tb.error_word(ws) == 0 and tb.error_word() == 0, "a call refused its arguments"
+    assert int((ref != 0).sum()) == 0 and int(lens.sum()) == 0, "pages left behind"
+    assert err_prompt < 2e-3 and err_decode < 2e-3, (err_prompt, err_decode)
+    return {"workload": f"serving, {n_layers} attention layers (qkv K2 5120x10240, paged 4-bit cache of 16 heads of 128, 48 "
+                        f"query heads, out K2 6144x5120): a prompt of {prompt} in chunks of {chunk}, {samples} samples of it, "
+                        f"one token each a step in a HIP graph",
+            "prefill_ms": round(prefill_ms, 3), "prefill_tokens_per_s": round(prompt / prefill_ms * 1e3, 1),
+            "decode_us_per_step": round(long_us, 1), "decode_tokens_per_s": round(samples / long_us * 1e6, 1),
+            "compact_us": round(compact_us, 1), "decode_us_per_step_after_compaction": round(short_us, 1),
+            "tokens_kept": len(keep), "pages_in_use": used, "cache_MB": round(cache.pool.numel() / 1e6, 1),
+            "fp16_cache_MB": round(n_pages * n_layers * page * Hk * D * 4 / 1e6, 1),
+            "rel_err_prompt": round(err_prompt, 6), "rel_err_decode": round(err_decode, 6)}
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--warmup", type=int, default=20)
     ap.add_argument("--seed", type=int, default=0)
-    ap.add_argument("--workload", default="dense", choices=["dense", "small_batch", "moe", "moe_mlp", "prefill", "encode", "kernels", "micro"])
+    ap.add_argument("--workload", default="dense", choices=["dense", "small_batch", "moe", "moe_mlp", "prefill", "encode", "kernels", "micro", "serve"])
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-prefill", action="store_true")
     ap.add_argument("--no-extra", action="store_true", help="dense: skip the single, small-batch, MoE and fused-MLP lines")
@@ -730,6 +878,8 @@ def main():
         print(json.dumps(run_encode(args, torch, tb, synth)), flush=True)
     elif args.workload == "kernels":
         print(json.dumps(run_kernels(args, torch, tb, synth)), flush=True)
+    elif args.workload == "serve":
+        print(json.dumps(run_serve(args, torch, tb, synth)), flush=True)
     elif args.workload == "micro":
         print(json.dumps(run_micro(args, torch, tb)), flush=True)
     else:

@@ -282,10 +282,12 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
       top = max4(top);
-      // by how much the maximum grows (where there was none, from 0)
-      const float by = m[ct] == kNegInf ? top - log2f : fmaxf(top - log2f, 0.f), up = by == kNegInf ? 0.f : by;
-      alpha = m[ct] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(-up);
-      m[ct] = m[ct] == kNegInf ? by : m[ct] + up;
+      // By how much the maximum grows (where there was none, from 0).  A column that does not need it
+      // stays as it is, so that no column's result depends on which others are beside it.
+      const bool first = m[ct] == kNegInf, need = max4u(!(add <= 128.f * one) | first) != 0;
+      const float by = first ? top - log2f : need ? fmaxf(top - log2f, 0.f) : 0.f, up = by == kNegInf ? 0.f : by;
+      alpha = first ? 0.f : __builtin_amdgcn_exp2f(-up);
+      m[ct] = first ? by : m[ct] + up;
       add = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j)

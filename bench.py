@@ -692,7 +692,7 @@ def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, sampl
     layers = _weight_copies(tb, base, n_layers)
     x1 = torch.from_numpy(wl.xs["qkv"]).cuda()
     gen = torch.Generator(device="cuda").manual_seed(args.seed)
-    xp = torch.randn((chunk, 5120), generator=gen, device="cuda", dtype=torch.float32).half()
+    xp = [torch.randn((chunk, 5120), generator=gen, device="cuda", dtype=torch.float32).half() for _ in range(prompt // chunk)]
     steps = args.warmup + args.steps
     slots = samples
     max_pages = -(-(prompt + steps + 4) // page) + 1
@@ -707,6 +707,10 @@ def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, sampl
         h = qkv.view(qkv.shape[0], Hq + 2 * Hk, D)
         return h[:, :Hq], h[:, Hq:Hq + Hk], h[:, Hq + Hk:]
 
+    # (the synthetic weights' outputs have no fixed size: scores of about unit spread)
+    q, k, _ = heads(tb.trellis_gemm(layers[0]["qkv"], xp[0]))
+    scale = float(1.5 * D ** -0.5 / (q.float().square().mean().sqrt() * k.float().square().mean().sqrt()))
+
     def check(q, y, cu, rows, who):
         """fp32 attention of rows 0..3 and the last over the read-back keys and values."""
         length = int(lens[who])
@@ -718,7 +722,7 @@ def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, sampl
             seen = (i <= pos) & ((i > pos - window) | (i < sinks) if window else torch.ones_like(i, dtype=torch.bool))
             kk = k.float().repeat_interleave(Hq // Hk, 1).transpose(0, 1).contiguous()
             vv = v.float().repeat_interleave(Hq // Hk, 1).transpose(0, 1).contiguous()
-            w = (kk @ q[cu + r].float().unsqueeze(-1)).squeeze(-1) * D ** -0.5
+            w = (kk @ q[cu + r].float().unsqueeze(-1)).squeeze(-1) * scale
             w = torch.softmax(w.masked_fill(~seen, float("-inf")), -1)
             want = (w.unsqueeze(1) @ vv).squeeze(1)
             worst = max(worst, float((y[cu + r].float() - want).norm() / want.norm()))
@@ -732,13 +736,14 @@ def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, sampl
     out_p = torch.empty((chunk, base["out"].out_features), dtype=torch.float16, device="cuda")
 
     def prefill():
-        for _ in range(prompt // chunk):
+        for x in xp:
             tb.trellis_kv4_reserve(cache, table, lens, ref, add, slots=one)
             for l in range(n_layers):
-                tb.trellis_gemm(layers[l]["qkv"], xp, out=qkv_p)
+                tb.trellis_gemm(layers[l]["qkv"], x, out=qkv_p)
                 q, k, v = heads(qkv_p)
                 tb.trellis_kv4_append(cache, l, table, lens, cu_p, k, v, slots=one)
-                tb.trellis_kv4_attn(cache, l, table, lens, cu_p, q, window=window, sinks=sinks, max_q=chunk, slots=one, out=y_p)
+                tb.trellis_kv4_attn(cache, l, table, lens, cu_p, q, window=window, sinks=sinks, scale=scale, max_q=chunk, slots=one,
+                                    out=y_p)
                 if l == 0:
                     kept[0].copy_(q), kept[1].copy_(y_p)
                 tb.trellis_gemm(layers[l]["out"], y_p.view(chunk, Hq * D), out=out_p)
@@ -773,7 +778,8 @@ def run_serve(args, torch, tb, synth, n_layers=8, prompt=4096, chunk=1024, sampl
             if l == 0:
                 q_0.copy_(q)
             tb.trellis_kv4_append(cache, l, table, lens, cu_d, k, v, ws=ws)
-            tb.trellis_kv4_attn(cache, l, table, lens, cu_d, q, window=window, sinks=sinks, max_q=1, out=y_d[l], ws=ws)
+            tb.trellis_kv4_attn(cache, l, table, lens, cu_d, q, window=window, sinks=sinks, scale=scale, max_q=1, out=y_d[l],
+                                ws=ws)
             tb.trellis_gemv(layers[l]["out"], y_d[l].view(samples, Hq * D), out=out_d, ws=ws)
 
     graph = torch.cuda.CUDAGraph()

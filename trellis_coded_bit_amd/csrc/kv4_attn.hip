@@ -334,8 +334,12 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
   }
 }
 
-// Few columns per sequence: single and drafted tokens.  HBM (or, for short contexts, latency)
-// bounds it: every key and value is read once and used for at most 16 columns.
+// Few columns per sequence: single and drafted tokens.  Every key and value is read once and used for
+// at most 16 columns, so HBM bounds long contexts in principle; what it measured (group 4, heads of
+// 128): 64 ragged contexts of 300 .. 12288 tokens 97 us for 461 MB, 4.8 TB/s (a copy of the kernel that
+// only loads takes the same); one token over 131071 39 us for 138 MB, 8.5 of them the join; one over
+// 777 12 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
+// 256 (12 sequences of 500 .. 9001 tokens): 40 us for 53 MB, bound by one workgroup a CU.
 //
 // All sequences' (head, column tile, key tile) units stand in one line; each workgroup takes an
 // equal stretch of it, whatever the lengths, and its four waves take the stretch's key tiles in
@@ -343,7 +347,9 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
 // (sequence, head, column tile)).  A segment that several workgroups share is joined by the last
 // of them to arrive, in order, so results do not depend on timing.
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kMinChunk = 2 * kWaves;  // tiles: two a wave; a join costs more than a second tile
+// Tiles: two a wave; a join costs more than a second tile (one sequence, 8 heads, at 1, 2, 4 tiles a
+// wave: 3000 tokens 14.3, 16.1, 19.3 us, 12000 tokens 15.8, 16.2, 20.3, 30000 tokens 22.8, 20.6, 22.0).
+constexpr int kMinChunk = 2 * kWaves;
 // What starting and ending a segment costs a workgroup, in tiles (64 ragged contexts: 106.7 us at 0,
 // 100.0 at 2, 98.0 at 4, 98.3 at 6).
 constexpr int kSegCost = 4;
@@ -750,7 +756,9 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
 }
 
 // How often the narrow kernel holds a column: as many columns as the sequences' rows are known or
-// expected to have, up to 4, 8 or 16 a tile.
+// expected to have, up to 4, 8 or 16 a tile (group 4, by this rule and with 16 throughout: one
+// token over 131071 39.7, 43.4 us, over 777 13.6, 15.6; 64 ragged contexts 99, 102; two tokens each
+// over 777 14.3, 15.4, 64 ragged contexts 103.9, 104.2).
 int replicas(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads, int max_rows) {
   const long long rows = max_rows > 0 ? max_rows : ((long long)b.rows + b.n_seq - 1) / b.n_seq;
   const long long cols = rows * (n_q_heads / c.n_kv_heads);
@@ -801,8 +809,12 @@ size_t kv4_attn_workspace_bytes(const trellis_kv4_cache &c, const trellis_kv4_ba
 
 // A sequence of at most this many columns (rows times query heads per key/value head) is the
 // narrow kernel's, whose tiles are 16 columns wide and shared by any number of workgroups; the
-// wide kernel's are 128.  MEASURED_FEW
-constexpr int kFew = 96;
+// wide kernel's are 64.  Narrow against wide, in us: 16 sequences of 3000 .. 6000 tokens, heads of 128,
+// 32 columns 40, 48, 48 columns 51, 58, 64 columns 60, 62, 96 columns 81, 85, 128 columns 102, 88; 64 such
+// sequences, 48 columns 182, 144; 8 of heads of 256, 32 columns 39, 49, 48 columns 49, 52, 64 columns 59, 50.
+// A single sequence has few wide segments, which have to be split and joined: 30000 tokens, 64 columns
+// 38, 53, 128 columns 52, 54, 192 columns 67, 71, 256 columns 80, 72.
+int few_columns(int n_seq) { return n_seq == 1 ? 128 : 48; }
 
 hipError_t launch_kv4_attn(const Kv4Attn &a, void *ws, hipStream_t stream) {
   AttnArgs g{};
@@ -819,19 +831,21 @@ hipError_t launch_kv4_attn(const Kv4Attn &a, void *ws, hipStream_t stream) {
   // Which kernels: one where every sequence is known to be its kind (that kernel then takes whatever
   // there is, so a wrong bound costs time and nothing else), otherwise both, each with its sequences.
   const long long bound = (long long)(a.b.n_seq == 1 ? a.b.rows : a.max_rows > 0 ? a.max_rows : a.b.rows) * g.group;
+  const int few = few_columns(a.b.n_seq);
+  const bool both = a.b.n_seq > 1 && bound > few;
   g.tends = 1;
-  if (a.b.n_seq > 1 && bound > kFew) {
-    g.few = kFew;
+  if (both) {
+    g.few = few;
     const hipError_t e = launch_kv4_attn_wide(g, stream);
     if (e != hipSuccess) return e;
     g.tends = 0;
-  } else if (bound > kFew) {
+  } else if (bound > few) {
     g.few = -1;
     return launch_kv4_attn_wide(g, stream);
   } else {
     g.few = 0x7FFFFFFF;
   }
-  const int R = replicas(a.c, a.b, a.n_q_heads, g.few == kFew ? 0 : a.max_rows);
+  const int R = replicas(a.c, a.b, a.n_q_heads, both ? 0 : a.max_rows);
   const bool bf = a.dtype == TRELLIS_KV4_BF16;
   if (a.c.head_dim == 128) return bf ? launch_narrow<true, 1>(g, R, stream) : launch_narrow<false, 1>(g, R, stream);
   return bf ? launch_narrow<true, 2>(g, R, stream) : launch_narrow<false, 2>(g, R, stream);

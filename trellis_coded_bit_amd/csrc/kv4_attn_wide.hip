@@ -1,17 +1,27 @@
 // Attention over the 4-bit key/value cache, many columns per sequence: prompts and chunks of them.
 // (Mathematics and formats: kv4_attn.hip.)
 //
-// A workgroup takes 128 columns (rows times the query heads of one key/value head) of one sequence
-// and walks its key tiles of 128; a wave has 32 of the columns, as two tiles of 16.  A tile's codes
-// pass through shared memory once for all four waves, in two buffers, with one barrier a tile.
+// A workgroup takes 64 columns (rows times the query heads of one key/value head) of one sequence,
+// 16 a wave, and walks its key tiles of 128.  A tile is copied to shared memory once for all four
+// waves, into two buffers in turn, with one barrier a tile.
 //
-// Scores are as in the narrow kernel: codes against three E4M3 parts of the query.  The second
-// product is different: at 32 columns a wave the three-way split of the weights would cost more
-// vector instructions than unpacking the values, so a value tile's codes are read transposed and
-// turned to fp16 in registers (exactly), once for both column tiles, and the weights p vs are rounded
-// once to fp16 (within 2^-12), with one power of two per wave that follows the tiles' largest value
-// scale.  The softmax's vector instructions and the two products' matrix instructions take about the
-// same time (MEASURED_WIDE); two workgroups a CU overlap them.
+// Scores are codes against three parts of the query, as in the narrow kernel, but E2M3 ones: their
+// products take half the time of E4M3's.  A part's steps are fixed ones where E4M3's shrink with
+// the element, so three reach 2^-12 of the block's largest element, not of each; a score is a sum
+// over the block, whose error the largest elements set either way.
+//
+// The second product is different: per column a tile's three-way split of the weights costs as many
+// vector instructions as turning the values to fp16 does, and its products twice the time.  So a
+// value tile's codes are read transposed and turned to fp16 in registers (exactly), and the weights
+// p vs are rounded once to fp16 (within 2^-12), with one power of two per wave that follows the
+// tiles' largest value scale.
+//
+// The matrix instructions (900 cycles a tile and wave at heads of 128) and the vector ones (about
+// 450 instructions, 32 exponentials among them) bound it, with three waves a SIMD to overlap them; more columns
+// a wave would share the values' conversion, but leave two waves (32 a wave: 374 us where 64 columns a
+// workgroup took 245).  4096 tokens, 32 query heads, 8 key/value heads of 128: 200 us, 137 GFLOP, 690
+// TFLOP/s (the library's fp16 product of 8192^3 reaches 1330).  Chunks of 300 .. 1023 tokens behind up to
+// 11000, window 2048: 90 us, 39 GFLOP.
 #include "kv4_attn_device.h"
 
 namespace trellis {
@@ -592,18 +602,26 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   }
 }
 
-// Segments (column tiles of 128 times heads), at most.
+// Segments (column tiles of 64 times heads), at most.
 long long wide_segments(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
-  return (((long long)b.rows * (n_q_heads / c.n_kv_heads) + kWideCols - 1) / kWideCols + b.n_seq) * c.n_kv_heads;
+  // (each sequence's last column tile may be partly filled)
+  return (((long long)b.rows * (n_q_heads / c.n_kv_heads) + kWideCols - 1) / kWideCols + b.n_seq - 1) * c.n_kv_heads;
 }
 
 // Workgroups that share a segment's keys: where there are too few segments to fill the card, as
-// many as do, but none with less than eight tiles of the longest context that the tables hold.
+// many as do, but with no fewer than four tiles each of the longest context that the tables hold, and
+// no more workgroups than the square root of its tiles, as one of them joins all their sums (one
+// sequence, group 4, 8 heads; by this rule, without the root, without splitting: 16 rows over 30000
+// tokens 53, 99, 220 us; 64 rows over 32000 78, 94, 754; over 4096 30, 27, 102; 256 rows over 8000
+// 68, 68, 193).
 int wide_splits(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
   const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? wide_waves<1>() : wide_waves<2>());
   const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
   long long n = room / segs;
   if (n > tiles / 4) n = tiles / 4;
+  long long root = 1;
+  while (root * root < tiles) ++root;
+  if (n > root) n = root;
   return n < 1 ? 1 : n > 64 ? 64 : (int)n;
 }
 

@@ -113,7 +113,7 @@ int trellis_kv4_read(const trellis_kv4_cache *c, int layer, const trellis_kv4_ba
  * A key whose weight is zero in fp32 adds nothing, whatever its value holds.
  * window >= 0 (0: none), sinks >= 0, scale finite.
  * max_rows: the caller's bound on n_b, 0 if unknown; it chooses kernels, results are right for
- *      any value. */
+ *      any value.  One launch, two where some sequences may have few and others many rows. */
 int trellis_kv4_attn(const trellis_kv4_cache *c, int layer, const trellis_kv4_batch *b, int dtype, const void *q,
                      int64_t q_row, int64_t q_head, int n_q_heads, float scale, int window, int sinks, int max_rows,
                      void *y, float *lse, void *ws, size_t ws_bytes, void *stream);

@@ -194,6 +194,30 @@ __device__ __forceinline__ void take_query(const float (&from)[NB][kCols][kRowF]
   }
 }
 
+// A lane's codes of a value tile's block, read transposed: tile dt = 2 p + d, 1024-byte half h.  One block
+// with its wait: for the builtin the compiler also waits for every copy to shared memory that is under
+// way, the next tile's among them.
+__device__ __forceinline__ void read_codes(const char *vp, int swizzle, v2i (&c)[4][2][2]) {
+  typedef __attribute__((address_space(3))) const char lds_char;
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_char *)vp;
+  const uint32_t a0 = at + swizzle * 16, a1 = at + (1 ^ swizzle) * 16, a2 = at + (2 ^ swizzle) * 16, a3 = at + (3 ^ swizzle) * 16;
+  asm volatile(
+      "ds_read_b64_tr_b4 %0, %16\n\tds_read_b64_tr_b4 %1, %16 offset:1024\n\t"
+      "ds_read_b64_tr_b4 %2, %16 offset:8\n\tds_read_b64_tr_b4 %3, %16 offset:1032\n\t"
+      "ds_read_b64_tr_b4 %4, %17\n\tds_read_b64_tr_b4 %5, %17 offset:1024\n\t"
+      "ds_read_b64_tr_b4 %6, %17 offset:8\n\tds_read_b64_tr_b4 %7, %17 offset:1032\n\t"
+      "ds_read_b64_tr_b4 %8, %18\n\tds_read_b64_tr_b4 %9, %18 offset:1024\n\t"
+      "ds_read_b64_tr_b4 %10, %18 offset:8\n\tds_read_b64_tr_b4 %11, %18 offset:1032\n\t"
+      "ds_read_b64_tr_b4 %12, %19\n\tds_read_b64_tr_b4 %13, %19 offset:1024\n\t"
+      "ds_read_b64_tr_b4 %14, %19 offset:8\n\tds_read_b64_tr_b4 %15, %19 offset:1032\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(c[0][0][0]), "=&v"(c[0][0][1]), "=&v"(c[0][1][0]), "=&v"(c[0][1][1]), "=&v"(c[1][0][0]), "=&v"(c[1][0][1]),
+        "=&v"(c[1][1][0]), "=&v"(c[1][1][1]), "=&v"(c[2][0][0]), "=&v"(c[2][0][1]), "=&v"(c[2][1][0]), "=&v"(c[2][1][1]),
+        "=&v"(c[3][0][0]), "=&v"(c[3][0][1]), "=&v"(c[3][1][0]), "=&v"(c[3][1][1])
+      : "v"(a0), "v"(a1), "v"(a2), "v"(a3)
+      : "memory");
+}
+
 // One tile into a wave's sums.  mask: some row does not see some key; bad: subtiles without a page;
 // odd: some value scale is not finite.
 template <int NB>
@@ -348,34 +372,24 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
         for (int nb = 0; nb < NB; ++nb) {
           const int row = lane & 15, sub = 2 * (lane >> 4);
           const char *vp = lds.v[buf][nb] + sub * 1024 + row * 64;
-          typedef __attribute__((address_space(3))) v2i lds_v2i;
           // Elements' tiles dt = 2 p, 2 p + 1 together, and the next word's codes turned to fp16 during
           // a word's products.
-          v2i codes[2][2][2];
-          const auto load = [&](int p) {
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const char *at = vp + ((p ^ (row >> 2)) * 16) + d * 8;
-              codes[p & 1][d][0] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)at);
-              codes[p & 1][d][1] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + 1024));
-            }
-          };
+          v2i codes[4][2][2];
+          read_codes(vp, row >> 2, codes);
           half8 a[2][2];
           const auto unpack = [&](int step) {  // word step & 3 of pair step >> 2
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-              const uint32_t c = codes[(step >> 2) & 1][d][(step >> 1) & 1][step & 1];
+              const uint32_t c = codes[step >> 2][d][(step >> 1) & 1][step & 1];
               const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
               const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
               a[step & 1][d] = half8{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
             }
           };
-          load(0);
           unpack(0);
 #pragma unroll
           for (int step = 0; step < 16; ++step) {
             const int p = step >> 2;
-            if ((step & 3) == 0 && p < 3) load(p + 1);
             if (step < 15) unpack(step + 1);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -30,11 +30,13 @@ namespace {
 
 constexpr int kColTiles = 1, kWideCols = 64 * kColTiles, kWideThreads = 256;  // column tiles a wave
 
+constexpr uint32_t kOdd = 1, kBad = 2;  // a value scale is not finite; the subtile has no page
+
 template <int NB>
 struct WideTiles {
   alignas(16) char k[2][NB][8192], v[2][NB][8192];
   alignas(16) float ks[2][NB][kTile], vs[2][NB][kTile];
-  int bad[2][8];  // subtiles without a page
+  alignas(16) uint32_t about[2][NB][8];  // subtiles: the largest finite value scale's exponent << 8 | kOdd | kBad
 };
 template <int NB>
 union WideLds {
@@ -107,7 +109,16 @@ __device__ __forceinline__ void put_share(const AttnArgs &g, const Seq &q, int t
     const uint32_t w = x.s & keep;
     float *to = kind ? lds.vs[buf][nb] : lds.ks[buf][nb];
     *reinterpret_cast<floatx2 *>(to + at) = floatx2{__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xFFFF0000u)};
-    if (i == 0) lds.bad[buf][s] = !here;
+    // the eight lanes' largest, as bf16's bits without sign
+    const uint32_t a = w & 0x7FFFu, b = (w >> 16) & 0x7FFFu;
+    const bool fa = a < 0x7F80u, fb = b < 0x7F80u;
+    uint32_t top = (max(fa ? a : 0u, fb ? b : 0u) << 1) & ~0xFFu;  // its exponent << 8
+    top |= ((fa & fb) ? 0 : kOdd) | (here ? 0 : kBad);
+    const auto merge = [](uint32_t x, uint32_t y) { return max(x & ~0xFFu, y & ~0xFFu) | ((x | y) & 0xFFu); };
+    top = merge(top, __builtin_amdgcn_update_dpp(0, top, 0xB1, 0xF, 0xF, true));
+    top = merge(top, __builtin_amdgcn_update_dpp(0, top, 0x4E, 0xF, 0xF, true));
+    top = merge(top, __builtin_amdgcn_update_dpp(0, top, 0x141, 0xF, 0xF, true));
+    if (kind && (i & 7) == 0) lds.about[buf][nb][s] = top;
   }
 }
 
@@ -502,26 +513,21 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     if (t + 1 < t1) load_share(g, q.lo, base, tile_at(q, t + 1), entry, lds.t, buf ^ 1, x);
     if (t + 2 < t1) entry = share_entry(g, q, tile_at(q, t + 2));
     if (!idle && k0 <= wp1) {
-      const uint32_t bad = (uint32_t)__ballot(lane < 8 && lds.t.bad[buf][lane & 7]);
-      const bool mask = !(k0 + kTile - 1 <= wp0 && bad == 0 &&
-                          (g.a.window == 0 || k0 > wp1 - g.a.window || k0 + kTile <= g.a.sinks));
       // ---- the value scales' power of two: the tile's largest finite one comes below 2^8; it stays
       // unless the tiles' scales outgrow it or fall far below
       float f[NB], keep[NB];
-      bool odd = false;
+      uint32_t flags = 0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const floatx2 w = *reinterpret_cast<const floatx2 *>(&lds.t.vs[buf][nb][2 * lane]);
-        const float a = fabsf(w[0]), b = fabsf(w[1]);
-        const bool fa = a <= 3.4028234e38f, fb = b <= 3.4028234e38f;
-        odd |= __any(!(fa & fb));
-        float big = fmaxf(fa ? a : 0.f, fb ? b : 0.f);
-        big = fmaxf(big, lane_xor<1>(big));
-        big = fmaxf(big, lane_xor<2>(big));
-        big = fmaxf(big, lane_xor<4>(big));
-        big = fmaxf(big, lane_xor<8>(big));
-        big = max4(big);
-        const int e = __builtin_amdgcn_readfirstlane(max((int)(__builtin_bit_cast(uint32_t, big) >> 23), 32));
+        uint32_t top = 0, any = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(lds.t.about[buf][nb] + 4 * h);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, v[k]), any |= v[k];
+        }
+        flags |= any;
+        const int e = max((int)(__builtin_amdgcn_readfirstlane(top) >> 8), 32);
         keep[nb] = 1.f;
         if (e > e_run[nb] || e < e_run[nb] - 8) {
           const int to = min(e + 2, 254), by = min(max(e_run[nb] - to, -126), 127);
@@ -530,6 +536,12 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
         }
         f[nb] = __builtin_bit_cast(float, (uint32_t)(261 - e_run[nb]) << 23);
       }
+      flags = __builtin_amdgcn_readfirstlane(flags);
+      const bool odd = flags & kOdd;
+      uint32_t bad = 0;
+      if (flags & kBad) bad = (uint32_t)__ballot(lane < 8 && (lds.t.about[buf][0][lane & 7] & kBad));
+      const bool mask = !(k0 + kTile - 1 <= wp0 && bad == 0 &&
+                          (g.a.window == 0 || k0 > wp1 - g.a.window || k0 + kTile <= g.a.sinks));
       wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, query, pos, f, keep, e_run, m, l, o);
     }
   }
@@ -619,7 +631,8 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
 // Segments (column tiles of 64 times heads), at most.
 long long wide_segments(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
   // (each sequence's last column tile may be partly filled)
-  return (((long long)b.rows * (n_q_heads / c.n_kv_heads) + kWideCols - 1) / kWideCols + b.n_seq - 1) * c.n_kv_heads;
+  const long long tiles = ((long long)b.rows * (n_q_heads / c.n_kv_heads) + kWideCols - 1) / kWideCols + b.n_seq - 1;
+  return (tiles > 1 ? tiles : 1) * c.n_kv_heads;
 }
 
 // Workgroups that share a segment's keys: where there are too few segments to fill the card, as
@@ -627,11 +640,14 @@ long long wide_segments(const trellis_kv4_cache &c, const trellis_kv4_batch &b, 
 // no more workgroups than the square root of its tiles, as one of them joins all their sums (one
 // sequence, group 4, 8 heads; by this rule, without the root, without splitting: 16 rows over 30000
 // tokens 53, 99, 220 us; 64 rows over 32000 78, 94, 754; over 4096 30, 27, 102; 256 rows over 8000
-// 68, 68, 193).
+// 68, 68, 193).  Segments that fill the card, but not one and a half times, are halved: their last
+// workgroups would run on alone (16 sequences of 3000 .. 6000 tokens, 40 rows each 133 -> 98 us, 48 rows
+// 135 -> 103; 64 rows of 8 sequences and heads of 256 104 -> 99).
 int wide_splits(const trellis_kv4_cache &c, const trellis_kv4_batch &b, int n_q_heads) {
   const long long segs = wide_segments(c, b, n_q_heads), room = (long long)micro_cus() * (c.head_dim == 128 ? wide_waves<1>() : wide_waves<2>());
   const long long tiles = ((long long)b.max_pages * c.page_size + kTile - 1) / kTile;
   long long n = room / segs;
+  if (n == 1 && 2 * segs < 3 * room) n = 2;
   if (n > tiles / 4) n = tiles / 4;
   long long root = 1;
   while (root * root < tiles) ++root;

@@ -2,15 +2,15 @@
 //
 // Mathematics.  With q' = H q (rotated once per row) a score is q . k = sum over blocks of
 // ks * (q' . kc): kc the stored E2M1 codes, ks the block's scale.  The codes are matrix operands
-// as they lie in memory: v_mfma_scale_f32_16x16x128_f8f6f4 takes an E2M1 operand against an
-// E4M3 one, 128 products deep, so a key is never unpacked and its scale is one multiplication
+// as they lie in memory: v_mfma_scale_f32_16x16x128_f8f6f4 takes an E2M1 operand against one of
+// more bits, 128 products deep, so a key is never unpacked and its scale is one multiplication
 // per score.  Likewise y' = sum_j (p_j vs_j) vc_j with the value's scale taken into the weight,
 // and y = H y' at the end.
 //
-// Precision.  What meets the codes is split into E4M3 parts, each the rounding of what the last
-// one left: a query into three (within 2^-12 of each element, its own 16 bits for fp16), with one
-// power of two per (row, block); a weight p_j vs_j into three (within 2^-12), with one power of
-// two per tile of 128 keys.  Products and sums are fp32, as are the maxima, the sums of weights and
+// Precision.  What meets the codes is split into parts, each the rounding of what the last one left: a
+// query into three of E2M3 (within 2^-12 of the block's largest element), with one power of two per
+// (row, block); a weight p_j vs_j into three of E4M3 (within 2^-12 of itself), with one power of two
+// per tile of 128 keys.  Products and sums are fp32, as are the maxima, the sums of weights and
 // everything that is joined.
 #include "kv4_attn_device.h"
 
@@ -25,6 +25,22 @@ struct WaveLds {
   alignas(16) char v[NB * kCols * kRowF * 4];  // >= NB * 8 KiB
   alignas(16) uint16_t ks[NB][kTile], vs[NB][kTile];
   alignas(16) int w[R > 1 ? 4 * (kCols / R) * 3 + 1 : 1][8];  // weights' parts on their way between lanes; then zeros
+};
+
+// C columns as matrix operands, in shared memory (QueryBlock), in words of two registers.
+template <int NB, int C>
+struct QueryLds {
+  alignas(16) v2i part[NB][3][3][4][C];
+  int scale[NB][C];
+  float add[NB][C];
+};
+
+// What a lane keeps of its column.
+template <int NB>
+struct Column {
+  int scale[NB];
+  float add;
+  int pos;  // the column's position (-1: sees nothing)
 };
 
 // Where a tile's keys go.  The 128 keys are eight subtiles of 16, each within one page.  Lane l
@@ -187,15 +203,20 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB,
     read_scales<R>(lds.ks[nb], ks);
     v8i part[3];
 #pragma unroll
-    for (int s = 0; s < 3; ++s) part[s] = read8(q.part[nb][s][lane & (C - 1)][lane >> 4]);
+    for (int s = 0; s < 3; ++s) {
+      v2i w[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) w[k] = q.part[nb][s][k][lane >> 4][lane & (C - 1)];
+      part[s] = v8i{w[0][0], w[0][1], w[1][0], w[1][1], w[2][0], w[2][1], 0, 0};
+    }
     float y[NT][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const v8i a = {k[nb][j][0], k[nb][j][1], k[nb][j][2], k[nb][j][3], 0, 0, 0, 0};
       floatx4 s = {0.f, 0.f, 0.f, 0.f};
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 0, 0, scale_byte(0), 0, col.scale[nb]);
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 0, 0, scale_byte(0), 1, col.scale[nb]);
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 0, 0, scale_byte(0), 2, col.scale[nb]);
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 2, 0, scale_byte(0), 0, col.scale[nb]);
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 2, 0, scale_byte(0), 1, col.scale[nb]);
+      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 2, 0, scale_byte(0), 2, col.scale[nb]);
       constexpr int H = 4 / R;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -208,7 +229,7 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float s = scale_of(ks, t, i);
-        x[t][i] = nb ? fmaf(y[t][i], s, x[t][i]) : y[t][i] * s;
+        x[t][i] = fmaf(y[t][i], s, nb ? x[t][i] : col.add);
       }
   }
 }
@@ -339,7 +360,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
 // 128): 64 ragged contexts of 300 .. 12288 tokens 97 us for 461 MB, 4.8 TB/s (a copy of the kernel that
 // only loads takes the same); one token over 131071 39 us for 138 MB, 8.5 of them the join; one over
 // 777 12 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
-// 256 (12 sequences of 500 .. 9001 tokens): 40 us for 53 MB, bound by one workgroup a CU.
+// 256 (12 sequences of 500 .. 9001 tokens): 40 us for 53 MB, bound by one wave a SIMD.
 //
 // All sequences' (head, column tile, key tile) units stand in one line; each workgroup takes an
 // equal stretch of it, whatever the lengths, and its four waves take the stretch's key tiles in
@@ -401,7 +422,8 @@ struct Segment {
   long long begin;  // the place of its first tile
 };
 
-// Resident waves a SIMD: two blocks need more than 256 registers for a tile on its way and the sums.
+// Resident waves a SIMD: two blocks need about 440 registers for a tile on its way and the sums (at 256
+// some 200 are spilled).
 template <int NB, int R>
 constexpr int narrow_waves() { return NB == 1 ? 2 : 1; }
 
@@ -550,8 +572,21 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       query_n = load_query<NB>(g, n.q, n.head, column_base(g, n.col0), tid >> 4);
     }
     const char *base_n = kv4_chunk(g.a.c, g.a.layer, 0, n.head);
-    put_query<BF, NB, C>(g, query, lds.q);
-    __syncthreads();
+    {
+      auto *stage = reinterpret_cast<float(*)[kCols][kRowF]>(lds.wave[0].v);  // (free between segments)
+      if ((tid >> 4) < C) stage_query<BF, NB>(g, query, tid >> 4, stage);
+      __syncthreads();
+      if (wave < NB && (lane & 15) < C) {
+        const int cc = lane & 15;
+        const QueryBlock b = take_block(stage[wave][cc] + 32 * (lane >> 4));
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) lds.q.part[wave][s][k][lane >> 4][cc] = v2i{(int)b.part[s][2 * k], (int)b.part[s][2 * k + 1]};
+        if (lane < 16) lds.q.scale[wave][cc] = b.scale, lds.q.add[wave][cc] = b.add;
+      }
+      __syncthreads();
+    }
     const int cols = (int)min((long long)C, (long long)q.n * g.group - col0);
     const ColumnBase from = column_base(g, col0);
     const int pos0 = q.len - q.n + from.row, pos1 = q.len - q.n + column_at(g, from, cols - 1).row;
@@ -561,6 +596,8 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       column.pos = cc < cols ? q.len - q.n + column_at(g, from, cc).row : -1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) column.scale[nb] = lds.q.scale[nb][cc];
+      column.add = lds.q.add[0][cc];
+      if constexpr (NB == 2) column.add += lds.q.add[1][cc];
     }
     // ---- this wave's tiles
     Sums<NB> sum;

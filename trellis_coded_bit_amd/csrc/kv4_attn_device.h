@@ -134,15 +134,6 @@ __device__ __forceinline__ ColumnBase column_at(const AttnArgs &g, const ColumnB
   return {from.row + (int)r, (int)(x - __umul24(r, g.group))};
 }
 
-// C columns' rotated queries as matrix operands, in shared memory, times the softmax's scale and
-// log2 e: a product with its scales is a score in powers of two.  Lane group g of a column's
-// E4M3 operand holds elements 16 g .. + 15 and 64 + 16 g .. + 15 of a block.
-template <int NB, int C>
-struct QueryLds {
-  alignas(16) int part[NB][3][C][4][8];
-  int scale[NB][C];  // a byte a part: its power of two as the matrix instructions take it
-};
-
 // Sixteen lanes to a column (the `col`-th from `from` on), eight elements each.
 template <int NB>
 struct QueryRaw {
@@ -163,64 +154,79 @@ __device__ __forceinline__ QueryRaw<NB> load_query(const AttnArgs &g, const Seq 
   return r;
 }
 
-template <bool BF, int NB, int C>
-__device__ __forceinline__ void put_query(const AttnArgs &g, const QueryRaw<NB> &raw, QueryLds<NB, C> &lds) {
-  const int c = threadIdx.x >> 4, i = threadIdx.x & 15, k = kv4_fwht16_place(i);  // elements 8 k .. 8 k + 7
+constexpr int kRowF = 132;  // floats of a column in shared memory: 128, and 4 to spread the banks
+
+// Rotates column c of `to`, 16 lanes a column, times the softmax's scale and log2 e; even elements of each
+// 32 first, as the conversion takes them.
+template <bool BF, int NB>
+__device__ __forceinline__ void stage_query(const AttnArgs &g, const QueryRaw<NB> &raw, int c, float (*to)[kCols][kRowF]) {
+  const int i = threadIdx.x & 15, k = kv4_fwht16_place(i);
   const float factor = g.a.scale * (kLog2e * kRsqrt128) * kv4_fwht16_sign(i);
-  if (c >= C) return;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     float x[8];
     kv4_unpack8<BF>(raw.x[nb], x);
     kv4_fwht16_signed(x, i);
-    // the largest magnitude as an integer: infinity is above every number, a NaN above infinity
-    uint32_t top = 0;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      x[t] *= factor;
-      const uint32_t w = __builtin_bit_cast(uint32_t, x[t]) & 0x7FFFFFFFu;
-      top = w > top ? w : top;
-    }
-    top = kv4_max16(top);
-    // the largest element comes to [128, 256); a column that is not finite becomes NaN
-    const int e = max((int)(top >> 23), 16);
-    const float f = top >= 0x7F800000u ? __builtin_nanf("") : __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);
-    if (i == 0) lds.scale[nb][c] = (e - 7) | (e - 11) << 8 | (e - 15) << 16;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) x[t] *= f;
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      v2i o;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        int z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w], x[4 * w + 1], 0, false);
-        z = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * w + 2], x[4 * w + 3], z, true);
-        o[w] = z;
-        const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8(z, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(z, true);
-        // what is left, times 16: at most 128
-        x[4 * w] = (x[4 * w] - a[0]) * 16.f;
-        x[4 * w + 1] = (x[4 * w + 1] - a[1]) * 16.f;
-        x[4 * w + 2] = (x[4 * w + 2] - b[0]) * 16.f;
-        x[4 * w + 3] = (x[4 * w + 3] - b[1]) * 16.f;
-      }
-      *reinterpret_cast<v2i *>(&lds.part[nb][s][c][(k & 7) >> 1][(k >> 3) * 4 + (k & 1) * 2]) = o;
-    }
+    float *at = to[nb][c] + 32 * (k >> 2) + 4 * (k & 3);
+    *reinterpret_cast<floatx4 *>(at) = floatx4{x[0], x[2], x[4], x[6]} * factor;
+    *reinterpret_cast<floatx4 *>(at + 16) = floatx4{x[1], x[3], x[5], x[7]} * factor;
   }
 }
 
-// What a lane keeps of its column.
-template <int NB>
-struct Column {
-  int scale[NB];
-  int pos;  // the column's position (-1: sees nothing)
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx32 __attribute__((ext_vector_type(32)));
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+
+// A block of a column as a matrix operand: lane (n, g) has elements 32 g .. 32 g + 31 of column n, as
+// three E2M3 parts.  (Their products take half the time of E4M3's.  A part's steps are fixed where
+// E4M3's shrink with the element, so three reach 2^-12 of the block's largest element, not of each; a
+// score is a sum over the block, whose error the largest elements set either way.)
+struct QueryBlock {
+  u32x6 part[3];
+  int scale;  // a byte a part: its power of two as the matrix instructions take it
+  float add;  // NaN where the block is not finite: no E2M3 number says so
 };
+
+__device__ __forceinline__ QueryBlock take_block(const float *from) {
+  const floatx4 *p = reinterpret_cast<const floatx4 *>(from);
+  QueryBlock q;
+  floatx16 x[2];  // elements 2 j, 2 j + 1
+  uint32_t top = 0;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const floatx4 v = p[t];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = v[e];
+      x[t >> 2][4 * (t & 3) + e] = w;
+      // the largest magnitude as an integer: infinity is above every number, a NaN above infinity
+      const uint32_t u = __builtin_bit_cast(uint32_t, w) & 0x7FFFFFFFu;
+      top = u > top ? u : top;
+    }
+  }
+  top = max4u(top);
+  q.add = top >= 0x7F800000u ? __builtin_nanf("") : 0.f;
+  // The largest comes to [3.75, 7.5), so nothing saturates; what a part leaves is at most 0.25, then
+  // 0.125, in its units: the next one's are 16, then 32 times smaller.
+  const int e = max((int)((top + 0x00100000u) >> 23), 24);
+  q.scale = (e - 2) | (e - 6) << 8 | (e - 11) << 16;
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const float unit = __builtin_bit_cast(float, (uint32_t)(e - (s == 0 ? 2 : s == 1 ? 6 : 11)) << 23);
+    q.part[s] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x[0], x[1], unit);
+    if (s < 2) {
+      const floatx32 back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(q.part[s], unit);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[0][j] -= back[2 * j], x[1][j] -= back[2 * j + 1];
+    }
+  }
+  return q;
+}
 
 __device__ __forceinline__ v8i read8(const int *p) {
   const v4i a = *reinterpret_cast<const v4i *>(p), b = *reinterpret_cast<const v4i *>(p + 4);
   return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
-
-constexpr int kRowF = 132;  // floats of a column's sums in shared memory: 128, and 4 to spread the banks
 
 // Clears the rows past the last sequence's (one workgroup).
 template <int NB, int THREADS>

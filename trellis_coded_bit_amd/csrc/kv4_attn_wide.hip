@@ -5,12 +5,8 @@
 // 16 a wave, and walks its key tiles of 128.  A tile is copied to shared memory once for all four
 // waves, into two buffers in turn, with one barrier a tile.
 //
-// Scores are codes against three parts of the query, as in the narrow kernel, but E2M3 ones: their
-// products take half the time of E4M3's.  A part's steps are fixed ones where E4M3's shrink with
-// the element, so three reach 2^-12 of the block's largest element, not of each; a score is a sum
-// over the block, whose error the largest elements set either way.
-//
-// The second product is different: per column a tile's three-way split of the weights costs as many
+// Scores are as in the narrow kernel: codes against three parts of the query.  The second product is
+// different: per column a tile's three-way split of the weights costs as many
 // vector instructions as turning the values to fp16 does, and its products twice the time.  So a
 // value tile's codes are read transposed and turned to fp16 in registers (exactly), and the weights
 // p vs are rounded once to fp16 (within 2^-12), with one power of two per wave that follows the
@@ -135,35 +131,13 @@ __device__ __forceinline__ void read_scales32(const float *s, float (&w)[32]) {
 // Key (j, i) of the products' results is key 16 (i >> 1) + 2 j + (i & 1) of the lane's.
 __device__ __forceinline__ constexpr int key32(int j, int i) { return 16 * (i >> 1) + 2 * j + (i & 1); }
 
-// A wave's 16 columns as matrix operands.  Lane (n, g) has elements 32 g .. 32 g + 31 of column n as
-// three E2M3 parts.
+// A wave's 16 columns as matrix operands (QueryBlock).
 template <int NB>
 struct Query {
   v8i part[NB][3];  // (six registers each)
-  int scale[NB];    // a byte a part: its power of two
-  float add;        // NaN where the column is not finite: no E2M3 number says so
+  int scale[NB];
+  float add;
 };
-
-// Rotates the wave's columns, 16 lanes a column, into shared memory, four columns a step; even elements
-// of each 32 first, as the conversion takes them.
-template <bool BF, int NB>
-__device__ __forceinline__ void stage_query(const AttnArgs &g, const QueryRaw<NB> &raw, int step, float (&to)[NB][kCols][kRowF]) {
-  const int c = 4 * step + ((threadIdx.x & 63) >> 4), i = threadIdx.x & 15, k = kv4_fwht16_place(i);
-  const float factor = g.a.scale * (kLog2e * kRsqrt128) * kv4_fwht16_sign(i);
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    float x[8];
-    kv4_unpack8<BF>(raw.x[nb], x);
-    kv4_fwht16_signed(x, i);
-    float *at = to[nb][c] + 32 * (k >> 2) + 4 * (k & 3);
-    *reinterpret_cast<floatx4 *>(at) = floatx4{x[0], x[2], x[4], x[6]} * factor;
-    *reinterpret_cast<floatx4 *>(at + 16) = floatx4{x[1], x[3], x[5], x[7]} * factor;
-  }
-}
-
-typedef float floatx16 __attribute__((ext_vector_type(16)));
-typedef float floatx32 __attribute__((ext_vector_type(32)));
-typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 
 template <int NB>
 __device__ __forceinline__ void take_query(const float (&from)[NB][kCols][kRowF], Query<NB> &q) {
@@ -171,37 +145,12 @@ __device__ __forceinline__ void take_query(const float (&from)[NB][kCols][kRowF]
   q.add = 0.f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const floatx4 *p = reinterpret_cast<const floatx4 *>(from[nb][lane & 15] + 32 * (lane >> 4));
-    floatx16 x[2];  // elements 2 j, 2 j + 1
-    uint32_t top = 0;
+    const QueryBlock b = take_block(from[nb][lane & 15] + 32 * (lane >> 4));
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const floatx4 v = p[t];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = v[e];
-        x[t >> 2][4 * (t & 3) + e] = w;
-        const uint32_t u = __builtin_bit_cast(uint32_t, w) & 0x7FFFFFFFu;
-        top = u > top ? u : top;
-      }
-    }
-    top = max4u(top);
-    if (top >= 0x7F800000u) q.add = __builtin_nanf("");
-    // The largest comes to [3.75, 7.5), so nothing saturates; what a part leaves is at most 0.25, then
-    // 0.125, in its units: the next one's are 16, then 32 times smaller.
-    const int e = max((int)((top + 0x00100000u) >> 23), 24);
-    q.scale[nb] = (e - 2) | (e - 6) << 8 | (e - 11) << 16;
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      const float unit = __builtin_bit_cast(float, (uint32_t)(e - (s == 0 ? 2 : s == 1 ? 6 : 11)) << 23);
-      const u32x6 w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(x[0], x[1], unit);
-      q.part[nb][s] = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], 0, 0};
-      if (s < 2) {
-        const floatx32 back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, unit);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[0][j] -= back[2 * j], x[1][j] -= back[2 * j + 1];
-      }
-    }
+    for (int s = 0; s < 3; ++s)
+      q.part[nb][s] = v8i{(int)b.part[s][0], (int)b.part[s][1], (int)b.part[s][2], (int)b.part[s][3], (int)b.part[s][4], (int)b.part[s][5], 0, 0};
+    q.scale[nb] = b.scale;
+    q.add += b.add;
   }
 }
 
@@ -479,7 +428,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
 #pragma unroll
     for (int k = 0; k < 4; ++k) r[k] = load_query<NB>(g, q, head, from, c0 + 4 * k + (lane >> 4));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) stage_query<BF, NB>(g, r[k], k, lds.o[wave]);
+    for (int k = 0; k < 4; ++k) stage_query<BF, NB>(g, r[k], 4 * k + (lane >> 4), lds.o[wave]);
     __builtin_amdgcn_wave_barrier();
     take_query<NB>(lds.o[wave], query[ct]);
     __builtin_amdgcn_wave_barrier();

@@ -368,9 +368,10 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
 // (sequence, head, column tile)).  A segment that several workgroups share is joined by the last
 // of them to arrive, in order, so results do not depend on timing.
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-// Tiles: two a wave; a join costs more than a second tile (one sequence, 8 heads, at 1, 2, 4 tiles a
-// wave: 3000 tokens 14.3, 16.1, 19.3 us, 12000 tokens 15.8, 16.2, 20.3, 30000 tokens 22.8, 20.6, 22.0).
-constexpr int kMinChunk = 2 * kWaves;
+// The least stretch of tiles for which a segment is split: one a wave, but two where a segment has more
+// than 128, as the join reads every part (8 heads, at one, two a wave: 777 tokens 11.3, 11.8 us, 3000 tokens
+// 13.6, 15.4, 12000 tokens 15.8, 16.2, 30000 tokens 22.8, 20.6; eight sequences of 3000 tokens 17.3, 16.6).
+constexpr int kMinChunk = kWaves, kMinChunkLong = 2 * kWaves, kLong = 128;
 // What starting and ending a segment costs a workgroup, in tiles (64 ragged contexts: 106.7 us at 0,
 // 100.0 at 2, 98.0 at 4, 98.3 at 6).
 constexpr int kSegCost = 4;
@@ -407,7 +408,7 @@ __device__ __forceinline__ long long block_prefix(long long v, long long *lds, l
   return before + x - v;
 }
 
-__device__ __forceinline__ int padded(int tiles) { return (tiles + kMinChunk - 1) / kMinChunk * kMinChunk; }
+__device__ __forceinline__ int padded(int tiles, int least) { return (tiles + least - 1) & -least; }
 
 __device__ __forceinline__ long long quotient(long long a, long long b) {  // of small numbers quickly
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
@@ -442,16 +443,18 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   long long U = 0, chunk = 0, u = 0, u1 = 0, pre = 0;
   Segment c;
   c.s = -1;
+  int least = kMinChunkLong;
   bool small = n_seq <= 64;
   if (small) {  // every wave by itself, a lane a sequence
     Seq q{};
     int we = 0, wr = 0;
+    if (lane < n_seq) q = seq_of<C>(g, lane, blockIdx.x == 0 && wave == 0 && g.tends);
+    if (!__any(q.col_tiles && q.tiles > kLong)) least = kMinChunk;
     if (lane < n_seq) {
-      q = seq_of<C>(g, lane, blockIdx.x == 0 && wave == 0 && g.tends);
       const long long segs = (long long)Hk * q.col_tiles;
-      small = segs * padded(q.tiles) < (1 << 24);
+      small = segs * padded(q.tiles, least) < (1 << 24);
       we = (int)min(segs * (kSegCost + q.tiles), 1LL << 24);
-      wr = (int)min(segs * padded(q.tiles), 1LL << 24);
+      wr = (int)min(segs * padded(q.tiles, least), 1LL << 24);
     }
     small = __all(small);
     if (small) {
@@ -462,9 +465,9 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
         if (lane >= d) pe += a, pr += b;
       }
       const int exact = __builtin_amdgcn_readlane(pe, 63), round = __builtin_amdgcn_readlane(pr, 63);
-      whole = round <= (long long)kMinChunk * G;
+      whole = round <= (long long)least * G;
       U = whole ? round : exact;
-      chunk = whole ? kMinChunk : ((uint32_t)exact + G - 1) / (uint32_t)G;
+      chunk = whole ? least : ((uint32_t)exact + G - 1) / (uint32_t)G;
       u = blockIdx.x * chunk;
       u1 = min(u + chunk, U);
       if (u >= u1) return;
@@ -476,22 +479,23 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     }
   }
   if (!small) {
+    least = kMinChunkLong;
     long long exact = 0, round = 0;
     for (int s0 = 0; s0 < n_seq; s0 += kThreads) {
       long long we = 0, wr = 0, t;
       if (s0 + tid < n_seq) {
         const Seq q = seq_of<C>(g, s0 + tid, blockIdx.x == 0 && g.tends);
         we = (long long)Hk * q.col_tiles * (kSegCost + q.tiles);
-        wr = (long long)Hk * q.col_tiles * padded(q.tiles);
+        wr = (long long)Hk * q.col_tiles * padded(q.tiles, least);
       }
       block_prefix(we, lds.scan, &t);
       exact += t;
       block_prefix(wr, lds.scan, &t);
       round += t;
     }
-    whole = round <= (long long)kMinChunk * G;
+    whole = round <= (long long)least * G;
     U = whole ? round : exact;
-    chunk = whole ? kMinChunk : (exact + G - 1) / G;
+    chunk = whole ? least : (exact + G - 1) / G;
     u = blockIdx.x * chunk;
     u1 = min(u + chunk, U);
     if (u >= u1) return;
@@ -502,7 +506,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
       long long w = 0, t;
       if (s0 + tid < n_seq) {
         const Seq q = seq_of<C>(g, s0 + tid, false);
-        w = (long long)Hk * q.col_tiles * (whole ? padded(q.tiles) : kSegCost + q.tiles);
+        w = (long long)Hk * q.col_tiles * (whole ? padded(q.tiles, least) : kSegCost + q.tiles);
       }
       const long long p = base + block_prefix(w, lds.scan, &t);
       if (u >= p && u < p + w) lds.found[0] = s0 + tid, lds.found[1] = p;
@@ -516,7 +520,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   }
   if (c.q.col_tiles == 0) return;  // (as above)
   const int ahead = whole ? 0 : kSegCost;  // of a segment's tiles
-  c.per = whole ? padded(c.q.tiles) : ahead + c.q.tiles;
+  c.per = whole ? padded(c.q.tiles, least) : ahead + c.q.tiles;
   {
     const long long seg = quotient(u - pre, c.per);
     c.begin = pre + seg * c.per + ahead;
@@ -563,7 +567,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
             if (++n.s >= n_seq) return;  // (the lengths changed under the call)
             n.q = seq_from(seq_of<C>(g, n.s, false), 0);
           } while (n.q.col_tiles == 0);
-          n.per = whole ? padded(n.q.tiles) : ahead + n.q.tiles;
+          n.per = whole ? padded(n.q.tiles, least) : ahead + n.q.tiles;
         }
       }
       n.t1 = (int)min((long long)n.q.tiles, u1 - n.begin);

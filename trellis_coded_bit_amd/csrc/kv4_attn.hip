@@ -195,7 +195,7 @@ __device__ __forceinline__ v8i read_values(const WaveLds<NB, R> &lds, int nb, in
 template <int NB, int R>
 __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB, kCols / R> &q, const Column<NB> &col,
                                        const WaveLds<NB, R> &lds, float (&x)[8 / R][4]) {
-  constexpr int NT = 8 / R, C = kCols / R;
+  constexpr int NT = 8 / R, C = kCols / R, kChains = 4;
   const int lane = opaque_tid() & 63, r = (lane & 15) / C;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -211,18 +211,30 @@ __device__ __forceinline__ void scores(const v4i (&k)[NB][8], const QueryLds<NB,
     }
     float y[NT][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const v8i a = {k[nb][j][0], k[nb][j][1], k[nb][j][2], k[nb][j][3], 0, 0, 0, 0};
-      floatx4 s = {0.f, 0.f, 0.f, 0.f};
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s, 4, 2, 0, scale_byte(0), 0, col.scale[nb]);
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s, 4, 2, 0, scale_byte(0), 1, col.scale[nb]);
-      s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s, 4, 2, 0, scale_byte(0), 2, col.scale[nb]);
+    for (int j0 = 0; j0 < 8; j0 += kChains) {
+      // several chains of three products side by side: one waits for itself
+      floatx4 s[kChains];
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int c = 0; c < kChains; ++c) {
+          const v4i &w = k[nb][j0 + c];
+          const v8i a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+          if (p == 0) s[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+          if (p == 0) s[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[0], s[c], 4, 2, 0, scale_byte(0), 0, col.scale[nb]);
+          if (p == 1) s[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[1], s[c], 4, 2, 0, scale_byte(0), 1, col.scale[nb]);
+          if (p == 2) s[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, part[2], s[c], 4, 2, 0, scale_byte(0), 2, col.scale[nb]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
       constexpr int H = 4 / R;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float &z = y[(i >> 1) * H + (j >> 1) % H][2 * (j & 1) + (i & 1)];
-        z = (j >> 1) / H == 0 ? s[i] : r == (j >> 1) / H ? s[i] : z;
-      }
+      for (int c = 0; c < kChains; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + c;
+          float &z = y[(i >> 1) * H + (j >> 1) % H][2 * (j & 1) + (i & 1)];
+          z = (j >> 1) / H == 0 ? s[c][i] : r == (j >> 1) / H ? s[c][i] : z;
+        }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -358,9 +370,9 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
 // Few columns per sequence: single and drafted tokens.  Every key and value is read once and used for
 // at most 16 columns, so HBM bounds long contexts in principle; what it measured (group 4, heads of
 // 128): 64 ragged contexts of 300 .. 12288 tokens 97 us for 461 MB, 4.8 TB/s (a copy of the kernel that
-// only loads takes the same); one token over 131071 39 us for 138 MB, 8.5 of them the join; one over
-// 777 12 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
-// 256 (12 sequences of 500 .. 9001 tokens): 40 us for 53 MB, bound by one wave a SIMD.
+// only loads takes the same); one token over 131071 40 us for 138 MB, 8.5 of them the join; one over
+// 777 10.9 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
+// 256 (12 sequences of 500 .. 9001 tokens): 39 us for 53 MB, bound by one wave a SIMD.
 //
 // All sequences' (head, column tile, key tile) units stand in one line; each workgroup takes an
 // equal stretch of it, whatever the lengths, and its four waves take the stretch's key tiles in
@@ -445,8 +457,9 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   c.s = -1;
   int least = kMinChunkLong;
   bool small = n_seq <= 64;
+  Seq lane_seq{};  // the lane's sequence, where every wave holds all
   if (small) {  // every wave by itself, a lane a sequence
-    Seq q{};
+    Seq &q = lane_seq;
     int we = 0, wr = 0;
     if (lane < n_seq) q = seq_of<C>(g, lane, blockIdx.x == 0 && wave == 0 && g.tends);
     if (!__any(q.col_tiles && q.tiles > kLong)) least = kMinChunk;
@@ -565,7 +578,7 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
           n.head = 0;
           do {
             if (++n.s >= n_seq) return;  // (the lengths changed under the call)
-            n.q = seq_from(seq_of<C>(g, n.s, false), 0);
+            n.q = small ? seq_from(lane_seq, n.s) : seq_from(seq_of<C>(g, n.s, false), 0);
           } while (n.q.col_tiles == 0);
           n.per = whole ? padded(n.q.tiles, least) : ahead + n.q.tiles;
         }

@@ -25,7 +25,7 @@ namespace trellis {
 
 namespace {
 
-constexpr int kColTiles = 1, kWideCols = 64 * kColTiles, kWideThreads = 256;  // column tiles a wave
+constexpr int kWideCols = 64, kWideThreads = 256;  // 16 columns a wave
 
 constexpr uint32_t kOdd = 1, kBad = 2;  // a value scale is not finite; the subtile has no page
 
@@ -183,184 +183,178 @@ __device__ __forceinline__ void read_codes(const char *vp, int swizzle, v2i (&c)
 // odd: some value scale is not finite.
 template <int NB>
 __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB> &lds, int buf, int k0, bool mask, uint32_t bad, bool odd,
-                                          const Query<NB> (&query)[kColTiles], const int (&pos)[kColTiles],
-                                          const float (&f)[NB], const float (&keep)[NB], const int (&e_run)[NB], float (&m)[kColTiles],
-                                          float (&l)[kColTiles], floatx4 (&o)[kColTiles][NB][8]) {
-  constexpr int CT = kColTiles;
+                                          const Query<NB> &query, int pos,
+                                          const float (&f)[NB], const float (&keep)[NB], const int (&e_run)[NB], float &m,
+                                          float &l, floatx4 (&o)[NB][8]) {
   const int lane = opaque_tid() & 63;
   const float log2f = (float)max(134 - e_run[0], -60);  // (2^-60: weights stay far from the smallest number)
-        half8 w[CT][NB][4];
+  half8 w[NB][4];
+  // ---- scores, from the running maximum (or from 0) as the weights' powers of two
+  const float mu = m == kNegInf ? 0.f : m, c0 = log2f - mu + query.add;
+  float y[8][4];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          // ---- scores, from the running maximum (or from 0) as the weights' powers of two
-          const float mu = m[ct] == kNegInf ? 0.f : m[ct], c0 = log2f - mu + query[ct].add;
-          float y[8][4];
+  for (int nb = 0; nb < NB; ++nb) {
+    // Products j = 2 p, 2 p + 1 together.  The order is kept as written: the next two's keys are
+    // on their way during the products, and two chains of three products alternate; left to
+    // itself the compiler waits for every load and every product.
+    const int row = lane & 15, sub = row >> 1;
+    const char *kp = lds.k[buf][nb] + sub * 1024;
+    const float *sp = lds.ks[buf][nb] + (lane >> 4) * 32;
+    v4i kv[2][2];
+    floatx4 s4[2][2], z[2][2];
+    const auto load = [&](int p) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            // Products j = 2 p, 2 p + 1 together.  The order is kept as written: the next two's keys are
-            // on their way during the products, and two chains of three products alternate; left to
-            // itself the compiler waits for every load and every product.
-            const int row = lane & 15, sub = row >> 1;
-            const char *kp = lds.k[buf][nb] + sub * 1024;
-            const float *sp = lds.ks[buf][nb] + (lane >> 4) * 32;
-            v4i kv[2][2];
-            floatx4 s4[2][2], z[2][2];
-            const auto load = [&](int p) {
+      for (int h = 0; h < 2; ++h) {
+        const int c = (8 * h + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
+        kv[p & 1][h] = *reinterpret_cast<const v4i *>(kp + p * 256 + c * 16);
+      }
+    };
+    load(0);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c = (8 * h + 4 * (row & 1) + (lane >> 4)) ^ key_swizzle(sub);
-                kv[p & 1][h] = *reinterpret_cast<const v4i *>(kp + p * 256 + c * 16);
-              }
-            };
-            load(0);
+    for (int p = 0; p < 5; ++p) {
+      const int at = p & 1;
+      if (p < 4) {
+        if (p < 3) load(p + 1);
+        // keys 4 p .. + 3 and 16 + 4 p .. + 3 of the lane's
+        s4[at][0] = *reinterpret_cast<const floatx4 *>(sp + 4 * p);
+        s4[at][1] = *reinterpret_cast<const floatx4 *>(sp + 16 + 4 * p);
+        __builtin_amdgcn_sched_barrier(0);
+        const v8i a0 = {kv[at][0][0], kv[at][0][1], kv[at][0][2], kv[at][0][3], 0, 0, 0, 0};
+        const v8i a1 = {kv[at][1][0], kv[at][1][1], kv[at][1][2], kv[at][1][3], 0, 0, 0, 0};
+        const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+        const int scale = query.scale[nb];
+        z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query.part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
+        z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query.part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
+        z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query.part[nb][1], z[at][0], 4, 2, 0, scale_byte(0), 1, scale);
+        z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query.part[nb][1], z[at][1], 4, 2, 0, scale_byte(0), 1, scale);
+        z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query.part[nb][2], z[at][0], 4, 2, 0, scale_byte(0), 2, scale);
+        z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query.part[nb][2], z[at][1], 4, 2, 0, scale_byte(0), 2, scale);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (p > 0) {
 #pragma unroll
-            for (int p = 0; p < 5; ++p) {
-              const int at = p & 1;
-              if (p < 4) {
-                if (p < 3) load(p + 1);
-                // keys 4 p .. + 3 and 16 + 4 p .. + 3 of the lane's
-                s4[at][0] = *reinterpret_cast<const floatx4 *>(sp + 4 * p);
-                s4[at][1] = *reinterpret_cast<const floatx4 *>(sp + 16 + 4 * p);
-                __builtin_amdgcn_sched_barrier(0);
-                const v8i a0 = {kv[at][0][0], kv[at][0][1], kv[at][0][2], kv[at][0][3], 0, 0, 0, 0};
-                const v8i a1 = {kv[at][1][0], kv[at][1][1], kv[at][1][2], kv[at][1][3], 0, 0, 0, 0};
-                const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-                const int scale = query[ct].scale[nb];
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][0], zero, 4, 2, 0, scale_byte(0), 0, scale);
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][1], z[at][0], 4, 2, 0, scale_byte(0), 1, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][1], z[at][1], 4, 2, 0, scale_byte(0), 1, scale);
-                z[at][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a0, query[ct].part[nb][2], z[at][0], 4, 2, 0, scale_byte(0), 2, scale);
-                z[at][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a1, query[ct].part[nb][2], z[at][1], 4, 2, 0, scale_byte(0), 2, scale);
-                __builtin_amdgcn_sched_barrier(0);
-              }
-              if (p > 0) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    float &to = y[2 * (p - 1) + h][i];
-                    to = fmaf(z[at ^ 1][h][i], s4[at ^ 1][i >> 1][2 * h + (i & 1)], nb ? to : c0);
-                  }
-              }
-              __builtin_amdgcn_sched_barrier(0);
-            }
+          for (int i = 0; i < 4; ++i) {
+            float &to = y[2 * (p - 1) + h][i];
+            to = fmaf(z[at ^ 1][h][i], s4[at ^ 1][i >> 1][2 * h + (i & 1)], nb ? to : c0);
           }
-          // ---- softmax
-          if (mask) {
-      asm volatile("");  // (a branch, not 32 selects on every tile)
-      const int kk = k0 + 32 * (lane >> 4), rel = pos[ct] - kk;
-      const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
-      const uint32_t gone = bad >> (2 * (lane >> 4));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 16 * (i >> 1) + 2 * j + (i & 1);
-          y[j][i] = ((k <= rel) & ((k > after) | (k < sink)) & !((gone >> (i >> 1)) & 1)) ? y[j][i] : kNegInf;
-        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    // The running maximum stays until a lane's weights outgrow 2^7 together: most tiles then need
-    // neither a maximum nor a rescaling.  The power of two f[0] is taken into the exponent.
-    float add = 0.f, alpha = 1.f;
-    float x[8][4];
+  }
+  // ---- softmax
+  if (mask) {
+    asm volatile("");  // (a branch, not 32 selects on every tile)
+    const int kk = k0 + 32 * (lane >> 4), rel = pos - kk;
+    const int after = g.a.window ? rel - g.a.window : -0x40000000, sink = g.a.window ? g.a.sinks - kk : 0;
+    const uint32_t gone = bad >> (2 * (lane >> 4));
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[j][i] = __builtin_amdgcn_exp2f(y[j][i]);
+        const int k = 16 * (i >> 1) + 2 * j + (i & 1);
+        y[j][i] = ((k <= rel) & ((k > after) | (k < sink)) & !((gone >> (i >> 1)) & 1)) ? y[j][i] : kNegInf;
+      }
+  }
+  // The running maximum stays until a lane's weights outgrow 2^7 together: most tiles then need
+  // neither a maximum nor a rescaling.  The power of two f[0] is taken into the exponent.
+  float add = 0.f, alpha = 1.f;
+  float x[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[j][i] = __builtin_amdgcn_exp2f(y[j][i]);
+      add += x[j][i];
+    }
+  const float one = __builtin_amdgcn_exp2f(log2f);  // a weight of 1
+  if (__any(!(add <= 128.f * one) | (m == kNegInf))) {
+    float top = kNegInf;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
+    top = max4(top);
+    // By how much the maximum grows (where there was none, from 0).  A column that does not need it
+    // stays as it is, so that no column's result depends on which others are beside it.
+    const bool first = m == kNegInf, need = max4u(!(add <= 128.f * one) | first) != 0;
+    const float by = first ? top - log2f : need ? fmaxf(top - log2f, 0.f) : 0.f, up = by == kNegInf ? 0.f : by;
+    alpha = first ? 0.f : __builtin_amdgcn_exp2f(-up);
+    m = first ? by : m + up;
+    add = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[j][i] = __builtin_amdgcn_exp2f(y[j][i] - up);
         add += x[j][i];
       }
-    const float one = __builtin_amdgcn_exp2f(log2f);  // a weight of 1
-    if (__any(!(add <= 128.f * one) | (m[ct] == kNegInf))) {
-      float top = kNegInf;
+  }
+  l = fmaf(l, alpha, add * __builtin_amdgcn_exp2f(-log2f));
+  // ---- weights
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(fmaxf(fmaxf(top, y[j][0]), fmaxf(y[j][1], y[j][2])), y[j][3]);
-      top = max4(top);
-      // By how much the maximum grows (where there was none, from 0).  A column that does not need it
-      // stays as it is, so that no column's result depends on which others are beside it.
-      const bool first = m[ct] == kNegInf, need = max4u(!(add <= 128.f * one) | first) != 0;
-      const float by = first ? top - log2f : need ? fmaxf(top - log2f, 0.f) : 0.f, up = by == kNegInf ? 0.f : by;
-      alpha = first ? 0.f : __builtin_amdgcn_exp2f(-up);
-      m[ct] = first ? by : m[ct] + up;
-      add = 0.f;
+  for (int nb = 0; nb < NB; ++nb) {
+    float vs[32];
+    read_scales32(lds.vs[buf][nb], vs);
+    if (nb == 0 && e_run[0] > 194) {  // what the exponent's bound left
+      asm volatile("");
+      const float rest = f[0] * __builtin_amdgcn_exp2f(-log2f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[j][i] = __builtin_amdgcn_exp2f(y[j][i] - up);
-          add += x[j][i];
-        }
+      for (int k = 0; k < 32; ++k) vs[k] *= rest;
     }
-    l[ct] = fmaf(l[ct], alpha, add * __builtin_amdgcn_exp2f(-log2f));
-    // ---- weights
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float vs[32];
-      read_scales32(lds.vs[buf][nb], vs);
-      if (nb == 0 && e_run[0] > 194) {  // what the exponent's bound left
-        asm volatile("");
-        const float rest = f[0] * __builtin_amdgcn_exp2f(-log2f);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) vs[k] *= rest;
-      }
-      if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
-        asm volatile("");
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vs[key32(j, i)] = x[j][i] == 0.f ? 0.f : vs[key32(j, i)];
-      }
+    if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
+      asm volatile("");
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u = x[j][i] * vs[key32(j, i)];
-          if (nb) u *= f[nb] * __builtin_amdgcn_exp2f(-log2f);
-          // step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
-          w[ct][nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
-        }
-        const float r = alpha * keep[nb];
-            if (__any(r != 1.f))
+        for (int i = 0; i < 4; ++i) vs[key32(j, i)] = x[j][i] == 0.f ? 0.f : vs[key32(j, i)];
+    }
 #pragma unroll
-              for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] *= r;
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // (keeps the phases' registers apart)
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u = x[j][i] * vs[key32(j, i)];
+        if (nb) u *= f[nb] * __builtin_amdgcn_exp2f(-log2f);
+        // step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
+        w[nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
+      }
+    const float r = alpha * keep[nb];
+    if (__any(r != 1.f))
+#pragma unroll
+      for (int dt = 0; dt < 8; ++dt) o[nb][dt] *= r;
+  }
+  __builtin_amdgcn_sched_barrier(0);  // (keeps the phases' registers apart)
   // ---- values
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int row = lane & 15, sub = 2 * (lane >> 4);
-          const char *vp = lds.v[buf][nb] + sub * 1024 + row * 64;
-          // Elements' tiles dt = 2 p, 2 p + 1 together, and the next word's codes turned to fp16 during
-          // a word's products.
-          v2i codes[4][2][2];
-          read_codes(vp, row >> 2, codes);
-          half8 a[2][2];
-          const auto unpack = [&](int step) {  // word step & 3 of pair step >> 2
+  for (int nb = 0; nb < NB; ++nb) {
+    const int row = lane & 15, sub = 2 * (lane >> 4);
+    const char *vp = lds.v[buf][nb] + sub * 1024 + row * 64;
+    // Elements' tiles dt = 2 p, 2 p + 1 together, and the next word's codes turned to fp16 during
+    // a word's products.
+    v2i codes[4][2][2];
+    read_codes(vp, row >> 2, codes);
+    half8 a[2][2];
+    const auto unpack = [&](int step) {  // word step & 3 of pair step >> 2
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const uint32_t c = codes[step >> 2][d][(step >> 1) & 1][step & 1];
-              const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
-              const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
-              a[step & 1][d] = half8{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-            }
-          };
-          unpack(0);
+      for (int d = 0; d < 2; ++d) {
+        const uint32_t c = codes[step >> 2][d][(step >> 1) & 1][step & 1];
+        const half2_t a0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 1);
+        const half2_t a2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, 1.f, 3);
+        a[step & 1][d] = half8{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+      }
+    };
+    unpack(0);
 #pragma unroll
-          for (int step = 0; step < 16; ++step) {
-            const int p = step >> 2;
-            if (step < 15) unpack(step + 1);
-            __builtin_amdgcn_sched_barrier(0);
+    for (int step = 0; step < 16; ++step) {
+      const int p = step >> 2;
+      if (step < 15) unpack(step + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct)
-                o[ct][nb][2 * p + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[step & 1][d], w[ct][nb][step & 3], o[ct][nb][2 * p + d], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
+      for (int d = 0; d < 2; ++d)
+        o[nb][2 * p + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[step & 1][d], w[nb][step & 3], o[nb][2 * p + d], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
 }
 
 template <int NB>
@@ -368,7 +362,7 @@ constexpr int wide_waves() { return NB == 1 ? 3 : 2; }  // a SIMD
 
 template <bool BF, int NB>
 __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wide_kernel(AttnArgs g) {
-  constexpr int D = 128 * NB, CT = kColTiles;
+  constexpr int D = 128 * NB;
   extern __shared__ __attribute__((aligned(16))) char raw[];
   WideLds<NB> &lds = *reinterpret_cast<WideLds<NB> *>(raw);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -420,41 +414,33 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   Share x;
   int entry = 0;
   if (t0 < t1) entry = share_entry(g, q, tile_at(q, t0));
-  Query<NB> query[CT];
-  int pos[CT];  // of the lane's column, -1: it sees nothing
+  Query<NB> query;
+  QueryRaw<NB> r[4];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int c0 = (wave * CT + ct) * kCols, c = c0 + (lane & 15);
-    QueryRaw<NB> r[4];
+  for (int k = 0; k < 4; ++k) r[k] = load_query<NB>(g, q, head, from, wave * kCols + 4 * k + (lane >> 4));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r[k] = load_query<NB>(g, q, head, from, c0 + 4 * k + (lane >> 4));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) stage_query<BF, NB>(g, r[k], 4 * k + (lane >> 4), lds.o[wave]);
-    __builtin_amdgcn_wave_barrier();
-    take_query<NB>(lds.o[wave], query[ct]);
-    __builtin_amdgcn_wave_barrier();
-    pos[ct] = c < cols ? q.len - q.n + column_at(g, from, c).row : -1;
-  }
+  for (int k = 0; k < 4; ++k) stage_query<BF, NB>(g, r[k], 4 * k + (lane >> 4), lds.o[wave]);
+  __builtin_amdgcn_wave_barrier();
+  take_query<NB>(lds.o[wave], query);
+  const int mine = wave * kCols + (lane & 15);
+  const int pos = mine < cols ? q.len - q.n + column_at(g, from, mine).row : -1;  // -1: sees nothing
   __syncthreads();
-  floatx4 o[CT][NB][8];
-  float m[CT], l[CT];
+  floatx4 o[NB][8];
+  float m, l;
   int e_run[NB];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt) o[ct][nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    m[ct] = pos[ct] < 0 ? 0.f : kNegInf;  // (a column past the last never sees a score)
-    l[ct] = 0.f;
-  }
+    for (int dt = 0; dt < 8; ++dt) o[nb][dt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  m = pos < 0 ? 0.f : kNegInf;  // (a column past the last never sees a score)
+  l = 0.f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) e_run[nb] = 127;
   if (t0 < t1) load_share(g, q.lo, base, tile_at(q, t0), entry, lds.t, 0, x);
   if (t0 + 1 < t1) entry = share_entry(g, q, tile_at(q, t0 + 1));
-  const int wp0 = q.len - q.n + column_at(g, from, min(wave * CT * kCols, cols - 1)).row;
-  const int wp1 = q.len - q.n + column_at(g, from, min((wave + 1) * CT * kCols, cols)).row;  // (one more at most)
-  const bool idle = wave * CT * kCols >= cols;  // no column of this wave's
+  const int wp0 = q.len - q.n + column_at(g, from, min(wave * kCols, cols - 1)).row;
+  const int wp1 = q.len - q.n + column_at(g, from, min((wave + 1) * kCols, cols)).row;  // (one more at most)
+  const bool idle = wave * kCols >= cols;  // no column of this wave's
   for (int t = t0; t < t1; ++t) {
     const int buf = (t - t0) & 1, tile = tile_at(q, t), k0 = tile * kTile;
     put_share(g, q, tile, x, lds.t, buf);
@@ -496,41 +482,38 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     }
   }
   // ---- results: back to the values' units, through shared memory, 16 lanes a column
+  l = sum4(l);
+  __syncthreads();
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    l[ct] = sum4(l[ct]);
-    __syncthreads();
+  for (int nb = 0; nb < NB; ++nb) {
+    const float f = __builtin_bit_cast(float, (uint32_t)max(e_run[nb] - 7, 1) << 23);
+#pragma unroll
+    for (int dt = 0; dt < 8; ++dt)
+      *reinterpret_cast<floatx4 *>(&lds.o[wave][nb][lane & 15][16 * dt + 4 * (lane >> 4)]) = o[nb][dt] * f;
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int i = lane & 15;
+  for (int p = 0; p < 4; ++p) {
+    const int c = 4 * p + (lane >> 4), at = wave * kCols + c;
+    const float mm = __shfl(m, c, 64), ll = __shfl(l, c, 64);
+    if (at >= cols) continue;  // (16 lanes together)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float f = __builtin_bit_cast(float, (uint32_t)max(e_run[nb] - 7, 1) << 23);
-#pragma unroll
-      for (int dt = 0; dt < 8; ++dt)
-        *reinterpret_cast<floatx4 *>(&lds.o[wave][nb][lane & 15][16 * dt + 4 * (lane >> 4)]) = o[ct][nb][dt] * f;
-    }
-    __builtin_amdgcn_wave_barrier();
-    const int i = lane & 15;
-    for (int p = 0; p < 4; ++p) {
-      const int c = 4 * p + (lane >> 4), at = (wave * CT + ct) * kCols + c;
-      const float mm = __shfl(m[ct], c, 64), ll = __shfl(l[ct], c, 64);
-      if (at >= cols) continue;  // (16 lanes together)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const floatx4 a = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i]);
-        const floatx4 b = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i + 4]);
-        float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        if (g.splits == 1) {
-          write_block<BF>(g, q, head, column_at(g, from, at), nb, v, mm, ll);
-        } else {
-          const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)(blockIdx.x / g.splits) * g.splits * kWideCols * (D + 8),
-                                                        (long long)g.splits * kWideCols * (D + 8) * 4);
-          const int to = ((split * kWideCols + at) * (D + 8)) * 4;
-          const u32x4 x0 = {__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]), __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
-          const u32x4 x1 = {__builtin_bit_cast(uint32_t, v[4]), __builtin_bit_cast(uint32_t, v[5]), __builtin_bit_cast(uint32_t, v[6]), __builtin_bit_cast(uint32_t, v[7])};
-          __builtin_amdgcn_raw_buffer_store_b128(x0, rs, to + (nb * 128 + 8 * i) * 4, 0, kSC1);
-          __builtin_amdgcn_raw_buffer_store_b128(x1, rs, to + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
-          if (nb == 0 && i == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, mm), __builtin_bit_cast(uint32_t, ll)}, rs, to + D * 4, 0, kSC1);
-        }
+      const floatx4 a = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i]);
+      const floatx4 b = *reinterpret_cast<const floatx4 *>(&lds.o[wave][nb][c][8 * i + 4]);
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      if (g.splits == 1) {
+        write_block<BF>(g, q, head, column_at(g, from, at), nb, v, mm, ll);
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)(blockIdx.x / g.splits) * g.splits * kWideCols * (D + 8),
+                                                      (long long)g.splits * kWideCols * (D + 8) * 4);
+        const int to = ((split * kWideCols + at) * (D + 8)) * 4;
+        const u32x4 x0 = {__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]), __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
+        const u32x4 x1 = {__builtin_bit_cast(uint32_t, v[4]), __builtin_bit_cast(uint32_t, v[5]), __builtin_bit_cast(uint32_t, v[6]), __builtin_bit_cast(uint32_t, v[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(x0, rs, to + (nb * 128 + 8 * i) * 4, 0, kSC1);
+        __builtin_amdgcn_raw_buffer_store_b128(x1, rs, to + (nb * 128 + 8 * i + 4) * 4, 0, kSC1);
+        if (nb == 0 && i == 0)
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, mm), __builtin_bit_cast(uint32_t, ll)}, rs, to + D * 4, 0, kSC1);
       }
     }
   }
@@ -547,7 +530,6 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   __syncthreads();
   if (!__builtin_amdgcn_readfirstlane(lds.last)) return;
   const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(g.parts + (size_t)seg * g.splits * kWideCols * (D + 8), (long long)g.splits * kWideCols * (D + 8) * 4);
-  const int i = tid & 15;
   for (int c = tid >> 4; c < cols; c += kWideThreads / 16) {
     float mm = kNegInf, ll = 0.f, acc[NB][8];
 #pragma unroll

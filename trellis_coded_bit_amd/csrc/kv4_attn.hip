@@ -181,14 +181,19 @@ struct Sums {
 // A tile's values as the left operand of the second product: rows are elements 16 dt + (l & 15);
 // the lane's depth holds the keys that the weights' E4M3 operand has there: two whole subtiles,
 // read transposed.
+// Tiles dt = 2 p, 2 p + 1 of block nb.
 template <int NB, int R>
-__device__ __forceinline__ v8i read_values(const WaveLds<NB, R> &lds, int nb, int dt) {
+__device__ __forceinline__ void read_values(const WaveLds<NB, R> &lds, int nb, int p, v8i (&v)[2]) {
   const int lane = opaque_tid() & 63, r = lane & 15;
-  const char *p = lds.v + (4 * ((lane >> 4) & 1) + (lane >> 5)) * 1024 + r * 64 + (((dt >> 1) ^ (r >> 2)) * 16);
+  typedef __attribute__((address_space(3))) const char lds_char;
   typedef __attribute__((address_space(3))) v2i lds_v2i;
-  const v2i a = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(p + nb * 8192 + (dt & 1) * 8));
-  const v2i b = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(p + nb * 8192 + (dt & 1) * 8 + 2048));
-  return v8i{a[0], a[1], b[0], b[1], 0, 0, 0, 0};
+  lds_char *at = (lds_char *)lds.v + (4 * ((lane >> 4) & 1) + (lane >> 5)) * 1024 + r * 64 + ((p ^ (r >> 2)) * 16) + nb * 8192;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const v2i a = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + d * 8));
+    const v2i b = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i *)(at + d * 8 + 2048));
+    v[d] = v8i{a[0], a[1], b[0], b[1], 0, 0, 0, 0};
+  }
 }
 
 // Scores of a lane's own keys (own word t's key i), in powers of two.
@@ -352,27 +357,38 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
     if (__any(alpha != 1.f))  // (rare once the first tiles are done)
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) sum.o[nb][dt] *= alpha;
+    // two tiles of elements at a time, the next two's reads under way
+    v8i v[2][2];
+    read_values(lds, nb, 0, v[0]);
 #pragma unroll
-    for (int dt = 0; dt < 8; ++dt) {
-      const v8i v = read_values(lds, nb, dt);
-      floatx4 o = sum.o[nb][dt];
-      o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p0, o, 4, 0, 0, scale_byte(0), 0, b0);
-      if constexpr (R == 2) o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p1, o, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
-      if constexpr (R == 1) {
-        o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p1, o, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 5);
-        o = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, p2, o, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
+    for (int p = 0; p < 4; ++p) {
+      if (p < 3) read_values(lds, nb, p + 1, v[(p + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      floatx4 &o0 = sum.o[nb][2 * p], &o1 = sum.o[nb][2 * p + 1];
+      const v8i &v0 = v[p & 1][0], &v1 = v[p & 1][1];
+      o0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v0, p0, o0, 4, 0, 0, scale_byte(0), 0, b0);
+      o1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v1, p0, o1, 4, 0, 0, scale_byte(0), 0, b0);
+      if constexpr (R == 2) {
+        o0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v0, p1, o0, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
+        o1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v1, p1, o1, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
       }
-      sum.o[nb][dt] = o;
+      if constexpr (R == 1) {
+        o0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v0, p1, o0, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 5);
+        o1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v1, p1, o1, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 5);
+        o0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v0, p2, o0, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
+        o1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v1, p2, o1, 4, 0, 0, scale_byte(0), 0, vbyte[nb] - 10);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
 // Few columns per sequence: single and drafted tokens.  Every key and value is read once and used for
 // at most 16 columns, so HBM bounds long contexts in principle; what it measured (group 4, heads of
-// 128): 64 ragged contexts of 300 .. 12288 tokens 97 us for 461 MB, 4.8 TB/s (a copy of the kernel that
+// 128): 64 ragged contexts of 300 .. 12288 tokens 95 us for 461 MB, 4.9 TB/s (a copy of the kernel that
 // only loads takes the same); one token over 131071 40 us for 138 MB, 8.5 of them the join; one over
-// 777 10.9 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
-// 256 (12 sequences of 500 .. 9001 tokens): 39 us for 53 MB, bound by one wave a SIMD.
+// 777 10.8 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
+// 256 (12 sequences of 500 .. 9001 tokens): 38 us for 53 MB, bound by one wave a SIMD.
 //
 // All sequences' (head, column tile, key tile) units stand in one line; each workgroup takes an
 // equal stretch of it, whatever the lengths, and its four waves take the stretch's key tiles in

@@ -9,7 +9,7 @@
 // different: per column a tile's three-way split of the weights costs as many
 // vector instructions as turning the values to fp16 does, and its products twice the time.  So a
 // value tile's codes are read transposed and turned to fp16 in registers (exactly), and the weights
-// p vs are rounded once to fp16 (within 2^-12), with one power of two per wave that follows the
+// p vs are rounded once to fp16 (within 2^-11), with one power of two per wave that follows the
 // tiles' largest value scale.
 //
 // The vector instructions bound it: 586 a tile and wave with starts and ends, 128 of them the values'
@@ -179,12 +179,27 @@ __device__ __forceinline__ void read_codes(const char *vp, int swizzle, v2i (&c)
       : "memory");
 }
 
+// By how many powers of two a wave's sums of a block can grow and stay below 2^126, so that later tiles
+// (2^42 at most, all together) still add up to a finite number.  Sums that are not finite stay so.
+__device__ __forceinline__ int sums_room(const floatx4 (&o)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = o[dt][i];
+      const uint32_t u = __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+      top = max(top, u < 0x7F800000u ? u : 0u);
+    }
+  top = max4u(kv4_max16(top));
+  return max(252 - (int)(__builtin_amdgcn_readfirstlane(top) >> 23), 0);
+}
+
 // One tile into a wave's sums.  mask: some row does not see some key; bad: subtiles without a page;
 // odd: some value scale is not finite.
 template <int NB>
 __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB> &lds, int buf, int k0, bool mask, uint32_t bad, bool odd,
-                                          const Query<NB> &query, int pos,
-                                          const float (&f)[NB], const float (&keep)[NB], const int (&e_run)[NB], float &m,
+                                          const Query<NB> &query, int pos, const float (&f)[NB], const int (&e_run)[NB], float &m,
                                           float &l, floatx4 (&o)[NB][8]) {
   const int lane = opaque_tid() & 63;
   const float log2f = (float)max(134 - e_run[0], -60);  // (2^-60: weights stay far from the smallest number)
@@ -302,6 +317,19 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
 #pragma unroll
       for (int k = 0; k < 32; ++k) vs[k] *= rest;
     }
+    // Block 1 turns from block 0's power of two to its own: in one factor where that neither leaves a
+    // float's range nor lets x vs leave it, otherwise its own first.
+    float turn = 1.f;
+    if (nb) {
+      const int own = 134 - e_run[nb], by = own - max(134 - e_run[0], -60);
+      turn = __builtin_bit_cast(float, (uint32_t)(127 + min(max(by, -60), 60)) << 23);
+      if (by < -60 || by > 60) {
+        asm volatile("");
+        turn = __builtin_amdgcn_exp2f(-log2f);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) vs[k] *= f[nb];
+      }
+    }
     if (odd) {  // a hidden key's NaN must not reach the sums: no weight, no scale
       asm volatile("");
 #pragma unroll
@@ -314,14 +342,13 @@ __device__ __forceinline__ void wide_tile(const AttnArgs &g, const WideTiles<NB>
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float u = x[j][i] * vs[key32(j, i)];
-        if (nb) u *= f[nb] * __builtin_amdgcn_exp2f(-log2f);
+        if (nb) u *= turn;
         // step 2 (i >> 1) + (j >> 2), element 2 (j & 3) + (i & 1)
         w[nb][2 * (i >> 1) + (j >> 2)][2 * (j & 3) + (i & 1)] = (_Float16)u;
       }
-    const float r = alpha * keep[nb];
-    if (__any(r != 1.f))
+    if (__any(alpha != 1.f))
 #pragma unroll
-      for (int dt = 0; dt < 8; ++dt) o[nb][dt] *= r;
+      for (int dt = 0; dt < 8; ++dt) o[nb][dt] *= alpha;
   }
   __builtin_amdgcn_sched_barrier(0);  // (keeps the phases' registers apart)
   // ---- values
@@ -450,8 +477,9 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     if (t + 2 < t1) entry = share_entry(g, q, tile_at(q, t + 2));
     if (!idle && k0 <= wp1) {
       // ---- the value scales' power of two: the tile's largest finite one comes below 2^8; it stays
-      // unless the tiles' scales outgrow it or fall far below
-      float f[NB], keep[NB];
+      // unless the tiles' scales outgrow it or fall far below, and falls no further than the sums can
+      // grow (a tile of zeros, which has no size, leaves it alone)
+      float f[NB];
       uint32_t flags = 0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -463,12 +491,16 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
           for (int k = 0; k < 4; ++k) top = max(top, v[k]), any |= v[k];
         }
         flags |= any;
-        const int e = max((int)(__builtin_amdgcn_readfirstlane(top) >> 8), 32);
-        keep[nb] = 1.f;
-        if (e > e_run[nb] || e < e_run[nb] - 8) {
-          const int to = min(e + 2, 254), by = min(max(e_run[nb] - to, -126), 127);
-          keep[nb] = __builtin_bit_cast(float, (uint32_t)(127 + by) << 23);
-          e_run[nb] = to;
+        const int seen = (int)(__builtin_amdgcn_readfirstlane(top) >> 8), e = max(seen, 32);
+        if (seen != 0 && (e > e_run[nb] || e < e_run[nb] - 8)) {
+          asm volatile("");
+          int by = e_run[nb] - min(e + 2, 254);
+          if (by > 0) by = min(by, sums_room(o[nb]));
+          e_run[nb] -= by;
+#pragma unroll
+          for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nb][dt][i] = __builtin_ldexpf(o[nb][dt][i], by);
         }
         f[nb] = __builtin_bit_cast(float, (uint32_t)(261 - e_run[nb]) << 23);
       }
@@ -478,7 +510,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
       if (flags & kBad) bad = (uint32_t)__ballot(lane < 8 && (lds.t.about[buf][0][lane & 7] & kBad));
       const bool mask = !(k0 + kTile - 1 <= wp0 && bad == 0 &&
                           (g.a.window == 0 || k0 > wp1 - g.a.window || k0 + kTile <= g.a.sinks));
-      wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, query, pos, f, keep, e_run, m, l, o);
+      wide_tile<NB>(g, lds.t, buf, k0, mask, bad, odd, query, pos, f, e_run, m, l, o);
     }
   }
   // ---- results: back to the values' units, through shared memory, 16 lanes a column

@@ -1,0 +1,37 @@
+"""What include/trellis_kv4.h promises of calls whose arguments are not as they should be, or far from
+usual, on the GPU: a bound on the rows that is too small."""
+import pytest
+import torch
+
+from trellis_coded_bit_amd import binding as tb
+
+from gpu_util import log_case
+from test_gpu_kv4 import Setup, ints
+
+pytestmark = pytest.mark.gpu
+
+
+def test_many_rows_under_too_small_a_bound():
+    """max_rows chooses kernels and nothing else: a long prompt called with a bound of one row leaves no
+    row unwritten, of itself or of the sequence behind it.  Its 8 heads have 8 x 16300 column tiles of 4
+    over 128 tiles of keys: their count is below 2^24 and, with what a segment costs, above."""
+    log_case("attn bound too small")
+    length, Hk, heads = 16384, 8, 32
+    st = Setup([length, 300], T=256, Hk=Hk, seed=40)
+    new = [16300, 1]
+    g = torch.Generator(device="cuda").manual_seed(41)
+    q = torch.randn((sum(new), heads, 128), generator=g, device="cuda").half()
+    cu = ints([0, new[0], sum(new)])
+    want = tb.trellis_kv4_attn(st.cache, 0, st.table, st.lens, cu, q)
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full((sum(new), heads), float("nan"), device="cuda")
+    ws = torch.zeros(tb.trellis_kv4_attn_workspace_bytes(st.cache, st.table, st.lens, cu, sum(new), heads), dtype=torch.uint8,
+                     device="cuda")
+    y = tb.trellis_kv4_attn(st.cache, 0, st.table, st.lens, cu, q, max_q=1, out=out, lse=lse, ws=ws)
+    torch.cuda.synchronize()
+    assert not bool(torch.isnan(y).any()) and not bool(torch.isnan(lse).any())
+    assert bool((ws[:256 + 65536] == 0).all())  # no join is left waiting
+    # both are within the formats' bound (2e-3 of the result, over a tensor) of the exact one
+    for at in (0, 1, 8000, new[0] - 1, new[0]):
+        assert (y[at].double() - want[at].double()).norm() <= 4e-3 * want[at].double().norm(), at
+    assert (y.float() - want.float()).norm() <= 4e-3 * want.float().norm()

@@ -481,9 +481,10 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     if (!__any(q.col_tiles && q.tiles > kLong)) least = kMinChunk;
     if (lane < n_seq) {
       const long long segs = (long long)Hk * q.col_tiles;
-      small = segs * padded(q.tiles, least) < (1 << 24);
-      we = (int)min(segs * (kSegCost + q.tiles), 1LL << 24);
-      wr = (int)min(segs * padded(q.tiles, least), 1LL << 24);
+      const long long exact = segs * (kSegCost + q.tiles), round = segs * padded(q.tiles, least);
+      small = max(exact, round) < (1 << 24);  // (so that 64 of either add up in 32 bits)
+      we = small ? (int)exact : 0;
+      wr = small ? (int)round : 0;
     }
     small = __all(small);
     if (small) {

@@ -141,7 +141,8 @@ int trellis_kv4_compact(const trellis_kv4_cache *c, int32_t *table, int32_t *len
                         const int32_t *keep_cu, int n_keep, void *ws, size_t ws_bytes, void *stream);
 
 /* Release slots[0 .. n): their pages' counts drop by one, their lengths become 0 (their table
- * rows are left).  A slot named twice is released once.  One launch. */
+ * rows are left).  A slot named twice is released once.  One launch (the list is checked before
+ * anything is released). */
 int trellis_kv4_free(const trellis_kv4_cache *c, const int32_t *table, int32_t *lens, int n_slots, int max_pages,
                      int32_t *ref, const int32_t *slots, int n, void *ws, size_t ws_bytes, void *stream);
 

@@ -1,12 +1,12 @@
 """What include/trellis_kv4.h promises of calls whose arguments are not as they should be, or far from
-usual, on the GPU: a bound on the rows that is too small."""
+usual, on the GPU: a bound on the rows that is too small, and lists to release with a bad entry."""
 import pytest
 import torch
 
 from trellis_coded_bit_amd import binding as tb
 
 from gpu_util import log_case
-from test_gpu_kv4 import Setup, ints
+from test_gpu_kv4 import Setup, both, ints, random_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,30 @@ def test_many_rows_under_too_small_a_bound():
     for at in (0, 1, 8000, new[0] - 1, new[0]):
         assert (y[at].double() - want[at].double()).norm() <= 4e-3 * want[at].double().norm(), at
     assert (y.float() - want.float()).norm() <= 4e-3 * want.float().norm()
+
+
+@pytest.mark.parametrize("length", [None, -1, -(1 << 31), 16 * 5 + 1, 1 << 30])
+@pytest.mark.parametrize("n", [2, 4, 300, 1500])
+def test_free_refuses_as_a_whole(n, length):
+    """A list with a slot out of range, or a slot whose length is, releases none of the others."""
+    log_case(f"free refuses n={n} length={length}")
+    lens = [1 + (11 * i) % 48 for i in range(n)]
+    st = Setup(lens, T=16, Hk=1, spare=3, fill=False)  # (tables of five pages)
+    random_pool(st)
+    args = (st.cache, st.table, st.lens, st.ref)
+    slots = list(range(n))
+    bad = n // 2
+    if length is None:
+        slots[bad] = n
+    else:
+        st.lens[bad] = length
+    o, same = both(st)
+    tb.clear_error_word()
+    tb.trellis_kv4_free(*args, ints(slots))
+    same()
+    assert tb.error_word() == 4
+    tb.clear_error_word()
+    tb.trellis_kv4_free(*args, ints([i for i in range(n) if i != bad]))
+    o.free([i for i in range(n) if i != bad])
+    same()
+    assert tb.error_word() == 0

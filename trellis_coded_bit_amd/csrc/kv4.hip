@@ -441,16 +441,32 @@ __global__ __launch_bounds__(256) void kv4_compact_commit_kernel(Kv4Pages p, Pag
   if (threadIdx.x == 0) p.lens[d] = kept;
 }
 
+// Every workgroup checks the whole list before it releases its slots: what another one has released by
+// then is a length of zero, which is in range, so all of them come to the same verdict.
 __global__ __launch_bounds__(256) void kv4_free_kernel(Kv4Pages p, uint32_t *errword) {
-  const int d = p.dst[blockIdx.x];
-  if ((uint32_t)d >= (uint32_t)p.n_slots) {
-    if (threadIdx.x == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
+  __shared__ int bad, len;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  const long long cap = (long long)p.max_pages * p.c.page_size;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.n; i += 256) {
+    const int d = p.dst[i];
+    const bool ok = (uint32_t)d < (uint32_t)p.n_slots;
+    const int l = ok ? p.lens[d] : -1;
+    if (l < 0 || l > cap) bad = 1;
+  }
+  __syncthreads();
+  if (bad) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) kv4_error(errword, TRELLIS_KV4_ERR_BAD);
     return;
   }
-  __shared__ int len;
-  if (threadIdx.x == 0) len = atomicExch(&p.lens[d], 0);  // a slot named twice is empty the second time
-  __syncthreads();
-  release_pages(p, d, len, threadIdx.x, 256, errword);
+  for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
+    const int d = p.dst[i];
+    if (threadIdx.x == 0) len = atomicExch(&p.lens[d], 0);  // a slot named twice is empty the second time
+    __syncthreads();
+    release_pages(p, d, len, threadIdx.x, 256, errword);
+    __syncthreads();  // len is read
+  }
 }
 
 size_t bits_bytes(int n_slots) { return (size_t)((n_slots + 31) / 32) * 4; }
@@ -521,7 +537,7 @@ hipError_t launch_kv4_compact(const Kv4Pages &p, void *ws, hipStream_t stream) {
 }
 
 hipError_t launch_kv4_free(const Kv4Pages &p, uint32_t *errword, hipStream_t stream) {
-  kv4_free_kernel<<<p.n, 256, 0, stream>>>(p, errword);
+  kv4_free_kernel<<<p.n < 1024 ? p.n : 1024, 256, 0, stream>>>(p, errword);
   return hipGetLastError();
 }
 

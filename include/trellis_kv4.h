@@ -134,7 +134,8 @@ int trellis_kv4_fork(const trellis_kv4_cache *c, int32_t *table, int32_t *lens, 
 
 /* Slot dst[i] becomes the tokens keep[keep_cu[i] .. keep_cu[i+1]-1] (positions in slot src[i],
  * in any order) packed into new pages of its own, every layer's.  What dst held is released.
- * dst distinct; dst[i] may be src[i] (in place), not another src.  n_keep = keep_cu[n].
+ * dst distinct; dst[i] may be src[i] (in place), not another src.  n_keep = keep_cu[n], at most
+ * 2^27.
  * Three launches. */
 int trellis_kv4_compact(const trellis_kv4_cache *c, int32_t *table, int32_t *lens, int n_slots, int max_pages,
                         int32_t *ref, const int32_t *src, const int32_t *dst, int n, const int32_t *keep,

@@ -235,7 +235,8 @@ int trellis_kv4_compact(const trellis_kv4_cache *c, int32_t *table, int32_t *len
   abi_clear();
   int st = check_pages(c, table, lens, n_slots, max_pages, ref, n);
   if (st) return st;
-  if (n_keep < 0 || n_keep > (1 << 30)) return abi_fail(TRELLIS_EINVAL, "n_keep=%d not in 0..2^30", n_keep);
+  if (n_keep < 0 || n_keep > trellis::kKv4MaxKeep)
+    return abi_fail(TRELLIS_EINVAL, "n_keep=%d not in 0..%d", n_keep, trellis::kKv4MaxKeep);
   if (n == 0) return TRELLIS_OK;
   if ((st = check_list("src", src)) || (st = check_list("dst", dst)) || (st = check_list("keep_cu", keep_cu))) return st;
   if (n_keep > 0 && (st = check_list("keep", keep))) return st;

@@ -516,6 +516,7 @@ hipError_t launch_kv4_fork(const Kv4Pages &p, void *ws, hipStream_t stream) {
   const PagesPlan plan = plan_of(ws, p.n);
   uint32_t *err = static_cast<uint32_t *>(ws);
   kv4_plan_kernel<kFork><<<1, kPlanThreads, bits_bytes(p.n_slots), stream>>>(p, plan, err);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   const int units = p.c.n_layers * p.c.n_kv_heads;
   const dim3 grid(p.n, (units + 3) / 4 < 4096 ? (units + 3) / 4 : 4096);
   if (p.c.head_dim == 128) kv4_fork_kernel<1><<<grid, 256, 0, stream>>>(p, plan, err);
@@ -527,10 +528,13 @@ hipError_t launch_kv4_compact(const Kv4Pages &p, void *ws, hipStream_t stream) {
   const PagesPlan plan = plan_of(ws, p.n);
   uint32_t *err = static_cast<uint32_t *>(ws);
   kv4_plan_kernel<kCompact><<<1, kPlanThreads, bits_bytes(p.n_slots), stream>>>(p, plan, err);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (p.n_keep > 0) {
     const int units = p.c.n_layers * p.c.n_kv_heads * 2 * (p.c.head_dim / 128);
     const int y = (units + 15) / 16;
     kv4_compact_copy_kernel<<<dim3((p.n_keep + 15) / 16, y < 1024 ? y : 1024), 256, 0, stream>>>(p, plan, err);
+    // (the tables must not change to pages that nothing filled)
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   kv4_compact_commit_kernel<<<p.n, 256, 0, stream>>>(p, plan, err);
   return hipGetLastError();

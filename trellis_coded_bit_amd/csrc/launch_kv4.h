@@ -41,6 +41,8 @@ struct Kv4Pages {
   const int32_t *keep, *keep_cu;  // compact
   int n_keep;
 };
+// Tokens that one compaction keeps, at most: 16 threads each, in a grid of less than 2^32.
+constexpr int kKv4MaxKeep = 1 << 27;
 size_t kv4_pages_workspace_bytes(int n_pages, int n);
 hipError_t launch_kv4_reserve(const Kv4Pages &p, void *ws, hipStream_t stream);
 hipError_t launch_kv4_fork(const Kv4Pages &p, void *ws, hipStream_t stream);

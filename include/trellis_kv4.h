@@ -28,7 +28,8 @@
  * enqueued, a caller-owned zero-filled workspace that every entry point of the library can
  * share on one stream.  What only the device can see (page numbers, slots, lengths) is checked
  * in the kernels: a bad value is never used as an address; the row concerned is skipped (append,
- * a compaction's row) or zero (read, attn) and bit 4 of the workspace's error word is set.  The
+ * a compaction's row) or zero (read, attn) and bit 4 of the workspace's error word is set.  A cu that
+ * does not start at 0, descends or passes the rows ends a call of attn there: what follows is zero.  The
  * page operations refuse a call with a bad slot or length as a whole (bit 4), and one that
  * needs more free pages than there are (bit 8): nothing is changed then.
  */

@@ -1,5 +1,6 @@
 """What include/trellis_kv4.h promises of calls whose arguments are not as they should be, or far from
-usual, on the GPU: a bound on the rows that is too small, and lists to release with a bad entry."""
+usual, on the GPU: a bound on the rows that is too small, lists to release with a bad entry, and
+sequences' bounds out of order."""
 import pytest
 import torch
 
@@ -62,3 +63,46 @@ def test_free_refuses_as_a_whole(n, length):
     o.free([i for i in range(n) if i != bad])
     same()
     assert tb.error_word() == 0
+
+
+@pytest.mark.parametrize("max_q", [0, 1])
+@pytest.mark.parametrize("each", [1, 30])
+@pytest.mark.parametrize("n", [1, 3, 64, 65, 300, 700])
+@pytest.mark.parametrize("how", ["past the rows", "descending", "negative", "late start", "short"])
+def test_bounds_out_of_order(how, n, each, max_q):
+    """The sequences before the first bad bound are as ever; every row behind them is zero and says that
+    it saw nothing."""
+    log_case(f"attn bounds {how} n={n} each={each} max_q={max_q}")
+    st = Setup([40 + i % 50 for i in range(n)], T=16, Hk=1, seed=42)
+    rows = n * each
+    g = torch.Generator().manual_seed(43)
+    q = torch.randn((rows, 4, 128), generator=g).half().cuda()
+    cu = [i * each for i in range(n + 1)]
+    want = tb.trellis_kv4_attn(st.cache, 0, st.table, st.lens, ints(cu), q, max_q=max_q)
+    lse = torch.empty((rows, 4), device="cuda")
+    tb.trellis_kv4_attn(st.cache, 0, st.table, st.lens, ints(cu), q, lse=lse, max_q=max_q)
+    assert tb.error_word() == 0
+    at = 2 * n // 3  # the first sequence that is bad; its rows are from at * each on
+    if how == "past the rows":
+        cu[at + 1] = rows + 1
+    elif how == "descending":
+        if at == 0:
+            cu[1] = -1
+        else:
+            cu[at + 1] = cu[at] - 1
+    elif how == "negative":
+        cu[at + 1] = -(1 << 31)
+    elif how == "late start":
+        cu[0], at = 1, 0
+    else:
+        cu[n], at = rows - each, n - 1
+    y = torch.full_like(q, float("nan"))
+    got = torch.full_like(lse, float("nan"))
+    tb.trellis_kv4_attn(st.cache, 0, st.table, st.lens, ints(cu), q, max_q=max_q, out=y, lse=got)
+    assert tb.error_word() == 4
+    tb.clear_error_word()
+    good = at * each
+    assert torch.equal(y[good:], torch.zeros_like(y[good:])) and bool((got[good:] == -torch.inf).all())
+    # (the work may be split at other places: both are within the formats' bound of the exact result)
+    assert (y[:good].float() - want[:good].float()).norm() <= 4e-3 * want[:good].float().norm()
+    assert bool(((got[:good] - lse[:good]).abs() <= 1e-3 * (1 + lse[:good].abs())).all())

@@ -462,9 +462,8 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   extern __shared__ __attribute__((aligned(16))) char raw[];
   NarrowLds<NB, R> &lds = *reinterpret_cast<NarrowLds<NB, R> *>(raw);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n_seq = g.a.b.n_seq, Hk = g.a.c.n_kv_heads;
-  const int G = gridDim.x;
-  if (blockIdx.x == 0 && g.tends) clear_rest<NB, kThreads>(g);
+  int n_seq = g.a.b.n_seq;  // (those whose bounds are in order)
+  const int G = gridDim.x, Hk = g.a.c.n_kv_heads;
   // ---- the line's length, with and without segments rounded up to whole chunks, and the
   // sequence of this workgroup's first unit
   bool whole = false;  // short contexts: whole chunks to a segment
@@ -478,6 +477,12 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
     Seq &q = lane_seq;
     int we = 0, wr = 0;
     if (lane < n_seq) q = seq_of<C>(g, lane, blockIdx.x == 0 && wave == 0 && g.tends);
+    if (const uint64_t broken = __ballot(lane < n_seq && !q.ordered)) {
+      n_seq = __builtin_ctzll(broken);
+      if (lane >= n_seq) q = Seq{};
+    }
+    if (blockIdx.x == 0 && g.tends)
+      clear_rest<NB, kThreads>(g, n_seq, n_seq ? __builtin_amdgcn_readlane(q.c0 + q.n, n_seq - 1) : 0);
     if (!__any(q.col_tiles && q.tiles > kLong)) least = kMinChunk;
     if (lane < n_seq) {
       const long long segs = (long long)Hk * q.col_tiles;
@@ -510,19 +515,32 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
   }
   if (!small) {
     least = kMinChunkLong;
-    long long exact = 0, round = 0;
-    for (int s0 = 0; s0 < n_seq; s0 += kThreads) {
-      long long we = 0, wr = 0, t;
-      if (s0 + tid < n_seq) {
-        const Seq q = seq_of<C>(g, s0 + tid, blockIdx.x == 0 && g.tends);
-        we = (long long)Hk * q.col_tiles * (kSegCost + q.tiles);
-        wr = (long long)Hk * q.col_tiles * padded(q.tiles, least);
+    long long exact, round;
+    for (;;) {  // (twice where some bounds are out of order)
+      exact = round = 0;
+      int broken = n_seq;
+      if (tid == 0) lds.last = n_seq;
+      for (int s0 = 0; s0 < n_seq; s0 += kThreads) {
+        long long we = 0, wr = 0, t;
+        if (s0 + tid < n_seq) {
+          const Seq q = seq_of<C>(g, s0 + tid, blockIdx.x == 0 && g.tends);
+          if (!q.ordered) broken = min(broken, s0 + tid);
+          we = (long long)Hk * q.col_tiles * (kSegCost + q.tiles);
+          wr = (long long)Hk * q.col_tiles * padded(q.tiles, least);
+        }
+        block_prefix(we, lds.scan, &t);  // (its barriers put the store of lds.last before the minimum)
+        exact += t;
+        block_prefix(wr, lds.scan, &t);
+        round += t;
       }
-      block_prefix(we, lds.scan, &t);
-      exact += t;
-      block_prefix(wr, lds.scan, &t);
-      round += t;
+      if (broken < n_seq) atomicMin(&lds.last, broken);
+      __syncthreads();
+      const int ordered = __builtin_amdgcn_readfirstlane(lds.last);
+      if (ordered == n_seq) break;
+      n_seq = ordered;
+      __syncthreads();  // lds.last is read
     }
+    if (blockIdx.x == 0 && g.tends) clear_rest<NB, kThreads>(g, n_seq, n_seq ? ldg(g.a.b.cu + n_seq) : 0);
     whole = round <= (long long)least * G;
     U = whole ? round : exact;
     chunk = whole ? least : (exact + G - 1) / G;

@@ -34,23 +34,30 @@ struct Seq {
   int lo;                   // keys below lo are seen by no row but as sinks
   int n_sink, first, tiles; // key tiles: [0, n_sink), then first ..; `tiles` in all, at least one
   int col_tiles;            // tiles of C (row, head) columns of one key/value head; 0: not this kernel's
+  bool ordered;             // its bounds are in order: the first starts at row 0, and c0 <= end <= rows
 };
+
+// A sequence whose bounds are out of order, and those after it, have no rows (the ones before it then
+// share none): their rows are the rest that clear_rest clears.
+__device__ __forceinline__ bool bounds_ok(const AttnArgs &g, int s, int c0, int c1) {
+  return (s > 0 ? c0 >= 0 : c0 == 0) && c1 >= c0 && c1 <= g.a.b.rows;
+}
 
 template <int C>
 __device__ Seq seq_of(const AttnArgs &g, int s, bool flag) {
   const trellis_kv4_batch &b = g.a.b;
   Seq q;
   const int c0 = ldg(b.cu + s), c1 = ldg(b.cu + s + 1);
-  const bool rows_ok = c0 >= 0 && c1 >= c0 && c1 <= b.rows;
-  q.c0 = rows_ok ? c0 : 0;
-  q.n = rows_ok ? c1 - c0 : 0;
+  q.ordered = bounds_ok(g, s, c0, c1);
+  q.c0 = q.ordered ? c0 : 0;
+  q.n = q.ordered ? c1 - c0 : 0;
   q.slot = b.slots ? ldg(b.slots + s) : s;
   bool ok = (uint32_t)q.slot < (uint32_t)b.n_slots;
   q.slot = ok ? q.slot : 0;
   q.len = ldg(b.lens + q.slot);
   if (q.len < 0 || q.len > (long long)b.max_pages * g.a.c.page_size) ok = false;
   if (!ok) q.len = 0;
-  if (flag && !(ok && rows_ok)) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
+  if (flag && !(ok && q.ordered)) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
   const int lo = q.len - q.n - g.a.window + 1;  // of the first row
   q.lo = g.a.window && lo > 0 ? lo : 0;
   q.first = q.lo / kTile;
@@ -228,11 +235,10 @@ __device__ __forceinline__ v8i read8(const int *p) {
   return v8i{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// Clears the rows past the last sequence's (one workgroup).
+// Clears the rows from `end` on, where the n_seq sequences whose bounds are in order end (one workgroup).
 template <int NB, int THREADS>
-__device__ __forceinline__ void clear_rest(const AttnArgs &g) {
-  const int n_seq = g.a.b.n_seq, end = min(max(n_seq ? ldg(g.a.b.cu + n_seq) : 0, 0), g.a.b.rows);
-  if (end >= g.a.b.rows) return;
+__device__ __forceinline__ void clear_rest(const AttnArgs &g, int n_seq, int end) {
+  if (n_seq == g.a.b.n_seq && end == g.a.b.rows) return;
   if (threadIdx.x == 0) kv4_error(g.errword, TRELLIS_KV4_ERR_BAD);
   const size_t words = (size_t)g.a.n_q_heads * 64 * NB;
   for (size_t i = end * words + threadIdx.x; i < g.a.b.rows * words; i += THREADS) static_cast<uint32_t *>(g.a.y)[i] = 0;

@@ -393,8 +393,17 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
   extern __shared__ __attribute__((aligned(16))) char raw[];
   WideLds<NB> &lds = *reinterpret_cast<WideLds<NB> *>(raw);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n_seq = g.a.b.n_seq, Hk = g.a.c.n_kv_heads;
-  if (blockIdx.x == 0 && g.tends) clear_rest<NB, kWideThreads>(g);
+  const int Hk = g.a.c.n_kv_heads;
+  int n_seq = g.a.b.n_seq;  // (those whose bounds are in order)
+  if (n_seq > 64) {
+    int broken = n_seq;
+#pragma unroll 4
+    for (int r = lane; r < n_seq; r += 64)
+      if (!bounds_ok(g, r, ldg(g.a.b.cu + r), ldg(g.a.b.cu + r + 1))) broken = min(broken, r);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) broken = min(broken, __shfl_xor(broken, d, 64));
+    n_seq = __builtin_amdgcn_readfirstlane(broken);
+  }
   // ---- which columns: the last sequence's last ones first, as they see the most keys.  The head
   // varies fastest: with eight of them each XCD's cache has one head's keys.
   const int split = blockIdx.x % g.splits, head = blockIdx.x / g.splits % Hk;
@@ -407,6 +416,10 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     if (mine >= 0) {
       x = seq_of<kWideCols>(g, mine, blockIdx.x == 0 && wave == 0 && g.tends);
       tiles = x.col_tiles;
+    }
+    if (const uint64_t broken = __ballot(mine >= 0 && !x.ordered)) {  // (64 sequences or fewer)
+      n_seq = s1 - 64 + __builtin_clzll(broken);
+      if (mine >= n_seq) tiles = x.col_tiles = 0;
     }
     int p = tiles;
 #pragma unroll
@@ -425,6 +438,7 @@ __global__ __launch_bounds__(kWideThreads, (wide_waves<NB>())) void kv4_attn_wid
     if (blockIdx.x == 0 && g.tends && s >= 0 && s1 > 64)  // (the rest only to be checked)
       for (int r = s1 - 64 - 1 - lane; wave == 0 && r >= 0; r -= 64) seq_of<kWideCols>(g, r, true);
   }
+  if (blockIdx.x == 0 && g.tends) clear_rest<NB, kWideThreads>(g, n_seq, n_seq ? ldg(g.a.b.cu + n_seq) : 0);
   if (s < 0) return;
   const int col0 = (q.col_tiles - 1 - item) * kWideCols;
   const int cols = (int)min((long long)kWideCols, (long long)q.n * g.group - col0);

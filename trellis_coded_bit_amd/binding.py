@@ -175,16 +175,26 @@ def _req(t: torch.Tensor, dtype: torch.dtype, name: str, device=None) -> None:
 # ---------------------------------------------------------------------------------------
 
 _ws: Dict[Tuple[int, int], torch.Tensor] = {}
+# Buffers that a capture outgrew: nothing of them is recorded into the graph, and their error words
+# count until they are cleared.
+_ws_outgrown: Dict[Tuple[int, int], List[torch.Tensor]] = {}
 
 
 def workspace(nbytes: int, device: torch.device, op: int = 0) -> torch.Tensor:
     """One zero-filled workspace per (device, stream), grown on demand.  Every entry point
     leaves the reserved region at the start of a workspace as it found it, so all of them
-    share one buffer (``op`` is accepted for compatibility and ignored)."""
+    share one buffer (``op`` is accepted for compatibility and ignored).  Its error word goes on
+    with it when it grows.  (A graph should be given a workspace of the program's own: one made
+    during a capture is cleared by every replay.)"""
     key = (device.index if device.index is not None else torch.cuda.current_device(), _stream())
     w = _ws.get(key)
     if w is None or w.numel() < nbytes:
-        w = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        old, w = w, torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if old is not None:
+            if torch.cuda.is_current_stream_capturing():
+                _ws_outgrown.setdefault(key, []).append(old)
+            else:
+                w[:4].copy_(old[:4])
         _ws[key] = w
     return w
 
@@ -485,21 +495,28 @@ def trellis_moe_gemv(table: ExpertTable, routed: torch.Tensor, x: torch.Tensor, 
     return out
 
 
+def _error_words(ws: Optional[torch.Tensor], device) -> List[torch.Tensor]:
+    if ws is not None:
+        return [ws]
+    key = (torch.device(device).index or 0, _stream())
+    return ([_ws[key]] if key in _ws else []) + _ws_outgrown.get(key, [])
+
+
 def error_word(ws: Optional[torch.Tensor] = None, device="cuda") -> int:
     """The error word of a workspace (default: the current stream's shared one); it is
     sticky (bit 1: a bad routed id or table entry was skipped; bit 2: a bounded wait ran
-    out).  Synchronises."""
-    if ws is None:
-        ws = _ws.get((torch.device(device).index or 0, _stream()))
-    return 0 if ws is None else int(ws[:4].view(torch.int32).item())
+    out; bits 4 and 8: the key/value cache's, a bad place and too few free pages).
+    Synchronises."""
+    word = 0
+    for w in _error_words(ws, device):
+        word |= int(w[:4].view(torch.int32).item())
+    return word
 
 
 def clear_error_word(ws: Optional[torch.Tensor] = None, device="cuda") -> None:
     """Clear a workspace's error word (a fill on the current stream; graph-safe)."""
-    if ws is None:
-        ws = _ws.get((torch.device(device).index or 0, _stream()))
-    if ws is not None:
-        ws[:4].zero_()
+    for w in _error_words(ws, device):
+        w[:4].zero_()
 
 
 class MoEMLPTables:

@@ -712,7 +712,8 @@ def _kv4_rows(cache: KV4Cache, x: torch.Tensor, heads: Optional[int], name: str)
     row, head, last = x.stride()
     if last != 1:
         raise ValueError(f"{name}: each head's vector must be contiguous")
-    return row, head
+    # (one row or head: its stride is used for nothing and may be any number)
+    return row if x.shape[0] > 1 else 0, head if x.shape[1] > 1 else 0
 
 
 def trellis_kv4_append(cache: KV4Cache, layer: int, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,

@@ -8,9 +8,10 @@
 // and y = H y' at the end.
 //
 // Precision.  What meets the codes is split into parts, each the rounding of what the last one left: a
-// query into three of E2M3 (within 2^-12 of the block's largest element), with one power of two per
-// (row, block); a weight p_j vs_j into three of E4M3 (within 2^-12 of itself), with one power of two
-// per tile of 128 keys.  Products and sums are fp32, as are the maxima, the sums of weights and
+// query into three of E2M3 (within 2^-13.9 of the block's largest element), with one power of two per
+// (row, block); a weight p_j vs_j into three of E4M3 (within 2^-14 of itself as long as it is 2^-14 of the
+// tile's largest value scale, and of 2^-28 of that below: the last part's smallest step), with one power
+// of two per tile of 128 keys.  Products and sums are fp32, as are the maxima, the sums of weights and
 // everything that is joined.
 #include "kv4_attn_device.h"
 
@@ -808,6 +809,9 @@ __global__ __launch_bounds__(kThreads, (narrow_waves<NB, R>())) void kv4_attn_na
             }
           }
         // the shares, in order
+        using W = WaveLds<NB, R>;
+        static_assert(R == 1 || kThreads * (8 * NB + 2) * sizeof(float) <= offsetof(W, w) + sizeof(W::w) - sizeof(W::w[0]),
+                      "the shares must leave the first wave's zeros alone");
         float *all = reinterpret_cast<float *>(lds.wave);
         float *put = all + tid * (8 * NB + 2);
         if (sub > 0) {

@@ -111,7 +111,9 @@ int trellis_kv4_read(const trellis_kv4_cache *c, int layer, const trellis_kv4_ba
  * y  : out [rows][n_q_heads][head_dim] of `dtype`, dense, 16-byte aligned; must not overlap q.
  * lse: NULL, or f32 out [rows][n_q_heads]: the natural logarithm of the softmax's denominator
  *      (-inf where no key is visible), by which results over parts of a context are joined.
- * A key whose weight is zero in fp32 adds nothing, whatever its value holds.
+ * A key whose weight is zero in fp32 adds nothing, whatever its value holds.  A weight times its value's
+ * scale is held within 2^-11 of itself, but in steps of up to 2^-24 of the largest value scale that some
+ * row of the call sees among its 128 tokens.
  * window >= 0 (0: none), sinks >= 0, scale finite.
  * max_rows: the caller's bound on n_b, 0 if unknown; it chooses kernels, results are right for
  *      any value.  One launch, two where some sequences may have few and others many rows. */

@@ -13,9 +13,10 @@ namespace {
 // values, one word of codes.  A workgroup takes 16 consecutive rows and N of the (keys or values,
 // head, block) kinds, so the 64-byte code rows of a kind fall next to each other in a page, and a
 // row's page is looked up once for N blocks.  HBM bounds long calls (16-bit values in, a quarter of
-// it out); a few rows are bound by the chain of loads cu -> slot, length -> table before the store,
-// which the rows' own loads overlap.  N = 4 where that still fills the card, else 1 (8901 rows of 8
-// heads, append and read, 107 MB: 33.8 us at N = 4, 3.2 TB/s, 34.0 at N = 2, 37 at N = 1; N = 8 cost a
+// it out), with the rotation's vector instructions partly beside it (a copy without them takes 26.0 of
+// 29.9 us); a few rows are bound by the chain of loads cu -> slot, length -> table before the store,
+// which the rows' own loads overlap.  N = 4 where that still fills the card, else 1 (10338 rows of 8
+// heads, append and read, 107 MB: 30.1 us at N = 4, 3.5 TB/s, 29.8 at N = 2, 33.7 at N = 1; N = 8 cost a
 // ninth more).
 
 template <bool BF, int N>
@@ -295,8 +296,9 @@ __device__ __forceinline__ void release_pages(const Kv4Pages &p, int slot, int l
 
 // A child's table row and counts (workgroup y = 0), and its last page: a wave copies the rows that
 // are filled of one (layer, head) at a time, codes and scales of keys and values together, so that
-// up to 20 loads are in flight before the first store.  HBM bounds it; the stores bypass the caches,
-// which keep the parents' pages (192 children of 48 parents, 32 layers: 126 -> 59 us).
+// up to 20 loads are in flight before the first store.  HBM bounds it (192 children of 48 parents, 32
+// layers, 390 MB, and their release: 84 us); the stores bypass the caches, which keep the parents' pages
+// where they are there already (59 us then, 126 with stores through the caches).
 // Grid: x = item, y = shares of the (layer, head) units.
 template <int NB>
 __global__ __launch_bounds__(256) void kv4_fork_kernel(Kv4Pages p, PagesPlan plan, uint32_t *errword) {

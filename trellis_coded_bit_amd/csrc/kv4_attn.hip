@@ -389,7 +389,7 @@ __device__ __forceinline__ void add_tile(const AttnArgs &g, int tile, bool mask,
 // 128): 64 ragged contexts of 300 .. 12288 tokens 95 us for 461 MB, 4.9 TB/s (a copy of the kernel that
 // only loads takes the same); one token over 131071 40 us for 138 MB, 8.5 of them the join; one over
 // 777 10.8 us, which is latency: the search, the queries, a tile a wave, the join.  Drafts over heads of
-// 256 (12 sequences of 500 .. 9001 tokens): 38 us for 53 MB, bound by one wave a SIMD.
+// 256 (12 sequences of 500 .. 9001 tokens): 39 us for 53 MB, bound by one wave a SIMD; over heads of 128 26 us.
 //
 // All sequences' (head, column tile, key tile) units stand in one line; each workgroup takes an
 // equal stretch of it, whatever the lengths, and its four waves take the stretch's key tiles in

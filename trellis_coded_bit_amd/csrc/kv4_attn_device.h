@@ -186,8 +186,8 @@ typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 
 // A block of a column as a matrix operand: lane (n, g) has elements 32 g .. 32 g + 31 of column n, as
 // three E2M3 parts.  (Their products take half the time of E4M3's.  A part's steps are fixed where
-// E4M3's shrink with the element, so three reach 2^-12 of the block's largest element, not of each; a
-// score is a sum over the block, whose error the largest elements set either way.)
+// E4M3's shrink with the element, so three reach 2^-12 / 3.75 of the block's largest element, not of each;
+// a score is a sum over the block, whose error the largest elements set either way.)
 struct QueryBlock {
   u32x6 part[3];
   int scale;  // a byte a part: its power of two as the matrix instructions take it

@@ -12,13 +12,14 @@
 // p vs are rounded once to fp16 (within 2^-11), with one power of two per wave that follows the
 // tiles' largest value scale.
 //
-// The vector instructions bound it: 586 a tile and wave with starts and ends, 128 of them the values'
-// conversion, keep a SIMD busy 76% of the time; the matrix instructions (900 cycles a tile and wave at heads
-// of 128) run beside them but take issue slots too.  Three waves a SIMD overlap them; more columns a wave
+// Issue bounds it: 586 vector instructions a tile and wave with starts and ends, 128 of them the values'
+// conversion, keep a SIMD busy 75% of the time, and the matrix instructions (900 cycles a tile and wave at
+// heads of 128) run beside them but take slots too.  Three waves a SIMD overlap them; more columns a wave
 // would share the conversion, but leave two waves (32 a wave: 374 us where 64 columns a workgroup took 245).
-// 4096 tokens, 32 query heads, 8 key/value heads of 128: 182 us, 137 GFLOP, 757 TFLOP/s (the library's fp16
-// product of 8192^3 reaches 1330).  Chunks of 300 .. 1023 tokens behind up to 11000, window 2048: 91 us,
-// 39 GFLOP.
+// 4096 tokens, 32 query heads, 8 key/value heads of 128: 182 us, 137 GFLOP, 755 TFLOP/s (the library's fp16
+// product of 8192^3 reaches 1330); copies that leave work out take 160 us without the conversion, 170 with
+// one of the query's three parts, 144 with a quarter of the second product.  16 query heads on 4 of 256:
+// 183 us.  Chunks of 300 .. 1023 tokens behind up to 11000, window 2048: 92 us, 39 GFLOP.
 #include "kv4_attn_device.h"
 
 namespace trellis {

@@ -26,9 +26,10 @@ hipError_t launch_had128(const void *x, int x_is_fp32, int rows, int n, const ui
 // serve every entry point in any order:
 //   [0, 256)                 header; word 0 is the error word (sticky: kernels only OR bits
 //                            into it, the caller clears it); the other words are unused
-//   [256, 256 + 64 KiB)      the small-batch products' column-block counters: zero between
-//                            calls (each call's finishing workgroups reset the ones it used);
-//                            no other entry point writes them
+//   [256, 256 + 64 KiB)      counters of workgroups that share work: the small-batch products'
+//                            column blocks, attention's segments; zero between calls (each
+//                            call's finishing workgroups reset the ones it used); no other
+//                            entry point writes them
 //   [kWsReserved, ...)       the entry point's own scratch
 constexpr size_t kWsHeaderBytes = 256;
 constexpr int kMaxFinishGroups = 16384;

@@ -1,0 +1,450 @@
+"""The block-scaled FP8 operators on the GPU against the 64-bit oracle: the norm, the gated
+activation, and products, at the sizes, types, strides and values where they can go wrong.
+
+Tolerances, from the roundings alone (u = 2^-24, one f32 rounding):
+  codes   : v / scale is formed with at most 8 roundings (h, h gamma, its largest, 448 / a, the
+            product; for the activation expf's 2 u, 1 + e, the division, the product), so a code is
+            one that some value within 2^-20 of the exact quotient rounds to.
+  scales  : the square sum of at most 32768 channels takes at most 8 + 4 + 6 + 16 additions in a
+            chain beside the squares' roundings, halved by the root; with the rest below 2^-19.
+  products: a matrix instruction adds the products of eight neighbouring channels in steps of 2^-13
+            of the power of two that the largest one's operands have, cutting each term off towards
+            zero (measured: 256 * 256 beside 7 gives 65536, beside 14 gives 65544, wherever the two
+            lie among eight channels; in different eights nothing is lost up to 2^-23).  That power
+            is at most the largest product, so eight channels lose less than 7 * 2^-13 of it.  The
+            sixteen sums of eight, the blocks (one fma each), the shares of split sums and the
+            factor take (16 + blocks + 32) roundings of at most 2 u sum |terms|.  The result is
+            rounded to its type.  Over a whole result the cuts are independent of the rounding and
+            far below it, and its relative 2-norm stays within half a step.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import f8 as FO
+from trellis_coded_bit_amd import binding as tb
+
+from gpu_util import log_case
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+HALF = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}
+TINY = {"fp16": 2.0 ** -25, "bf16": 2.0 ** -134}  # half a step of the smallest numbers
+U = 2.0 ** -24
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def check_rounded(got, ref, dtype, rel=0.0, extra=0.0):
+    """Within half a step of `dtype` beside a relative and an absolute error before it."""
+    err = np.abs(got - ref)
+    bound = np.abs(ref) * (HALF[dtype] * (1 + rel) + rel) + extra * (1 + HALF[dtype]) + TINY[dtype]
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+def check_quantized(q, s, v, rel_code, rel_scale):
+    """Codes' values and scales of rows v (64 bits)."""
+    rq, rs = FO.quantize(v)
+    nan = np.isnan(rs)
+    assert np.array_equal(np.isnan(s), nan)
+    assert (np.abs(s - rs)[~nan] <= rel_scale * rs[~nan]).all()
+    # the quotient from the exact scale: the scale's own error does not reach the codes
+    full = np.repeat(FO.block_top(v) / 448.0, 128, 1)[:, :v.shape[1]]
+    zero = np.repeat(nan | (rs == 0), 128, 1)[:, :v.shape[1]]
+    with np.errstate(all="ignore"):
+        t = np.where(zero, 0.0, v / full)
+    a, b = FO.e4m3_round(t * (1 - rel_code)), FO.e4m3_round(t * (1 + rel_code))
+    ok = (q >= np.minimum(a, b)) & (q <= np.maximum(a, b))
+    assert ok.all(), (int((~ok).sum()), q[~ok][:4], t[~ok][:4])
+    assert (q != rq).mean() < 1e-3
+    return rq, rs
+
+
+# ---------------------------------------------------------------------------------------
+# Norm
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n,residual,gamma,stride", [
+    (1, 16, False, True, 0), (1, 5120, True, True, 0), (3, 128, True, False, 8), (5, 144, True, True, 0),
+    (7, 2032, False, True, 24), (33, 1024, True, True, 0), (2, 8192, True, True, 0), (3, 8208, True, True, 0),
+    (2, 17408, True, True, 0), (2, 32768, True, True, 0), (700, 6144, True, True, 0), (4100, 256, False, False, 0),
+])
+def test_norm(dtype, rows, n, residual, gamma, stride):
+    log_case(f"f8 norm {dtype} rows={rows} n={n} residual={residual} gamma={gamma} stride=+{stride}")
+    g = torch.Generator().manual_seed(rows * 7 + n)
+    x = torch.randn((rows, n + stride), generator=g)
+    x[:, ::37] *= 9
+    x = x.to(DT[dtype]).cuda()[:, :n]
+    res = (3 * torch.randn((rows, n), generator=g)).to(DT[dtype]).cuda() if residual else None
+    gam = (1 + 0.3 * torch.randn((n,), generator=g)).to(DT[dtype]).cuda() if gamma else None
+    y = torch.empty((rows, n), dtype=DT[dtype], device="cuda")
+    q, s, h = tb.trellis_f8_norm(x, gam, 1e-5, residual=res, y=y)
+    v, rh = FO.norm(host(x), float(np.float32(1e-5)), host(gam) if gamma else None, host(res) if residual else None)
+    assert q.dtype == torch.float8_e4m3fn and s.shape == (rows, -(-n // 128))
+    check_quantized(host(q), host(s), v, 2.0 ** -20, 2.0 ** -19)
+    check_rounded(host(y), v, dtype, 2.0 ** -19)
+    if residual:
+        check_rounded(host(h), rh, dtype, U)
+    else:
+        assert h is None
+    # the norm alone, and the residual in place, give the same bits
+    y2, h2 = tb.trellis_f8_norm(x, gam, 1e-5, residual=res, quantize=False)
+    assert torch.equal(y, y2)
+    if residual:
+        assert torch.equal(h, h2)
+        r2 = res.clone()
+        q3, s3, h3 = tb.trellis_f8_norm(x, gam, 1e-5, residual=r2, h=r2)
+        assert h3 is r2 and torch.equal(r2, h) and torch.equal(q3.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s3, s)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_norm_of_special_rows(dtype, rows):
+    """Zeros, one channel alone, the type's largest, numbers whose squares leave f32, NaN and
+    infinities: rows beside them are not touched."""
+    log_case(f"f8 norm special {dtype} rows={rows}")
+    n = 400
+    g = torch.Generator().manual_seed(3)
+    kinds = [torch.randn(n, generator=g), torch.zeros(n), torch.zeros(n), torch.full((n,), torch.finfo(DT[dtype]).max),
+             torch.randn(n, generator=g), torch.randn(n, generator=g), torch.randn(n, generator=g) * 1e-6]
+    kinds[2][131] = 5.0
+    kinds[4][200] = float("nan")
+    kinds[5][399] = float("-inf")
+    if dtype == "bf16":
+        kinds += [torch.randn(n, generator=g) * 1e30, torch.randn(n, generator=g) * 1e-30]
+    x = torch.stack(kinds).repeat(rows, 1)
+    gam = 1 + 0.3 * torch.randn(n, generator=g)
+    gam[300:310] = 0
+    x, gam = x.to(DT[dtype]).cuda(), gam.to(DT[dtype]).cuda()
+    y = torch.empty_like(x)
+    q, s, _ = tb.trellis_f8_norm(x, gam, 1e-12, y=y)
+    v, _ = FO.norm(host(x), float(np.float32(1e-12)), host(gam))
+    q, s, y = host(q), host(s), host(y)
+    assert np.isnan(s).any() and (s[1] == 0).all() and s[2, 1] > 0 and s[2, 0] == 0
+    nan = np.isnan(v)
+    assert np.array_equal(np.isnan(y), nan)
+    assert not np.isnan(s[0]).any() and np.isnan(s[4]).all() and np.isnan(s[5]).tolist() == [False, False, False, True]
+    check_quantized(np.where(nan, 0, q), s, v, 2.0 ** -20, 2.0 ** -19)
+    check_rounded(np.where(nan, 0, y), np.where(nan, 0, v), dtype, 2.0 ** -19)
+    assert (q[np.repeat(np.isnan(s), 128, 1)[:, :n]] == 0).all()
+
+
+# ---------------------------------------------------------------------------------------
+# Gated activation
+# ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n,stride", [(1, 16, 0), (1, 2048, 0), (5, 144, 8), (264, 2048, 0), (3, 17408, 0), (1000, 112, 32)])
+def test_silu_mul(dtype, rows, n, stride):
+    log_case(f"f8 silu_mul {dtype} rows={rows} n={n} stride=+{stride}")
+    g = torch.Generator().manual_seed(rows + n)
+    x = (2 * torch.randn((rows, 2 * n + stride), generator=g)).to(DT[dtype]).cuda()[:, :2 * n]
+    y = torch.empty((rows, n), dtype=DT[dtype], device="cuda")
+    q, s = tb.trellis_f8_silu_mul(x, y=y)
+    v = FO.silu_mul(host(x))
+    check_quantized(host(q), host(s), v, 2.0 ** -20, 2.0 ** -20)
+    check_rounded(host(y), v, dtype, 2.0 ** -20)
+    assert torch.equal(tb.trellis_f8_silu_mul(x, quantize=False), y)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_silu_mul_of_special_values(dtype):
+    log_case(f"f8 silu_mul special {dtype}")
+    big = torch.finfo(DT[dtype]).max
+    x = torch.zeros((4, 2 * 256))
+    x[0, :256] = torch.linspace(-80, 80, 256)
+    x[0, 256:] = 1.0
+    x[1, 3], x[1, 256 + 3] = float("nan"), 1.0
+    x[1, 200], x[1, 256 + 200] = 2.0, 3.0
+    x[2, 0], x[2, 256] = big, 1.0
+    x[2, 128], x[2, 256 + 128] = -big, big      # silu is 0 from below, times the largest
+    x[3, 7], x[3, 256 + 7] = float("inf"), 2.0
+    x = x.to(DT[dtype]).cuda()
+    q, s = tb.trellis_f8_silu_mul(x)
+    v = FO.silu_mul(host(x))
+    q, s = host(q), host(s)
+    assert np.isnan(s).tolist() == [[False, False], [True, False], [False, False], [True, False]]
+    assert s[2, 1] == 0 and (q[2, 128:] == 0).all() and (q[1, :128] == 0).all() and (q[3, :128] == 0).all()
+    check_quantized(q[:1], s[:1], v[:1], 2.0 ** -20, 2.0 ** -20)
+    assert abs(s[2, 0] * 448 / v[2, 0] - 1) < 2.0 ** -20 and abs(s[1, 1] * 448 / v[1, 200] - 1) < 2.0 ** -20
+
+
+# ---------------------------------------------------------------------------------------
+# Products
+# ---------------------------------------------------------------------------------------
+
+def codes(shape, g, spread=1.0):
+    return (spread * 60 * torch.randn(shape, generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn)
+
+
+def make_matrix(n, k, g, experts=None, gain=1.0):
+    lead = () if experts is None else (experts,)
+    s = gain * torch.exp(torch.randn((*lead, -(-n // 128), -(-k // 128)), generator=g)) / (60 * 60 * k ** 0.5)
+    return tb.F8Linear(codes((*lead, n, k), g).cuda(), s.cuda())
+
+
+def make_rows(m, k, g, q_stride=0, s_stride=0):
+    kb = -(-k // 128)
+    q = codes((m, k + q_stride), g).cuda()[:, :k]
+    s = torch.exp(torch.randn((m, kb + s_stride), generator=g)).cuda()[:, :kb]
+    return q, s
+
+
+def largest_of_eights(q, s, w, sw):
+    """Sum over the eights of neighbouring channels of their largest product's magnitude."""
+    pad = lambda t: torch.nn.functional.pad(t.float().abs(), (0, -t.shape[1] % 8)).unflatten(1, (-1, 8))  # noqa: E731
+    x, m, cols = pad(q), pad(w), torch.arange(w.shape[0], device=w.device) // 128
+    total = torch.zeros((q.shape[0], w.shape[0]), device="cuda")
+    for i in range(x.shape[1]):
+        top = (x[:, None, i] * m[None, :, i]).amax(-1)
+        total += top * s[:, None, i // 16] * sw[cols, i // 16]
+    return host(total)
+
+
+def check_product(y, q, s, w, sw, dtype):
+    ref, mass = FO.product(host(q), host(s), host(w), host(sw))
+    kb = s.shape[1]
+    extra = 7 * 2.0 ** -13 * (1 + 2.0 ** -10) * largest_of_eights(q, s, w, sw) + 2 * (16 + kb + 32) * U * mass
+    check_rounded(host(y), ref, dtype, 0.0, extra)
+    # (results below the type's smallest normal number are rounded to its absolute step)
+    assert np.linalg.norm(host(y) - ref) <= HALF[dtype] * np.linalg.norm(ref) + TINY[dtype] * ref.size ** 0.5
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 16), (1, 16, 128), (1, 130, 144), (1, 5120, 6144), (1, 1000, 17408), (2, 257, 272), (3, 640, 2048), (8, 129, 1040),
+    (15, 512, 512), (16, 136, 640), (17, 1000, 400), (31, 384, 1024), (33, 264, 2048), (64, 2048, 1024), (65, 300, 784),
+    (100, 1032, 1296), (127, 128, 128), (128, 640, 128), (129, 257, 16), (200, 1288, 2064), (255, 768, 640), (256, 1024, 1152),
+    (257, 513, 1024), (300, 256, 4096), (513, 2050, 528), (1000, 264, 272), (2048, 384, 512),
+])
+def test_gemm(dtype, m, n, k):
+    log_case(f"f8 gemm {dtype} m={m} n={n} k={k}")
+    g = torch.Generator().manual_seed(m * 131 + n * 7 + k)
+    L = make_matrix(n, k, g)
+    q, s = make_rows(m, k, g)
+    out = torch.full((m, n), 7.0, dtype=DT[dtype], device="cuda")
+    y = tb.trellis_f8_gemm(L, q, s, out=out)
+    assert y is out
+    check_product(y, q, s, L.w, L.scale, dtype)
+    # again, into a new tensor: the same bits, whatever shares the sums
+    assert torch.equal(tb.trellis_f8_gemm(L, q, s, dtype=DT[dtype]), y)
+    assert tb.error_word() == 0
+
+
+@pytest.mark.parametrize("m", [1, 5, 40, 200])
+def test_gemm_of_slices(m):
+    """Rows of q, scales and results inside wider buffers; what is between them stays."""
+    log_case(f"f8 gemm slices m={m}")
+    g = torch.Generator().manual_seed(m)
+    n, k = 392, 656
+    L = make_matrix(n, k, g)
+    q, s = make_rows(m, k, g, 48, 3)
+    for width, first in ((n + 8, 0), (n + 13, 5), (n + 16, 8)):
+        wide = torch.full((m, width), 3.0, dtype=torch.float16, device="cuda")
+        y = wide[:, first:first + n]
+        tb.trellis_f8_gemm(L, q, s, out=y)
+        check_product(y, q, s, L.w, L.scale, "fp16")
+        wide[:, first:first + n] = 3.0
+        assert (wide == 3.0).all()
+        assert torch.equal(tb.trellis_f8_gemm(L, q.contiguous(), s.contiguous()), tb.trellis_f8_gemm(L, q, s))
+
+
+@pytest.mark.parametrize("m", [1, 20, 150])
+def test_gemm_of_special_values(m):
+    """A NaN code or scale reaches its row's or its columns' results and no others; zeros of rows
+    behind the last and channels behind the last block's end are no part of the sums."""
+    log_case(f"f8 gemm special m={m}")
+    g = torch.Generator().manual_seed(m)
+    n, k = 300, 400
+    L = make_matrix(n, k, g)
+    wide = torch.full((m + 4, 512), float("nan")).to(torch.float8_e4m3fn).cuda()  # what lies around q
+    scales = torch.full((m + 4, 8), float("nan"), device="cuda")
+    q, s = wide[:m, :k], scales[:m, :4]
+    q0, s0 = make_rows(m, k, g)
+    q.copy_(q0)
+    s.copy_(s0)
+    y = tb.trellis_f8_gemm(L, q, s)
+    check_product(y, q0, s0, L.w, L.scale, "fp16")
+    q.view(torch.uint8)[m - 1, 399] = 0x7F
+    w = L.w.clone()
+    w.view(torch.uint8)[299, 0] = 0xFF
+    sw = L.scale.clone()
+    sw[1, 2] = float("inf")
+    z = tb.trellis_f8_gemm(tb.F8Linear(w, sw), q, s)
+    bad = torch.zeros((m, n), dtype=torch.bool, device="cuda")
+    bad[m - 1], bad[:, 299], bad[:, 128:256] = True, True, True
+    assert torch.isfinite(z[~bad]).all() and torch.equal(z[~bad], y[~bad])
+    assert torch.isnan(z[m - 1]).all() and torch.isnan(z[:, 299]).all() and not torch.isfinite(z[:, 128:256]).any()
+
+
+def test_gemm_overflow_is_infinite():
+    log_case("f8 gemm overflow")
+    L = tb.F8Linear(torch.full((16, 128), 448.0).to(torch.float8_e4m3fn).cuda(), torch.ones((1, 1), device="cuda"))
+    q = torch.full((3, 128), 448.0).to(torch.float8_e4m3fn).cuda()
+    q[1] = -q[1].float()
+    q[2] = 0
+    y = tb.trellis_f8_gemm(L, q, torch.ones((3, 1), device="cuda"))
+    assert (y[0] == float("inf")).all() and (y[1] == float("-inf")).all() and (y[2] == 0).all()
+    y = tb.trellis_f8_gemm(L, q, torch.ones((3, 1), device="cuda"), dtype=torch.bfloat16)
+    assert torch.isfinite(y).all()
+
+
+def grouped(counts, n, k, g, per=0, tokens=0):
+    E = len(counts)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    L = make_matrix(n, k, g, E)
+    total = int(off[-1])
+    if per:
+        order = torch.randperm(tokens * per, generator=g)[:total].to(torch.int32)
+        q, s = make_rows(tokens, k, g)
+        src = order.long() // per
+    else:
+        order, src = None, torch.arange(total)
+        q, s = make_rows(total, k, g)
+    return L, q, s, ints(off.tolist()), order, src
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("counts,n,k,per", [
+    ([1], 128, 128, 0), ([0, 0, 3, 0], 136, 144, 0), ([5, 0, 1, 17, 16, 0, 33, 2], 264, 272, 4),
+    ([130, 1, 0, 257, 128, 64], 392, 656, 2), ([1] * 70 + [0] * 30 + [2] * 30, 160, 384, 8), ([300, 700], 512, 1024, 0),
+    ([0] * 199 + [40], 128, 256, 8), ([2, 3, 1, 2, 0, 4, 2, 2], 1024, 2048, 8),
+])
+def test_moe_gemm(dtype, counts, n, k, per):
+    log_case(f"f8 moe_gemm {dtype} experts={len(counts)} rows={sum(counts)} n={n} k={k} per={per}")
+    g = torch.Generator().manual_seed(sum(counts) + n)
+    total = sum(counts)
+    tokens = -(-total // per) + 3 if per else 0
+    L, q, s, off, order, src = grouped(counts, n, k, g, per, tokens)
+    extra = 5  # rows behind the last expert's
+    if per:
+        full = torch.full((total + extra,), -1, dtype=torch.int32)
+        full[:total] = order
+        order = full.cuda()
+    else:
+        q, s = torch.cat((q, q[:1].expand(extra, -1).clone())), torch.cat((s, s[:1].expand(extra, -1)))
+    out = torch.full((total + extra, n), 5.0, dtype=DT[dtype], device="cuda")
+    y = tb.trellis_f8_moe_gemm(L, q, s, off, order=order, per=max(per, 1), out=out)
+    assert (y[total:] == 5.0).all()
+    src, o = src.cuda(), off.tolist()
+    for e in range(len(counts)):
+        if counts[e]:
+            at = src[o[e]:o[e + 1]]
+            check_product(y[o[e]:o[e + 1]], q.view(torch.uint8)[at].view(torch.float8_e4m3fn), s[at], L.w[e], L.scale[e], dtype)
+    again = torch.full_like(out, 5.0)
+    assert torch.equal(tb.trellis_f8_moe_gemm(L, q, s, off, order=order, per=max(per, 1), out=again), y)
+    assert tb.error_word() == 0
+
+
+def test_moe_gemm_without_rows():
+    log_case("f8 moe_gemm no rows")
+    g = torch.Generator().manual_seed(0)
+    L = make_matrix(128, 128, g, 3)
+    q, s = make_rows(6, 128, g)
+    out = torch.full((6, 128), 5.0, dtype=torch.float16, device="cuda")
+    tb.trellis_f8_moe_gemm(L, q, s, ints([0, 0, 0, 0]), out=out)
+    assert (out == 5.0).all() and tb.error_word() == 0
+    assert tb.trellis_f8_moe_gemm(L, q[:0], s[:0], ints([0, 0, 0, 0])).shape == (0, 128)
+    assert tb.trellis_f8_gemm(make_matrix(128, 128, g), q[:0], s[:0]).shape == (0, 128)
+
+
+@pytest.mark.parametrize("offsets,done", [([0, 4, 2, 9], 4), ([0, 4, 8, 99], 8), ([1, 4, 8, 9], 0), ([0, -3, 8, 9], 0), ([0, 4, 8, 9], 9)])
+def test_moe_gemm_bad_offsets(offsets, done):
+    """The call ends at the first pair that is out of order: rows before it are right, the rest left."""
+    log_case(f"f8 moe_gemm offsets={offsets}")
+    g = torch.Generator().manual_seed(1)
+    L = make_matrix(128, 256, g, 3)
+    q, s = make_rows(12, 256, g)
+    good = torch.zeros((12, 128), dtype=torch.float16, device="cuda")
+    tb.trellis_f8_moe_gemm(L, q, s, ints([0, 4, 8, 9]), out=good)
+    out = torch.full((12, 128), 5.0, dtype=torch.float16, device="cuda")
+    tb.clear_error_word()
+    tb.trellis_f8_moe_gemm(L, q, s, ints(offsets), out=out)
+    assert torch.equal(out[:done], good[:done]) and (out[done:] == 5.0).all()
+    assert tb.error_word() == (0 if done == 9 else 1)
+    tb.clear_error_word()
+
+
+@pytest.mark.parametrize("rows", [9, 140])
+def test_moe_gemm_bad_order(rows):
+    log_case(f"f8 moe_gemm bad order rows={rows}")
+    g = torch.Generator().manual_seed(2)
+    L = make_matrix(136, 144, g, 2)
+    q, s = make_rows(10, 144, g)
+    order = torch.arange(rows, dtype=torch.int32, device="cuda") % 20
+    good = tb.trellis_f8_moe_gemm(L, q, s, ints([0, 3, rows]), order=order, per=2)
+    for at, v in ((1, -1), (4, 20), (6, 2 ** 31 - 1), (rows - 1, -(2 ** 31))):
+        order[at] = v
+        good[at] = 0
+    tb.clear_error_word()
+    assert torch.equal(tb.trellis_f8_moe_gemm(L, q, s, ints([0, 3, rows]), order=order, per=2), good)
+    assert tb.error_word() == 1
+    tb.clear_error_word()
+
+
+def test_refusals():
+    log_case("f8 refusals")
+    g = torch.Generator().manual_seed(0)
+    L, E = make_matrix(128, 128, g), make_matrix(128, 128, g, 2)
+    q, s = make_rows(4, 128, g)
+    x = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
+    off = ints([0, 2, 4])
+    for error, f in (
+            (ValueError, lambda: tb.trellis_f8_gemm(E, q, s)), (ValueError, lambda: tb.trellis_f8_moe_gemm(L, q, s, off)),
+            (ValueError, lambda: tb.trellis_f8_gemm(L, q[:, :112], s)), (ValueError, lambda: tb.trellis_f8_gemm(L, q, s[:3])),
+            (TypeError, lambda: tb.trellis_f8_gemm(L, q.view(torch.uint8), s)), (TypeError, lambda: tb.trellis_f8_gemm(L, q, s, dtype=torch.float32)),
+            (ValueError, lambda: tb.trellis_f8_gemm(L, q, s, out=x)), (ValueError, lambda: tb.trellis_f8_moe_gemm(E, q, s, off[:2])),
+            (TypeError, lambda: tb.trellis_f8_moe_gemm(E, q, s, off.long())), (tb.TrellisError, lambda: tb.trellis_f8_moe_gemm(E, q, s, off, per=0)),
+            (ValueError, lambda: tb.F8Linear(L.w, L.scale[:, :0])), (TypeError, lambda: tb.F8Linear(x, L.scale)),
+            (tb.TrellisError, lambda: tb.trellis_f8_norm(x[:, :200], None, 1e-6)), (tb.TrellisError, lambda: tb.trellis_f8_norm(x, None, 0.0)),
+            (tb.TrellisError, lambda: tb.trellis_f8_norm(x[:, 1:241], None, 1e-6)), (ValueError, lambda: tb.trellis_f8_norm(x.t(), None, 1e-6)),
+            (TypeError, lambda: tb.trellis_f8_norm(x, x[0].float(), 1e-6)), (ValueError, lambda: tb.trellis_f8_norm(x, x[0, :128].contiguous(), 1e-6)),
+            (tb.TrellisError, lambda: tb.trellis_f8_norm(x, None, 1e-6, y=x)), (ValueError, lambda: tb.trellis_f8_norm(x, None, 1e-6, quantize=False, q=q)),
+            (ValueError, lambda: tb.trellis_f8_silu_mul(x[:, :255])), (tb.TrellisError, lambda: tb.trellis_f8_silu_mul(x[:, :48]))):
+        with pytest.raises(error):
+            f()
+
+
+@pytest.mark.parametrize("m", [1, 48, 300])
+def test_gemm_in_a_graph_and_on_streams(m):
+    """Captured with a workspace of its own and replayed with other inputs, beside eager calls on
+    two streams with theirs."""
+    log_case(f"f8 gemm graph m={m}")
+    g = torch.Generator().manual_seed(m)
+    n, k = 640, 4096
+    L, E = make_matrix(n, k, g), make_matrix(n, k, g, 3)
+    q, s = make_rows(m, k, g)
+    off = ints([0, m // 3, m // 3, m])
+    ws = torch.zeros(max(tb.trellis_f8_workspace_bytes(L, m), tb.trellis_f8_workspace_bytes(E, m)), dtype=torch.uint8, device="cuda")
+    y, z = (torch.empty((m, n), dtype=torch.float16, device="cuda") for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    tb.trellis_f8_gemm(L, q, s, out=y, ws=ws)
+    tb.trellis_f8_moe_gemm(E, q, s, off, out=z, ws=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        tb.trellis_f8_gemm(L, q, s, out=y, ws=ws)
+        tb.trellis_f8_moe_gemm(E, q, s, off, out=z, ws=ws)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(4):
+        q2, s2 = make_rows(m, k, g)
+        q.copy_(q2)
+        s.copy_(s2)
+        torch.cuda.synchronize()
+        graph.replay()
+        got = []
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append((tb.trellis_f8_gemm(L, q2, s2), tb.trellis_f8_moe_gemm(E, q2, s2, off)))
+        torch.cuda.synchronize()
+        for a, b in got:
+            assert torch.equal(a, y) and torch.equal(b, z)
+        check_product(y, q2, s2, L.w, L.scale, "fp16")
+    assert tb.error_word() == 0 and tb.error_word(ws) == 0

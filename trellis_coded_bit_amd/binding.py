@@ -129,6 +129,30 @@ def lib() -> ctypes.CDLL:
             L.trellis_kv4_compact.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, sz, vp]
             L.trellis_kv4_free.restype = i32
             L.trellis_kv4_free.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp, sz, vp]
+            L.trellis_f8_norm.restype = i32
+            L.trellis_f8_norm.argtypes = [i32, vp, i64, vp, vp, i32, i32, f32, vp, vp, vp, vp, vp]
+            L.trellis_f8_silu_mul.restype = i32
+            L.trellis_f8_silu_mul.argtypes = [i32, vp, i64, i32, i32, vp, vp, vp, vp]
+            L.trellis_f8_gemm_workspace_bytes.restype = sz
+            L.trellis_f8_gemm_workspace_bytes.argtypes = [vp, i32]
+            L.trellis_f8_moe_gemm_workspace_bytes.restype = sz
+            L.trellis_f8_moe_gemm_workspace_bytes.argtypes = [vp, i32]
+            L.trellis_f8_gemm.restype = i32
+            L.trellis_f8_gemm.argtypes = [vp, vp, i64, vp, i64, i32, i32, vp, i64, vp, sz, vp]
+            L.trellis_f8_moe_gemm.restype = i32
+            L.trellis_f8_moe_gemm.argtypes = [vp, vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, sz, vp]
+            L.trellis_moe_sort_workspace_bytes.restype = sz
+            L.trellis_moe_sort_workspace_bytes.argtypes = [i32, i32, i32]
+            L.trellis_moe_rows_workspace_bytes.restype = sz
+            L.trellis_moe_rows_workspace_bytes.argtypes = []
+            L.trellis_moe_sort.restype = i32
+            L.trellis_moe_sort.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+            L.trellis_moe_gather.restype = i32
+            L.trellis_moe_gather.argtypes = [vp, i64, i32, i64, vp, i32, i32, vp, vp, sz, vp]
+            L.trellis_moe_combine.restype = i32
+            L.trellis_moe_combine.argtypes = [i32, vp, i32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+            L.trellis_moe_combine_grad.restype = i32
+            L.trellis_moe_combine_grad.argtypes = [i32, vp, vp, i32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
             L.trellis_validate_table.restype = i32
             L.trellis_validate_table.argtypes = [ctypes.POINTER(CLinear), i32, i32, i32, i32]
             _lib = L
@@ -859,6 +883,316 @@ def trellis_kv4_free(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, r
     ws = _kv4_ws(ws, _kv4_ws_bytes(), cache.device, stream)
     _check(lib().trellis_kv4_free(cache._ref, table.data_ptr(), lens.data_ptr(), table.shape[0], table.shape[1],
                                   ref.data_ptr(), slots.data_ptr(), n, ws.data_ptr(), ws.numel(), stream))
+
+
+# ---------------------------------------------------------------------------------------
+# Block-scaled FP8 (include/trellis_f8.h) and routed tokens (include/trellis_route.h)
+# ---------------------------------------------------------------------------------------
+
+class CF8Linear(ctypes.Structure):
+    """Mirror of ``trellis_f8_linear`` in include/trellis_f8.h."""
+
+    _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("n_experts", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32)]
+
+
+_E4M3 = torch.float8_e4m3fn
+_F8_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _f8_rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None, device=None,
+             cols: Optional[int] = None) -> int:
+    """Checks a [rows, cols] tensor on the current device whose rows are contiguous (16-bit if
+    no dtype is given); its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _F8_DTYPE):
+        raise TypeError(f"{name} must be {'float16 or bfloat16' if dtype is None else dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device")
+    if t.device.index != torch._C._cuda_getDevice() or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}: the current device is cuda:{torch._C._cuda_getDevice()}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [rows, {'n' if cols is None else cols}], got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: each row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _f8_ws(ws: Optional[torch.Tensor], nb: int, device) -> torch.Tensor:
+    return _kv4_ws(ws, nb, device, _stream())
+
+
+def _f8_out(q, scale, rows: int, n: int, device):
+    return (_out(q, (rows, n), device, _E4M3, "q"), _out(scale, (rows, _f8_blocks(n)), device, torch.float32, "scale"))
+
+
+def trellis_f8_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, residual: Optional[torch.Tensor] = None,
+                    quantize: bool = True, h: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                    scale: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of h = x + residual, x [rows, n] fp16 or bf16 (a slice with its own
+    row stride is fine), residual [rows, n], gamma [n] of the same type or None: (q, scale, h),
+    the E4M3 codes (float8_e4m3fn [rows, n]) with one f32 scale per 128 channels, and h rounded
+    (the next residual; ``h=residual`` updates it in place), None if there is no residual and no
+    ``h``.  ``y``: optional 16-bit output of the norm itself; with ``quantize=False`` it is the
+    only one (q and scale are None, y is made if not given) and takes their place: (y, h)."""
+    x_row = _f8_rows(x, "x")
+    rows, n = x.shape
+    dev = x.device
+    if residual is not None:
+        _req(residual, x.dtype, "residual", dev)
+        if tuple(residual.shape) != (rows, n):
+            raise ValueError(f"residual must be {(rows, n)}, got {tuple(residual.shape)}")
+    if gamma is not None:
+        _req(gamma, x.dtype, "gamma", dev)
+        if gamma.numel() != n:
+            raise ValueError(f"gamma must have {n} elements")
+    if residual is not None or h is not None:
+        h = _out(h, (rows, n), dev, x.dtype, "h")
+    if quantize:
+        q, scale = _f8_out(q, scale, rows, n, dev)
+    elif q is not None or scale is not None:
+        raise ValueError("q and scale are not written with quantize=False")
+    if y is not None or not quantize:
+        y = _out(y, (rows, n), dev, x.dtype, "y")
+    _check(lib().trellis_f8_norm(_F8_DTYPE[x.dtype], x.data_ptr(), x_row, _ptr(residual), _ptr(gamma), rows, n, eps, _ptr(h),
+                                 _ptr(q), _ptr(scale), _ptr(y), _stream()))
+    return (q, scale, h) if quantize else (y, h)
+
+
+def trellis_f8_silu_mul(x: torch.Tensor, quantize: bool = True, q: Optional[torch.Tensor] = None,
+                        scale: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """silu(g) * u of x [rows, 2n] fp16 or bf16 with g in its first n columns: (q, scale), E4M3
+    codes with one f32 scale per 128 channels.  ``y``: optional 16-bit output; with
+    ``quantize=False`` the only one, returned."""
+    x_row = _f8_rows(x, "x")
+    rows, n = x.shape[0], x.shape[1] // 2
+    if x.shape[1] % 2:
+        raise ValueError(f"x must have an even number of columns, got {x.shape[1]}")
+    if quantize:
+        q, scale = _f8_out(q, scale, rows, n, x.device)
+    elif q is not None or scale is not None:
+        raise ValueError("q and scale are not written with quantize=False")
+    if y is not None or not quantize:
+        y = _out(y, (rows, n), x.device, x.dtype, "y")
+    _check(lib().trellis_f8_silu_mul(_F8_DTYPE[x.dtype], x.data_ptr(), x_row, rows, n, _ptr(q), _ptr(scale), _ptr(y), _stream()))
+    return (q, scale) if quantize else y
+
+
+class F8Linear:
+    """E4M3 matrices with one f32 scale per 128 x 128 block: w float8_e4m3fn [out, in] and scale
+    [ceil(out / 128), ceil(in / 128)], or one per expert, [experts, out, in] and [experts, ...]."""
+
+    def __init__(self, w: torch.Tensor, scale: torch.Tensor):
+        _req(w, _E4M3, "w")
+        _req(scale, torch.float32, "scale", w.device)
+        if w.dim() not in (2, 3):
+            raise ValueError(f"w must be [out, in] or [experts, out, in], got {tuple(w.shape)}")
+        out, inn = w.shape[-2:]
+        want = (*w.shape[:-2], _f8_blocks(out), _f8_blocks(inn))
+        if tuple(scale.shape) != want:
+            raise ValueError(f"scale must be {want}, got {tuple(scale.shape)}")
+        self.w, self.scale, self.device = w, scale, w.device
+        self.experts = w.shape[0] if w.dim() == 3 else None
+        self.in_features, self.out_features = inn, out
+        self._c = CF8Linear(w.data_ptr(), scale.data_ptr(), w.shape[0] if w.dim() == 3 else 1, inn, out)
+        self._ref = ctypes.byref(self._c)
+
+
+# Workspace sizes of the products by the sizes they follow from (not by tensors).
+_f8_nb: Dict[Tuple[int, ...], int] = {}
+
+
+def _f8_bytes(layer: F8Linear, rows: int) -> int:
+    grouped = layer.experts is not None
+    key = (layer._c.n_experts, layer.in_features, layer.out_features, rows, grouped, layer.device.index)
+    nb = _f8_nb.get(key)
+    if nb is None:
+        f = lib().trellis_f8_moe_gemm_workspace_bytes if grouped else lib().trellis_f8_gemm_workspace_bytes
+        nb = f(layer._ref, rows)
+        if nb == 0:
+            raise TrellisError(-1, lib().trellis_last_error().decode())
+        if len(_f8_nb) >= 4096:
+            _f8_nb.clear()
+        _f8_nb[key] = nb
+    return nb
+
+
+def trellis_f8_workspace_bytes(layer: F8Linear, rows: int) -> int:
+    """Workspace bytes of trellis_f8_gemm (trellis_f8_moe_gemm for experts' matrices)."""
+    return _f8_bytes(layer, rows)
+
+
+def _f8_product(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, rows: int, dtype, out):
+    q_row = _f8_rows(q, "q", _E4M3, layer.device, layer.in_features)
+    s_row = _f8_rows(scale, "scale", torch.float32, layer.device, _f8_blocks(layer.in_features))
+    if scale.shape[0] != q.shape[0]:
+        raise ValueError(f"scale must have one row per row of q ({q.shape[0]}), got {scale.shape[0]}")
+    if out is None:
+        if dtype not in _F8_DTYPE:
+            raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+        out = torch.empty((rows, layer.out_features), dtype=dtype, device=layer.device)
+    y_row = _f8_rows(out, "out", None, layer.device, layer.out_features)
+    if out.shape[0] != rows:
+        raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
+    return q_row, s_row, out, y_row
+
+
+def trellis_f8_gemm(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.float16,
+                    out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M, out] (fp16 or bf16) of E4M3 rows q [M, in] with scales [M, ceil(in / 128)] and one
+    matrix; rows of q, scale and ``out`` may have strides of their own."""
+    if layer.experts is not None:
+        raise ValueError("the layer has one matrix per expert: trellis_f8_moe_gemm takes it")
+    M = q.shape[0]
+    q_row, s_row, out, y_row = _f8_product(layer, q, scale, M, dtype, out)
+    ws = _f8_ws(ws, _f8_bytes(layer, M), layer.device)
+    _check(lib().trellis_f8_gemm(layer._ref, q.data_ptr(), q_row, scale.data_ptr(), s_row, M, _F8_DTYPE[out.dtype],
+                                 out.data_ptr(), y_row, ws.data_ptr(), ws.numel(), _stream()))
+    return out
+
+
+def trellis_f8_moe_gemm(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, offsets: torch.Tensor,
+                        order: Optional[torch.Tensor] = None, per: int = 1, dtype: torch.dtype = torch.float16,
+                        out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows sorted by expert times their experts' matrices: row r in offsets[e] .. offsets[e+1]
+    (int32 [experts + 1]) takes matrix e and row r of q, or row order[r] // per of it (``order``
+    int32 [rows], trellis_moe_sort's, with per = choices a token).  Rows of ``out`` from the last
+    offset on are left alone."""
+    if layer.experts is None:
+        raise ValueError("the layer has one matrix: trellis_f8_gemm takes it")
+    _kv4_int(offsets, "offsets", layer.device)
+    if offsets.numel() != layer.experts + 1:
+        raise ValueError(f"offsets must have {layer.experts + 1} entries, got {offsets.numel()}")
+    if order is not None:
+        _kv4_int(order, "order", layer.device)
+    rows = q.shape[0] if order is None else order.numel()
+    q_row, s_row, out, y_row = _f8_product(layer, q, scale, rows, dtype, out)
+    ws = _f8_ws(ws, _f8_bytes(layer, rows), layer.device)
+    _check(lib().trellis_f8_moe_gemm(layer._ref, q.data_ptr(), q_row, scale.data_ptr(), s_row, q.shape[0], offsets.data_ptr(),
+                                     _ptr(order), per, rows, _F8_DTYPE[out.dtype], out.data_ptr(), y_row, ws.data_ptr(),
+                                     ws.numel(), _stream()))
+    return out
+
+
+def _moe_ids(t: torch.Tensor, name: str, device=None) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be [tokens, top]")
+    _req(t, torch.int32, name, device)
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}: the current device is cuda:{torch._C._cuda_getDevice()}")
+    return t.shape[0], t.shape[1]
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_sort_bytes(tokens: int, top: int, experts: int) -> int:
+    nb = lib().trellis_moe_sort_workspace_bytes(tokens, top, experts)
+    if nb == 0:
+        raise TrellisError(-1, lib().trellis_last_error().decode() or f"n_experts={experts} not in 1..2048")
+    return nb
+
+
+@functools.lru_cache(maxsize=None)
+def _moe_rows_bytes() -> int:
+    return lib().trellis_moe_rows_workspace_bytes()
+
+
+def trellis_moe_sort(ids: torch.Tensor, n_experts: int, offsets: Optional[torch.Tensor] = None,
+                     order: Optional[torch.Tensor] = None, inverse: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Routed ids int32 [tokens, top] (-1: not here) sorted by expert: (offsets [n_experts + 1],
+    order [tokens * top]: the entry t * top + j at each position, -1 behind the last, inverse
+    [tokens, top]: each entry's position or -1)."""
+    tokens, top = _moe_ids(ids, "ids")
+    i32, dev = torch.int32, ids.device
+    nb = _moe_sort_bytes(tokens, top, n_experts)
+    offsets = _out(offsets, (n_experts + 1,), dev, i32, "offsets")
+    order = _out(order, (tokens * top,), dev, i32, "order")
+    inverse = _out(inverse, (tokens, top), dev, i32, "inverse")
+    ws = _f8_ws(ws, nb, dev)
+    _check(lib().trellis_moe_sort(ids.data_ptr(), tokens, top, n_experts, offsets.data_ptr(), order.data_ptr(),
+                                  inverse.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return offsets, order, inverse
+
+
+def trellis_moe_gather(x: torch.Tensor, order: torch.Tensor, per: int, out: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows brought into the experts' order: out[p] = x[order[p] // per], x [tokens, n] of any
+    type whose rows are multiples of 4 bytes; rows whose entry is -1 are left as they are.  Its
+    gradient is ``trellis_moe_combine(d_out, inverse)``."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    x_row, e = _f8_rows(x, "x", x.dtype), x.element_size()
+    _kv4_int(order, "order", x.device)
+    tokens, n = x.shape
+    out = _out(out, (order.numel(), n), x.device, x.dtype)
+    ws = _f8_ws(ws, _moe_rows_bytes(), x.device)
+    _check(lib().trellis_moe_gather(x.data_ptr(), x_row * e, tokens, n * e, order.data_ptr(), order.numel(), per,
+                                    out.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return out
+
+
+def _moe_weights(weights: Optional[torch.Tensor], inverse: torch.Tensor) -> None:
+    if weights is not None:
+        _req(weights, torch.float32, "weights", inverse.device)
+        if weights.shape != inverse.shape:
+            raise ValueError(f"weights must be {tuple(inverse.shape)}, got {tuple(weights.shape)}")
+
+
+def _moe_rows(t: torch.Tensor, name: str, device, dtype=None, rows=None) -> None:
+    """A dense 16-bit [rows, n] tensor."""
+    _f8_rows(t, name, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
+
+
+def trellis_moe_combine(y: torch.Tensor, inverse: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                        add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = add[t] + sum_j weights[t, j] * y[inverse[t, j]] over the entries with a position:
+    y [rows, n] fp16 or bf16, inverse int32 [tokens, top], weights f32 [tokens, top] (None: ones),
+    add [tokens, n] (None: zeros; ``out=add`` adds in place)."""
+    tokens, top = _moe_ids(inverse, "inverse")
+    _moe_rows(y, "y", inverse.device)
+    _moe_weights(weights, inverse)
+    n = y.shape[1]
+    if add is not None:
+        _moe_rows(add, "add", inverse.device, y.dtype, tokens)
+        if add.shape[1] != n:
+            raise ValueError(f"add must be {(tokens, n)}, got {tuple(add.shape)}")
+    out = _out(out, (tokens, n), inverse.device, y.dtype)
+    ws = _f8_ws(ws, _moe_rows_bytes(), inverse.device)
+    _check(lib().trellis_moe_combine(_F8_DTYPE[y.dtype], y.data_ptr(), y.shape[0], n, inverse.data_ptr(), _ptr(weights), tokens,
+                                     top, _ptr(add), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return out
+
+
+def trellis_moe_combine_grad(d_out: torch.Tensor, y: torch.Tensor, inverse: torch.Tensor,
+                             weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                             d_weights: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """The gradient of trellis_moe_combine: (d_y, d_weights) for d_out [tokens, n] and the forward
+    pass's y; rows of d_y (``out``, which may be y) that no entry names are left as they are.
+    (That of add is d_out itself.)"""
+    tokens, top = _moe_ids(inverse, "inverse")
+    _moe_rows(y, "y", inverse.device)
+    rows, n = y.shape
+    _moe_rows(d_out, "d_out", inverse.device, y.dtype, tokens)
+    if d_out.shape[1] != n:
+        raise ValueError(f"d_out must be {(tokens, n)}, got {tuple(d_out.shape)}")
+    _moe_weights(weights, inverse)
+    out = _out(out, (rows, n), inverse.device, y.dtype)
+    d_weights = _out(d_weights, (tokens, top), inverse.device, torch.float32, "d_weights")
+    ws = _f8_ws(ws, _moe_rows_bytes(), inverse.device)
+    _check(lib().trellis_moe_combine_grad(_F8_DTYPE[y.dtype], d_out.data_ptr(), y.data_ptr(), rows, n, inverse.data_ptr(),
+                                          _ptr(weights), tokens, top, out.data_ptr(), d_weights.data_ptr(), ws.data_ptr(),
+                                          ws.numel(), _stream()))
+    return out, d_weights
 
 
 # ---------------------------------------------------------------------------------------

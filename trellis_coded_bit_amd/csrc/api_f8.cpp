@@ -114,6 +114,9 @@ int product(trellis::F8Gemm &a, int n_q, const char *what, void *ws, size_t ws_b
   if ((st = check_16("w", a.L.w)) || (st = check_4("matrix scale", a.L.scale)) || (st = check_16("q", a.q)) || (st = check_4("s", a.s)))
     return st;
   if ((st = check_stride("q", a.q_row, k, 16, n_q)) || (st = check_stride("s", a.s_row, kb, 1, n_q))) return st;
+  // the kernels count q's bytes from its start in 32 bits of 16
+  if (n_q > 1 && a.q_row > (1LL << 36) / n_q)
+    return abi_fail(TRELLIS_EINVAL, "q: %d rows at a stride of %lld bytes exceed 2^36", n_q, (long long)a.q_row);
   if (!a.y) return abi_fail(TRELLIS_EINVAL, "y is NULL");
   if (!aligned(a.y, 2)) return abi_fail(TRELLIS_EALIGN, "y must be 2-byte aligned");
   if ((st = check_stride("y", a.y_row, n, 1, a.rows))) return st;

@@ -19,19 +19,37 @@ struct GemmArgs {
   int kb;         // blocks of 128 inputs
   int col_tiles;  // tiles over out_features
   int row_tiles;  // tiles over rows, at most
+  int tile_rows;  // rows of a tile, at most
+  int y8;         // every row of y begins at a multiple of 8 bytes
 };
 
-// Which rows a tile of BM rows has: of expert e, rows [row, end).  e < 0: none.
+// Which rows a tile has: of expert e, rows [row, end).  e < 0: none.
 struct RowTile {
   int e, row, end;
 };
 
-// Tile `at` of the list: every expert's rows in tiles of BM, expert after expert.  Called by whole
-// waves; each lane looks at every 64th expert.  The list ends at the first pair of offsets that is
-// out of order or out of range.
-template <int BM>
+// n rows as tiles of at most T rows, T a multiple of U: as few as that takes, of the same size (a
+// multiple of U) but for the last.
+struct Cut {
+  int tiles, size;
+};
+template <int U>
+__device__ __forceinline__ Cut cut_rows(int n, int T) {
+  const int tiles = (n + T - 1) / T;
+  const int size = tiles ? ((n + tiles - 1) / tiles + U - 1) / U * U : U;
+  return {(n + size - 1) / size, size};
+}
+
+// Tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert after expert.
+// Called by whole waves; each lane looks at every 64th expert.  The list ends at the first pair of
+// offsets that is out of order or out of range.
+template <int U>
 __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool report) {
-  if (!p.g.offsets) return {0, at * BM, p.g.rows};
+  if (!p.g.offsets) {
+    const Cut c = cut_rows<U>(p.g.rows, p.tile_rows);
+    if (at >= c.tiles) return {-1, 0, 0};
+    return {0, at * c.size, min(p.g.rows, (at + 1) * c.size)};
+  }
   const int lane = threadIdx.x & 63, E = p.g.L.n_experts;
   if (ldg(p.g.offsets) != 0) {
     if (report && lane == 0) f8_error(p.errword);
@@ -46,8 +64,8 @@ __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool rep
     }
     const uint64_t bad = __ballot(a < 0 || b < a || b > p.g.rows);
     const int good = bad ? __builtin_ctzll(bad) : 64;
-    const int tiles = lane < good ? (b - a + BM - 1) / BM : 0;
-    int s = tiles;
+    const Cut c = cut_rows<U>(lane < good ? b - a : 0, p.tile_rows);
+    int s = c.tiles;
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(s, d, 64);
       if (lane >= d) s += o;
@@ -55,14 +73,14 @@ __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool rep
     const uint64_t has = __ballot(at < s);
     if (has) {
       const int l = __builtin_ctzll(has);
-      const int before = __shfl(s - tiles, l, 64);
-      return {e0 + l, __shfl(a, l, 64) + (at - before) * BM, __shfl(b, l, 64)};
+      const int row = a + (at - (s - c.tiles)) * c.size;
+      return {e0 + l, __builtin_amdgcn_readlane(row, l), __builtin_amdgcn_readlane(min(b, row + c.size), l)};
     }
     if (bad) {
       if (report && lane == 0) f8_error(p.errword);
       return {-1, 0, 0};
     }
-    at -= __shfl(s, 63, 64);
+    at -= __builtin_amdgcn_readlane(s, 63);
   }
   return {-1, 0, 0};
 }
@@ -123,6 +141,180 @@ __global__ __launch_bounds__(64) void simple_kernel(GemmArgs p) {
   }
 }
 
+// ---------------------------------------------------------------------------------------
+// Many rows: 256 matrix rows by up to 256 tokens a workgroup of eight waves, 64 by up to 128 a wave.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kWideThreads = 512, kWideOut = 256, kWideRows = 256;
+
+struct WideLds {
+  alignas(16) char w[2][kWideOut * 128], x[2][kWideRows * 128];  // a block of 128 inputs, two in turn
+  alignas(16) float sx[2][kWideRows], sw[2][64];
+};
+
+typedef __attribute__((address_space(1))) const void gbl_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane, copied to 16 * lane behind a place in shared memory, past the registers.
+__device__ __forceinline__ void copy16(const void *from, void *to) {
+  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 16, 0, 0);
+}
+__device__ __forceinline__ void copy4(const void *from, void *to) {
+  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 4, 0, 0);
+}
+
+// Where a lane's copies come from.  A row in shared memory is 128 bytes, eight chunks of 16; chunk
+// p of row r holds the row's chunk p ^ (r & 7), so that the products' reads of one chunk from
+// eight rows fall on eight places.  Lane l of a copy has row l / 8 of its eight rows.
+struct WideFrom {
+  uint32_t w[4], x[4];  // rows 64 j + 8 wave + l / 8: in 16 bytes from the tile's first row, from q
+  const float *s;       // waves 0..3: the scales of row 64 wave + l; wave 4: of the tile's matrix blocks
+  int chunk;
+};
+
+template <int MF>
+__device__ __forceinline__ void wide_copy(const GemmArgs &p, const char *w, const WideFrom &f, int wave, int b, WideLds &lds, int buf) {
+  const uint32_t u = (uint32_t)min(8 * b + f.chunk, p.g.L.in_features / 16 - 1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) copy16(w + ((uint64_t)(f.w[j] + u) << 4), lds.w[buf] + (64 * j + 8 * wave) * 128);
+#pragma unroll
+  for (int j = 0; j < (MF + 1) / 2; ++j)
+    if (64 * j + 32 < 32 * MF || wave < 4)
+      copy16(p.g.q + ((uint64_t)(f.x[j] + u) << 4), lds.x[buf] + (64 * j + 8 * wave) * 128);
+  if (wave < 4) copy4(f.s + b, lds.sx[buf] + 64 * wave);
+  else if (wave == 4) copy4(f.s + b, lds.sw[buf]);
+}
+
+__device__ __forceinline__ intx8 operand(const char *row, int lane) {
+  const int g = lane >> 4, r = lane & 7;
+  const u32x4 a = *reinterpret_cast<const u32x4 *>(row + ((g ^ r) << 4));
+  const u32x4 b = *reinterpret_cast<const u32x4 *>(row + (((g + 4) ^ r) << 4));
+  return intx8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+template <int MF>
+__device__ __forceinline__ void wide_block(const WideLds &lds, int buf, int lane, int wm, int wn, floatx4 (&acc)[MF][4]) {
+  const int i = lane & 15;
+  intx8 w[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) w[n] = operand(lds.w[buf] + (64 * wn + 16 * n + i) * 128, lane);
+  const float sw = lds.sw[buf][wn >> 1];
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const intx8 x = operand(lds.x[buf] + (16 * MF * wm + 16 * m + i) * 128, lane);
+    const float f = lds.sx[buf][16 * MF * wm + 16 * m + i] * sw;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+      const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n], x, zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d[j], f, acc[m][n][j]);
+    }
+  }
+}
+
+// The last block of in_features that are no multiple of 128: chunks behind the end become zero.
+template <int MF>
+__device__ __forceinline__ void wide_clear(const GemmArgs &p, int wave, int lane, WideLds &lds, int buf) {
+  const int chunk = (lane & 7) ^ (lane >> 3), rest = (p.g.L.in_features & 127) >> 4;
+  if (chunk < rest) return;
+  const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    *reinterpret_cast<u32x4 *>(lds.w[buf] + (64 * j + 8 * wave) * 128 + 16 * lane) = zero;
+    *reinterpret_cast<u32x4 *>(lds.x[buf] + (64 * j + 8 * wave) * 128 + 16 * lane) = zero;
+  }
+}
+
+template <bool BF, int MF>
+__device__ __forceinline__ void wide_tile(const GemmArgs &p, const RowTile &t, int n0, WideLds &lds) {
+  const trellis_f8_linear &L = p.g.L;
+  const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const char *w = reinterpret_cast<const char *>(L.w) + ((int64_t)t.e * N + n0) * K;
+  WideFrom f;
+  f.chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 64 * j + 8 * wave + (lane >> 3);
+    f.w[j] = (uint32_t)min(r, N - 1 - n0) * (uint32_t)(K >> 4);
+    f.x[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + r, t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
+  }
+  if (wave < 4) f.s = p.g.s + (int64_t)max(source_row(p, min(t.row + 64 * wave + lane, t.end - 1)), 0) * p.g.s_row;
+  else f.s = L.scale + ((int64_t)t.e * nb + min((n0 >> 7) + (lane & 1), nb - 1)) * p.kb;
+  floatx4 acc[MF][4];
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+  wide_copy<MF>(p, w, f, wave, 0, lds, 0);
+  for (int b = 0; b < p.kb; ++b) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies of block b have arrived
+    __syncthreads();
+    if (b + 1 < p.kb) wide_copy<MF>(p, w, f, wave, b + 1, lds, (b + 1) & 1);
+    else if (K & 127) {
+      wide_clear<MF>(p, wave, lane, lds, b & 1);
+      __syncthreads();
+    }
+    wide_block<MF>(lds, b & 1, lane, wm, wn, acc);
+  }
+  const int g = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int row = t.row + 16 * MF * wm + 16 * m + (lane & 15);
+    if (row >= t.end) continue;
+    const bool zero = p.g.order && source_row(p, row) < 0;
+    uint16_t *y = p.g.y + (int64_t)row * p.g.y_row;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int c = n0 + 64 * wn + 16 * n + 4 * g;
+      uint16_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = f8_narrow<BF>(zero ? 0.f : acc[m][n][j]);
+      if (p.y8 && c + 4 <= N) {
+        stg(reinterpret_cast<u32x2 *>(y + c), u32x2{v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16});
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < N) stg(y + c + j, v[j]);
+      }
+    }
+  }
+}
+
+// Tiles in an order that keeps what runs at a time on one XCD (every eighth workgroup) close
+// together: eight row tiles by the column tiles, row tiles first.
+__device__ __forceinline__ void tile_of(const GemmArgs &p, int block, int &rt, int &ct) {
+  const int total = p.row_tiles * p.col_tiles, per = total >> 3, rest = total & 7;
+  const int x = block & 7, at = x * per + min(x, rest) + (block >> 3);
+  const int band = at / (8 * p.col_tiles), in = at - band * 8 * p.col_tiles;
+  const int high = min(8, p.row_tiles - 8 * band);
+  ct = in / high;
+  rt = 8 * band + in - ct * high;
+}
+
+template <bool BF>
+__global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
+  extern __shared__ char raw[];
+  WideLds &lds = *reinterpret_cast<WideLds *>(raw);
+  int rt, ct;
+  tile_of(p, blockIdx.x, rt, ct);
+  const RowTile t = find_tile<32>(p, rt, rt == p.row_tiles - 1 && ct == 0);
+  if (t.e < 0) return;
+  const int n0 = ct * kWideOut;
+  switch ((t.end - t.row + 31) >> 5) {
+    case 8: wide_tile<BF, 8>(p, t, n0, lds); break;
+    case 7: wide_tile<BF, 7>(p, t, n0, lds); break;
+    case 6: wide_tile<BF, 6>(p, t, n0, lds); break;
+    case 5: wide_tile<BF, 5>(p, t, n0, lds); break;
+    case 4: wide_tile<BF, 4>(p, t, n0, lds); break;
+    case 3: wide_tile<BF, 3>(p, t, n0, lds); break;
+    case 2: wide_tile<BF, 2>(p, t, n0, lds); break;
+    default: wide_tile<BF, 1>(p, t, n0, lds); break;
+  }
+}
+
 }  // namespace
 
 size_t f8_gemm_workspace_bytes(const trellis_f8_linear &L, int rows, bool grouped) { return kWsReserved; }
@@ -132,11 +324,37 @@ hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
   p.g = a;
   p.errword = static_cast<uint32_t *>(ws);
   p.kb = (a.L.in_features + 127) / 128;
-  p.col_tiles = (a.L.out_features + 15) / 16;
-  p.row_tiles = a.offsets ? a.rows / 16 + min(a.rows, a.L.n_experts) : (a.rows + 15) / 16;
+  p.y8 = a.y_row % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
+  const bool wide = a.rows >= (a.offsets ? 32LL * a.L.n_experts : 128);
+  if (!wide) {
+    p.tile_rows = 16;
+    p.col_tiles = (a.L.out_features + 15) / 16;
+    p.row_tiles = a.offsets ? a.rows / 16 + min(a.rows, a.L.n_experts) : (a.rows + 15) / 16;
+    const long long grid = (long long)p.row_tiles * p.col_tiles;
+    if (a.bf16) simple_kernel<true><<<(unsigned)grid, 64, 0, stream>>>(p);
+    else simple_kernel<false><<<(unsigned)grid, 64, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  p.col_tiles = (a.L.out_features + kWideOut - 1) / kWideOut;
+  p.tile_rows = kWideRows;
+  if (!a.offsets) {
+    long long best = -1;
+    for (int mf = 8; mf >= 4; --mf) {  // rounds of 256 workgroups, each about as long as its rows
+      const long long tiles = (long long)((a.rows + 32 * mf - 1) / (32 * mf)) * p.col_tiles;
+      const long long cost = (tiles + 255) / 256 * (mf + 1);
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.tile_rows = 32 * mf;
+      }
+    }
+  }
+  p.row_tiles = a.offsets ? a.rows / p.tile_rows + min(a.rows, a.L.n_experts) : (a.rows + p.tile_rows - 1) / p.tile_rows;
   const long long grid = (long long)p.row_tiles * p.col_tiles;
-  if (a.bf16) simple_kernel<true><<<(unsigned)grid, 64, 0, stream>>>(p);
-  else simple_kernel<false><<<(unsigned)grid, 64, 0, stream>>>(p);
+  const void *kernel = a.bf16 ? reinterpret_cast<const void *>(wide_kernel<true>) : reinterpret_cast<const void *>(wide_kernel<false>);
+  const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WideLds));
+  if (e != hipSuccess) return e;
+  if (a.bf16) wide_kernel<true><<<(unsigned)grid, kWideThreads, sizeof(WideLds), stream>>>(p);
+  else wide_kernel<false><<<(unsigned)grid, kWideThreads, sizeof(WideLds), stream>>>(p);
   return hipGetLastError();
 }
 

@@ -165,24 +165,52 @@ __device__ __forceinline__ void copy4(const void *from, void *to) {
 
 // Where a lane's copies come from.  A row in shared memory is 128 bytes, eight chunks of 16; chunk
 // p of row r holds the row's chunk p ^ (r & 7), so that the products' reads of one chunk from
-// eight rows fall on eight places.  Lane l of a copy has row l / 8 of its eight rows.
+// eight rows fall on eight places.  Lane l of a copy has row l / 8 of its eight rows.  Chunks
+// behind in_features repeat the row's last one; the products take zeros of the matrix there.
 struct WideFrom {
   uint32_t w[4], x[4];  // rows 64 j + 8 wave + l / 8: in 16 bytes from the tile's first row, from q
-  const float *s;       // waves 0..3: the scales of row 64 wave + l; wave 4: of the tile's matrix blocks
+  const float *s;       // waves 0..3: the scales of row 64 wave + l; 4..7: of the tile's matrix blocks
   int chunk;
 };
 
+// The copies of a block are made in two parts: the matrix and the tokens that the first products
+// take, and the other tokens (64 a copy: what two of a wave's tiles take) with the scales.
 template <int MF>
-__device__ __forceinline__ void wide_copy(const GemmArgs &p, const char *w, const WideFrom &f, int wave, int b, WideLds &lds, int buf) {
+struct WidePart {
+  static constexpr int copies = (MF + 1) / 2, first = copies / 2, second = copies - first + 1;
+  static constexpr int tiles = 2 * first;  // of a wave in the first part
+};
+template <int MF>
+__device__ __forceinline__ void wide_copy_x(const GemmArgs &p, const WideFrom &f, int wave, uint32_t u, int j, WideLds &lds, int buf) {
+  // (of an odd number of tiles the last copy's second half would not be read; it is made all the
+  // same, so that every wave has the same number under way)
+  copy16(p.g.q + ((uint64_t)(f.x[j] + u) << 4), lds.x[buf] + (64 * j + 8 * wave) * 128);
+}
+template <int MF>
+__device__ __forceinline__ void wide_copy1(const GemmArgs &p, const char *w, const WideFrom &f, int wave, int b, WideLds &lds) {
   const uint32_t u = (uint32_t)min(8 * b + f.chunk, p.g.L.in_features / 16 - 1);
+  const int buf = b & 1;
 #pragma unroll
   for (int j = 0; j < 4; ++j) copy16(w + ((uint64_t)(f.w[j] + u) << 4), lds.w[buf] + (64 * j + 8 * wave) * 128);
 #pragma unroll
-  for (int j = 0; j < (MF + 1) / 2; ++j)
-    if (64 * j + 32 < 32 * MF || wave < 4)
-      copy16(p.g.q + ((uint64_t)(f.x[j] + u) << 4), lds.x[buf] + (64 * j + 8 * wave) * 128);
-  if (wave < 4) copy4(f.s + b, lds.sx[buf] + 64 * wave);
-  else if (wave == 4) copy4(f.s + b, lds.sw[buf]);
+  for (int j = 0; j < WidePart<MF>::first; ++j) wide_copy_x<MF>(p, f, wave, u, j, lds, buf);
+}
+template <int MF>
+__device__ __forceinline__ void wide_copy2(const GemmArgs &p, const WideFrom &f, int wave, int b, WideLds &lds) {
+  const uint32_t u = (uint32_t)min(8 * b + f.chunk, p.g.L.in_features / 16 - 1);
+#pragma unroll
+  for (int j = WidePart<MF>::first; j < WidePart<MF>::copies; ++j) wide_copy_x<MF>(p, f, wave, u, j, lds, b & 1);
+  copy4(f.s + b, wave < 4 ? lds.sx[b & 1] + 64 * wave : lds.sw[b & 1]);  // (waves 4..7: the same)
+}
+
+// Waits until at most N of this wave's copies are under way, then for the workgroup's other waves.
+// Reads of shared memory stay on their side of it.
+template <int N>
+__device__ __forceinline__ void wide_meet() {
+  static_assert(N < 16, "the lower four bits of the count");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 __device__ __forceinline__ intx8 operand(const char *row, int lane) {
@@ -191,39 +219,96 @@ __device__ __forceinline__ intx8 operand(const char *row, int lane) {
   const u32x4 b = *reinterpret_cast<const u32x4 *>(row + (((g + 4) ^ r) << 4));
   return intx8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
-
-template <int MF>
-__device__ __forceinline__ void wide_block(const WideLds &lds, int buf, int lane, int wm, int wn, floatx4 (&acc)[MF][4]) {
-  const int i = lane & 15;
-  intx8 w[4];
+// The chunks behind `rest` channels of a block become zero.
+__device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
+  const int g = lane >> 4;
 #pragma unroll
-  for (int n = 0; n < 4; ++n) w[n] = operand(lds.w[buf] + (64 * wn + 16 * n + i) * 128, lane);
-  const float sw = lds.sw[buf][wn >> 1];
-#pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const intx8 x = operand(lds.x[buf] + (16 * MF * wm + 16 * m + i) * 128, lane);
-    const float f = lds.sx[buf][16 * MF * wm + 16 * m + i] * sw;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-      const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n], x, zero, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d[j], f, acc[m][n][j]);
-    }
-  }
+  for (int j = 0; j < 8; ++j) w[j] = 16 * (g + 4 * (j >> 2)) < rest ? w[j] : 0;
 }
 
-// The last block of in_features that are no multiple of 128: chunks behind the end become zero.
+// A wave's 64 matrix rows by 16 MF tokens over all blocks.  Its tile m takes tokens 32 m + 16 wm ..
+// A product's results are added to the sums while the next four products run, and operands are
+// read one tile ahead, the next block's first ones too: what they wait for was met half a block
+// before.  Two meetings a block: at the middle all waves have read the block's matrix and first
+// tokens, whose places then take the block after next; at the end the rest.
+constexpr int kBehind = 3;  // products between one and the use of its results (at most 4)
+
 template <int MF>
-__device__ __forceinline__ void wide_clear(const GemmArgs &p, int wave, int lane, WideLds &lds, int buf) {
-  const int chunk = (lane & 7) ^ (lane >> 3), rest = (p.g.L.in_features & 127) >> 4;
-  if (chunk < rest) return;
-  const u32x4 zero = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    *reinterpret_cast<u32x4 *>(lds.w[buf] + (64 * j + 8 * wave) * 128 + 16 * lane) = zero;
-    *reinterpret_cast<u32x4 *>(lds.x[buf] + (64 * j + 8 * wave) * 128 + 16 * lane) = zero;
+__device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_w, const WideFrom &f, int wave, int lane, WideLds &lds,
+                                            floatx4 (&acc)[MF][4]) {
+  using Part = WidePart<MF>;
+  const int i = lane & 15, wm = wave & 1, wn = wave >> 1, kb = p.kb, rest = p.g.L.in_features & 127;
+  const char *wp = lds.w[0] + (64 * wn + i) * 128, *xp = lds.x[0] + (16 * wm + i) * 128;
+  constexpr int kBuf = kWideOut * 128;
+  wide_copy1<MF>(p, from_w, f, wave, 0, lds);
+  wide_copy2<MF>(p, f, wave, 0, lds);
+  if (kb > 1) {
+    wide_copy1<MF>(p, from_w, f, wave, 1, lds);
+    wide_copy2<MF>(p, f, wave, 1, lds);
+    wide_meet<4 + Part::first + Part::second>();
+  } else {
+    wide_meet<0>();
   }
+  intx8 w[4], next;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) w[n] = operand(wp + n * 2048, lane);
+  next = operand(xp, lane);
+  const float *sx = lds.sx[0] + 16 * wm + i;
+  float s[2] = {0.f, 0.f};              // of this tile's products and the last one's
+  floatx4 d[kBehind];                   // the last products
+#pragma unroll
+  for (int k = 0; k < kBehind; ++k) d[k] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma clang loop unroll(disable)
+  for (int b = 0; b < kb; ++b) {
+    const int buf = b & 1;
+    if (rest && b == kb - 1)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) clear_behind(w[n], lane, rest);
+    const float sw = lds.sw[buf][wn >> 1];
+    float sn = sx[buf * kWideRows];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      if (m == Part::tiles) {
+        // (before the block's first product its matrix operands may still be on their way from
+        // where the copies go)
+        if (m == 0) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wide_meet<Part::second>();
+        if (b + 2 < kb) wide_copy1<MF>(p, from_w, f, wave, b + 2, lds);
+      }
+      const intx8 x = next;
+      if (m + 1 < MF) next = operand(xp + buf * kBuf + (m + 1) * 4096, lane);
+      else if (Part::tiles) next = operand(xp + (buf ^ 1) * kBuf, lane);
+      s[1] = s[0];
+      s[0] = sn * sw;
+      if (m + 1 < MF) sn = sx[buf * kWideRows + 32 * (m + 1)];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+        const floatx4 e = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n], x, zero, 0, 0, 0, 0, 0, 0);
+        floatx4 &into = acc[n < kBehind ? (m + MF - 1) % MF : m][(n + 4 - kBehind) & 3];
+        const float by = s[n < kBehind];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) into[j] = fmaf(d[0][j], by, into[j]);
+        asm volatile("" : "+v"(into));  // (here, not where the sums are used)
+#pragma unroll
+        for (int k = 0; k + 1 < kBehind; ++k) d[k] = d[k + 1];
+        d[kBehind - 1] = e;
+        if (m + 1 == MF) w[n] = operand(wp + (buf ^ 1) * kBuf + n * 2048, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (b + 2 < kb) {
+      wide_meet<4 + Part::first>();
+      wide_copy2<MF>(p, f, wave, b + 2, lds);
+    } else {
+      wide_meet<0>();
+    }
+    if (!Part::tiles) next = operand(xp + (buf ^ 1) * kBuf, lane);  // (all tokens are in the second part)
+  }
+#pragma unroll
+  for (int n = 0; n < kBehind; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[MF - 1][n + 4 - kBehind][j] = fmaf(d[n][j], s[0], acc[MF - 1][n + 4 - kBehind][j]);
 }
 
 template <bool BF, int MF>
@@ -239,7 +324,8 @@ __device__ __forceinline__ void wide_tile(const GemmArgs &p, const RowTile &t, i
   for (int j = 0; j < 4; ++j) {
     const int r = 64 * j + 8 * wave + (lane >> 3);
     f.w[j] = (uint32_t)min(r, N - 1 - n0) * (uint32_t)(K >> 4);
-    f.x[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + r, t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
+    if (j < WidePart<MF>::copies)
+      f.x[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + r, t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
   }
   if (wave < 4) f.s = p.g.s + (int64_t)max(source_row(p, min(t.row + 64 * wave + lane, t.end - 1)), 0) * p.g.s_row;
   else f.s = L.scale + ((int64_t)t.e * nb + min((n0 >> 7) + (lane & 1), nb - 1)) * p.kb;
@@ -248,21 +334,11 @@ __device__ __forceinline__ void wide_tile(const GemmArgs &p, const RowTile &t, i
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int n = 0; n < 4; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-  wide_copy<MF>(p, w, f, wave, 0, lds, 0);
-  for (int b = 0; b < p.kb; ++b) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's copies of block b have arrived
-    __syncthreads();
-    if (b + 1 < p.kb) wide_copy<MF>(p, w, f, wave, b + 1, lds, (b + 1) & 1);
-    else if (K & 127) {
-      wide_clear<MF>(p, wave, lane, lds, b & 1);
-      __syncthreads();
-    }
-    wide_block<MF>(lds, b & 1, lane, wm, wn, acc);
-  }
+  wide_blocks<MF>(p, w, f, wave, lane, lds, acc);
   const int g = lane >> 4;
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
-    const int row = t.row + 16 * MF * wm + 16 * m + (lane & 15);
+    const int row = t.row + 32 * m + 16 * wm + (lane & 15);
     if (row >= t.end) continue;
     const bool zero = p.g.order && source_row(p, row) < 0;
     uint16_t *y = p.g.y + (int64_t)row * p.g.y_row;

@@ -20,7 +20,7 @@ struct GemmArgs {
   int col_tiles;  // tiles over out_features
   int row_tiles;  // tiles over rows, at most
   int tile_rows;  // rows of a tile, at most
-  int y8;         // every row of y begins at a multiple of 8 bytes
+  int y16;        // every row of y begins at a multiple of 16 bytes
 };
 
 // Which rows a tile has: of expert e, rows [row, end).  e < 0: none.
@@ -41,21 +41,20 @@ __device__ __forceinline__ Cut cut_rows(int n, int T) {
 }
 
 // Tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert after expert.
-// Called by whole waves; each lane looks at every 64th expert.  The list ends at the first pair of
-// offsets that is out of order or out of range.
+// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  Called by whole waves;
+// each lane looks at every 64th expert.  The list ends at the first pair of offsets that is out of
+// order or out of range.
 template <int U>
 __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool report) {
   if (!p.g.offsets) {
     const Cut c = cut_rows<U>(p.g.rows, p.tile_rows);
-    if (at >= c.tiles) return {-1, 0, 0};
+    if (at >= c.tiles) return {-1, c.tiles, 0};
     return {0, at * c.size, min(p.g.rows, (at + 1) * c.size)};
   }
-  const int lane = threadIdx.x & 63, E = p.g.L.n_experts;
-  if (ldg(p.g.offsets) != 0) {
-    if (report && lane == 0) f8_error(p.errword);
-    return {-1, 0, 0};
-  }
-  for (int e0 = 0; e0 < E; e0 += 64) {
+  const int lane = opaque_tid() & 63, E = p.g.L.n_experts;
+  int passed = 0;
+  bool wrong = ldg(p.g.offsets) != 0;
+  for (int e0 = 0; e0 < E && !wrong; e0 += 64) {
     const int e = e0 + lane;
     int a = 0, b = 0;
     if (e < E) {
@@ -70,19 +69,17 @@ __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool rep
       const int o = __shfl_up(s, d, 64);
       if (lane >= d) s += o;
     }
-    const uint64_t has = __ballot(at < s);
+    const uint64_t has = __ballot(at < passed + s);
     if (has) {
       const int l = __builtin_ctzll(has);
-      const int row = a + (at - (s - c.tiles)) * c.size;
+      const int row = a + (at - passed - (s - c.tiles)) * c.size;
       return {e0 + l, __builtin_amdgcn_readlane(row, l), __builtin_amdgcn_readlane(min(b, row + c.size), l)};
     }
-    if (bad) {
-      if (report && lane == 0) f8_error(p.errword);
-      return {-1, 0, 0};
-    }
-    at -= __builtin_amdgcn_readlane(s, 63);
+    passed += __builtin_amdgcn_readlane(s, 63);
+    wrong = bad != 0;
   }
-  return {-1, 0, 0};
+  if (wrong && report && lane == 0) f8_error(p.errword);
+  return {-1, passed, 0};
 }
 
 // The row of q that a row reads, or -1.
@@ -180,7 +177,6 @@ struct WidePart {
   static constexpr int copies = (MF + 1) / 2, first = copies / 2, second = copies - first + 1;
   static constexpr int tiles = 2 * first;  // of a wave in the first part
 };
-template <int MF>
 __device__ __forceinline__ void wide_copy_x(const GemmArgs &p, const WideFrom &f, int wave, uint32_t u, int j, WideLds &lds, int buf) {
   // (of an odd number of tiles the last copy's second half would not be read; it is made all the
   // same, so that every wave has the same number under way)
@@ -193,13 +189,13 @@ __device__ __forceinline__ void wide_copy1(const GemmArgs &p, const char *w, con
 #pragma unroll
   for (int j = 0; j < 4; ++j) copy16(w + ((uint64_t)(f.w[j] + u) << 4), lds.w[buf] + (64 * j + 8 * wave) * 128);
 #pragma unroll
-  for (int j = 0; j < WidePart<MF>::first; ++j) wide_copy_x<MF>(p, f, wave, u, j, lds, buf);
+  for (int j = 0; j < WidePart<MF>::first; ++j) wide_copy_x(p, f, wave, u, j, lds, buf);
 }
 template <int MF>
 __device__ __forceinline__ void wide_copy2(const GemmArgs &p, const WideFrom &f, int wave, int b, WideLds &lds) {
   const uint32_t u = (uint32_t)min(8 * b + f.chunk, p.g.L.in_features / 16 - 1);
 #pragma unroll
-  for (int j = WidePart<MF>::first; j < WidePart<MF>::copies; ++j) wide_copy_x<MF>(p, f, wave, u, j, lds, b & 1);
+  for (int j = WidePart<MF>::first; j < WidePart<MF>::copies; ++j) wide_copy_x(p, f, wave, u, j, lds, b & 1);
   copy4(f.s + b, wave < 4 ? lds.sx[b & 1] + 64 * wave : lds.sw[b & 1]);  // (waves 4..7: the same)
 }
 
@@ -229,26 +225,22 @@ __device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
 // A wave's 64 matrix rows by 16 MF tokens over all blocks.  Its tile m takes tokens 32 m + 16 wm ..
 // A product's results are added to the sums while the next four products run, and operands are
 // read one tile ahead, the next block's first ones too: what they wait for was met half a block
-// before.  Two meetings a block: at the middle all waves have read the block's matrix and first
+// before.  On entry blocks 0 and 1 are in shared memory.  Two meetings a block: at the middle all waves have read the block's matrix and first
 // tokens, whose places then take the block after next; at the end the rest.
 constexpr int kBehind = 3;  // products between one and the use of its results (at most 4)
 
 template <int MF>
-__device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_w, const WideFrom &f, int wave, int lane, WideLds &lds,
+__device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_w, const WideFrom &f, int wave, WideLds &lds,
                                             floatx4 (&acc)[MF][4]) {
+  const int lane = opaque_tid() & 63;
   using Part = WidePart<MF>;
   const int i = lane & 15, wm = wave & 1, wn = wave >> 1, kb = p.kb, rest = p.g.L.in_features & 127;
   const char *wp = lds.w[0] + (64 * wn + i) * 128, *xp = lds.x[0] + (16 * wm + i) * 128;
   constexpr int kBuf = kWideOut * 128;
-  wide_copy1<MF>(p, from_w, f, wave, 0, lds);
-  wide_copy2<MF>(p, f, wave, 0, lds);
-  if (kb > 1) {
-    wide_copy1<MF>(p, from_w, f, wave, 1, lds);
-    wide_copy2<MF>(p, f, wave, 1, lds);
-    wide_meet<4 + Part::first + Part::second>();
-  } else {
-    wide_meet<0>();
-  }
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
   intx8 w[4], next;
 #pragma unroll
   for (int n = 0; n < 4; ++n) w[n] = operand(wp + n * 2048, lane);
@@ -311,83 +303,143 @@ __device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_
     for (int j = 0; j < 4; ++j) acc[MF - 1][n + 4 - kBehind][j] = fmaf(d[n][j], s[0], acc[MF - 1][n + 4 - kBehind][j]);
 }
 
-template <bool BF, int MF>
-__device__ __forceinline__ void wide_tile(const GemmArgs &p, const RowTile &t, int n0, WideLds &lds) {
+// A tile to be: its rows, its first matrix row, and where its copies come from.
+struct WideTile {
+  RowTile t;
+  int n0;
+  const char *w;
+  WideFrom f;
+};
+
+// Looks a tile up and starts the copies of its first two blocks.
+__device__ __forceinline__ void wide_begin(const GemmArgs &p, WideTile &x, int wave, WideLds &lds) {
+  const int lane = opaque_tid() & 63;
   const trellis_f8_linear &L = p.g.L;
   const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
-  const char *w = reinterpret_cast<const char *>(L.w) + ((int64_t)t.e * N + n0) * K;
-  WideFrom f;
+  x.w = reinterpret_cast<const char *>(L.w) + ((int64_t)x.t.e * N + x.n0) * K;
+  WideFrom &f = x.f;
   f.chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = 64 * j + 8 * wave + (lane >> 3);
-    f.w[j] = (uint32_t)min(r, N - 1 - n0) * (uint32_t)(K >> 4);
-    if (j < WidePart<MF>::copies)
-      f.x[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + r, t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
+    f.w[j] = (uint32_t)min(r, N - 1 - x.n0) * (uint32_t)(K >> 4);
+    f.x[j] = (uint32_t)((uint64_t)max(source_row(p, min(x.t.row + r, x.t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
   }
-  if (wave < 4) f.s = p.g.s + (int64_t)max(source_row(p, min(t.row + 64 * wave + lane, t.end - 1)), 0) * p.g.s_row;
-  else f.s = L.scale + ((int64_t)t.e * nb + min((n0 >> 7) + (lane & 1), nb - 1)) * p.kb;
-  floatx4 acc[MF][4];
+  if (wave < 4) f.s = p.g.s + (int64_t)max(source_row(p, min(x.t.row + 64 * wave + lane, x.t.end - 1)), 0) * p.g.s_row;
+  else f.s = L.scale + ((int64_t)x.t.e * nb + min((x.n0 >> 7) + (lane & 1), nb - 1)) * p.kb;
+  const int copies = (x.t.end - x.t.row + 63) >> 6;
+  for (int b = 0; b < min(p.kb, 2); ++b) {
+    const uint32_t u = (uint32_t)min(8 * b + f.chunk, K / 16 - 1);
 #pragma unroll
-  for (int m = 0; m < MF; ++m)
+    for (int j = 0; j < 4; ++j) copy16(x.w + ((uint64_t)(f.w[j] + u) << 4), lds.w[b] + (64 * j + 8 * wave) * 128);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-  wide_blocks<MF>(p, w, f, wave, lane, lds, acc);
-  const int g = lane >> 4;
+    for (int j = 0; j < 4; ++j)
+      if (j < copies) wide_copy_x(p, f, wave, u, j, lds, b);
+    copy4(f.s + b, wave < 4 ? lds.sx[b] + 64 * wave : lds.sw[b]);
+  }
+}
+
+// The sums of a tile, rounded and stored.  A lane has four neighbouring columns
+// of one token in each of its tiles; two tiles' are exchanged between neighbouring rows of lanes
+// so that it has eight of one.
+template <bool BF, int MF>
+__device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, int n0, int wave, const floatx4 (&acc)[MF][4]) {
+  const int lane = opaque_tid() & 63;
+  const int N = p.g.L.out_features, wm = wave & 1, wn = wave >> 1, g = lane >> 4;
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
     const int row = t.row + 32 * m + 16 * wm + (lane & 15);
-    if (row >= t.end) continue;
-    const bool zero = p.g.order && source_row(p, row) < 0;
+    const bool live = row < t.end;
+    const bool zero = live && p.g.order && source_row(p, row) < 0;
     uint16_t *y = p.g.y + (int64_t)row * p.g.y_row;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int c = n0 + 64 * wn + 16 * n + 4 * g;
-      uint16_t v[4];
+    for (int n = 0; n < 4; n += 2) {
+      u32x2 v[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = f8_narrow<BF>(zero ? 0.f : acc[m][n][j]);
-      if (p.y8 && c + 4 <= N) {
-        stg(reinterpret_cast<u32x2 *>(y + c), u32x2{v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16});
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const floatx4 &a = acc[m][n + h];
+          v[h][j] = zero ? 0u : f8_narrow<BF>(a[2 * j]) | (uint32_t)f8_narrow<BF>(a[2 * j + 1]) << 16;
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v[0][j], v[1][j], false, false);
+        v[0][j] = r[0];
+        v[1][j] = r[1];
+      }
+      // lanes of even rows have the first tile's columns, those of odd rows the second's
+      const int c = n0 + 64 * wn + 16 * (n + (g & 1)) + 8 * (g >> 1);
+      if (!live) continue;
+      if (p.y16 && c + 8 <= N) {
+        stg(reinterpret_cast<u32x4 *>(y + c), u32x4{v[0][0], v[0][1], v[1][0], v[1][1]});
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < N) stg(y + c + j, v[j]);
+        for (int j = 0; j < 8; ++j)
+          if (c + j < N) stg(y + c + j, (uint16_t)(v[j >> 2][(j >> 1) & 1] >> (16 * (j & 1))));
       }
     }
   }
 }
 
 // Tiles in an order that keeps what runs at a time on one XCD (every eighth workgroup) close
-// together: eight row tiles by the column tiles, row tiles first.
-__device__ __forceinline__ void tile_of(const GemmArgs &p, int block, int &rt, int &ct) {
-  const int total = p.row_tiles * p.col_tiles, per = total >> 3, rest = total & 7;
-  const int x = block & 7, at = x * per + min(x, rest) + (block >> 3);
+// together: eight row tiles by the column tiles, row tiles first.  Each XCD has a run of the list.
+__device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int turn, int &rt, int &ct) {
+  const int total = row_tiles * p.col_tiles, per = total >> 3, rest = total & 7;
+  const int x = blockIdx.x & 7, i = (blockIdx.x >> 3) + turn * ((int)gridDim.x >> 3);
+  if (i >= per + (x < rest)) return false;
+  const int at = x * per + min(x, rest) + i;
   const int band = at / (8 * p.col_tiles), in = at - band * 8 * p.col_tiles;
-  const int high = min(8, p.row_tiles - 8 * band);
+  const int high = min(8, row_tiles - 8 * band);
   ct = in / high;
   rt = 8 * band + in - ct * high;
+  return true;
 }
 
+// One tile's products; the next tile's first copies are under way while this one is stored.
+template <bool BF, int MF>
+__device__ __forceinline__ bool wide_tile(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
+  floatx4 acc[MF][4];
+  wide_blocks<MF>(p, x.w, x.f, wave, lds, acc);
+  const RowTile t = x.t;
+  const int n0 = x.n0;
+  int rt, ct;
+  const bool more = tile_of(p, row_tiles, turn, rt, ct);
+  if (more) {
+    x.t = find_tile<32>(p, rt, false);
+    x.n0 = ct * kWideOut;
+    wide_begin(p, x, wave, lds);
+  }
+  wide_store<BF, MF>(p, t, n0, wave, acc);
+  return more;
+}
+
+// One workgroup a CU, tile after tile.
 template <bool BF>
 __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   extern __shared__ char raw[];
   WideLds &lds = *reinterpret_cast<WideLds *>(raw);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row_tiles = find_tile<32>(p, 0x7FFFFFFF, blockIdx.x == 0).row;
+  WideTile x;
   int rt, ct;
-  tile_of(p, blockIdx.x, rt, ct);
-  const RowTile t = find_tile<32>(p, rt, rt == p.row_tiles - 1 && ct == 0);
-  if (t.e < 0) return;
-  const int n0 = ct * kWideOut;
-  switch ((t.end - t.row + 31) >> 5) {
-    case 8: wide_tile<BF, 8>(p, t, n0, lds); break;
-    case 7: wide_tile<BF, 7>(p, t, n0, lds); break;
-    case 6: wide_tile<BF, 6>(p, t, n0, lds); break;
-    case 5: wide_tile<BF, 5>(p, t, n0, lds); break;
-    case 4: wide_tile<BF, 4>(p, t, n0, lds); break;
-    case 3: wide_tile<BF, 3>(p, t, n0, lds); break;
-    case 2: wide_tile<BF, 2>(p, t, n0, lds); break;
-    default: wide_tile<BF, 1>(p, t, n0, lds); break;
+  if (!tile_of(p, row_tiles, 0, rt, ct)) return;
+  x.t = find_tile<32>(p, rt, false);
+  x.n0 = ct * kWideOut;
+  wide_begin(p, x, wave, lds);
+  bool more = true;
+  for (int turn = 1; more; ++turn) {
+    wide_meet<0>();
+    switch ((x.t.end - x.t.row + 31) >> 5) {
+      case 8: more = wide_tile<BF, 8>(p, row_tiles, turn, wave, x, lds); break;
+      case 7: more = wide_tile<BF, 7>(p, row_tiles, turn, wave, x, lds); break;
+      case 6: more = wide_tile<BF, 6>(p, row_tiles, turn, wave, x, lds); break;
+      case 5: more = wide_tile<BF, 5>(p, row_tiles, turn, wave, x, lds); break;
+      case 4: more = wide_tile<BF, 4>(p, row_tiles, turn, wave, x, lds); break;
+      case 3: more = wide_tile<BF, 3>(p, row_tiles, turn, wave, x, lds); break;
+      case 2: more = wide_tile<BF, 2>(p, row_tiles, turn, wave, x, lds); break;
+      default: more = wide_tile<BF, 1>(p, row_tiles, turn, wave, x, lds); break;
+    }
   }
 }
 
@@ -400,7 +452,7 @@ hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
   p.g = a;
   p.errword = static_cast<uint32_t *>(ws);
   p.kb = (a.L.in_features + 127) / 128;
-  p.y8 = a.y_row % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
+  p.y16 = a.y_row % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
   const bool wide = a.rows >= (a.offsets ? 32LL * a.L.n_experts : 128);
   if (!wide) {
     p.tile_rows = 16;
@@ -425,7 +477,8 @@ hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
     }
   }
   p.row_tiles = a.offsets ? a.rows / p.tile_rows + min(a.rows, a.L.n_experts) : (a.rows + p.tile_rows - 1) / p.tile_rows;
-  const long long grid = (long long)p.row_tiles * p.col_tiles;
+  // one workgroup a CU (its shared memory holds one), whole eights of them for the XCDs
+  const long long grid = min((long long)p.row_tiles * p.col_tiles, (long long)256) + 7 & ~7LL;
   const void *kernel = a.bf16 ? reinterpret_cast<const void *>(wide_kernel<true>) : reinterpret_cast<const void *>(wide_kernel<false>);
   const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WideLds));
   if (e != hipSuccess) return e;

@@ -5,6 +5,8 @@
 // one v_mfma_f32_16x16x128_f8f6f4 forms a 16 x 16 tile of a block's products from zero, and a
 // vector fma adds it times its scales.  Matrix rows are the tile's rows and tokens its columns, so
 // a lane's four sums belong to one token and take one factor.
+#include <cstdlib>
+
 #include "f8_device.h"
 
 namespace trellis {
@@ -20,7 +22,7 @@ struct GemmArgs {
   int col_tiles;  // tiles over out_features
   int row_tiles;  // tiles over rows, at most
   int tile_rows;  // rows of a tile, at most
-  int y16;        // every row of y begins at a multiple of 16 bytes
+  int y8, y16;    // every row of y begins at a multiple of 8, 16 bytes
 };
 
 // Which rows a tile has: of expert e, rows [row, end).  e < 0: none.
@@ -41,8 +43,8 @@ __device__ __forceinline__ Cut cut_rows(int n, int T) {
 }
 
 // Tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert after expert.
-// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  Called by whole waves;
-// each lane looks at every 64th expert.  The list ends at the first pair of offsets that is out of
+// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  Called by whole waves.
+// The list ends at the first pair of offsets that is out of
 // order or out of range.
 template <int U>
 __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool report) {
@@ -54,29 +56,43 @@ __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool rep
   const int lane = opaque_tid() & 63, E = p.g.L.n_experts;
   int passed = 0;
   bool wrong = ldg(p.g.offsets) != 0;
-  for (int e0 = 0; e0 < E && !wrong; e0 += 64) {
-    const int e = e0 + lane;
-    int a = 0, b = 0;
-    if (e < E) {
-      a = ldg(p.g.offsets + e);
-      b = ldg(p.g.offsets + e + 1);
+  for (int e0 = 0; e0 < E && !wrong; e0 += 256) {
+    // four neighbouring experts a lane, their tiles summed, then over the lanes
+    int o[5], sum = 0;
+    Cut c[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) o[k] = ldg(p.g.offsets + min(e0 + 4 * lane + k, E));
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      bad |= o[k] < 0 || o[k + 1] < o[k] || o[k + 1] > p.g.rows;
+      c[k] = cut_rows<U>(bad ? 0 : o[k + 1] - o[k], p.tile_rows);
+      sum += c[k].tiles;
     }
-    const uint64_t bad = __ballot(a < 0 || b < a || b > p.g.rows);
-    const int good = bad ? __builtin_ctzll(bad) : 64;
-    const Cut c = cut_rows<U>(lane < good ? b - a : 0, p.tile_rows);
-    int s = c.tiles;
+    const uint64_t bads = __ballot(bad);
+    if (bads && lane > __builtin_ctzll(bads)) sum = 0;
+    int s = sum;
     for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(s, d, 64);
-      if (lane >= d) s += o;
+      const int t = __shfl_up(s, d, 64);
+      if (lane >= d) s += t;
     }
     const uint64_t has = __ballot(at < passed + s);
     if (has) {
       const int l = __builtin_ctzll(has);
-      const int row = a + (at - passed - (s - c.tiles)) * c.size;
-      return {e0 + l, __builtin_amdgcn_readlane(row, l), __builtin_amdgcn_readlane(min(b, row + c.size), l)};
+      int i = at - passed - (s - sum), e = e0 + 4 * lane, row = 0, end = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i >= 0 && i < c[k].tiles) {
+          row = o[k] + i * c[k].size;
+          end = min(o[k + 1], row + c[k].size);
+          e = e0 + 4 * lane + k;
+        }
+        i -= c[k].tiles;
+      }
+      return {__builtin_amdgcn_readlane(e, l), __builtin_amdgcn_readlane(row, l), __builtin_amdgcn_readlane(end, l)};
     }
     passed += __builtin_amdgcn_readlane(s, 63);
-    wrong = bad != 0;
+    wrong = bads != 0;
   }
   if (wrong && report && lane == 0) f8_error(p.errword);
   return {-1, passed, 0};
@@ -94,48 +110,218 @@ __device__ __forceinline__ int source_row(const GemmArgs &p, int row) {
   return src;
 }
 
-template <bool BF>
-__global__ __launch_bounds__(64) void simple_kernel(GemmArgs p) {
+// ---------------------------------------------------------------------------------------
+// Rows of 128 bytes through shared memory, in both kernels: a copy takes eight of them, 1 KB, past
+// the registers.  Read straight into the products' registers, neighbouring lanes would have
+// different rows and each take a turn of its own at the cache (one token over 17408 x 5120: 21 us).
+// A row's eight chunks of 16 bytes are permuted, chunk p of row r holding the row's chunk
+// p ^ (r & 7), so that the products' reads of one chunk from eight rows fall on eight places.
+// ---------------------------------------------------------------------------------------
+
+typedef __attribute__((address_space(1))) const void gbl_void;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 bytes a lane, copied to 16 * lane behind a place in shared memory, past the registers.
+__device__ __forceinline__ void copy16(const void *from, void *to) {
+  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 16, 0, 0);
+}
+__device__ __forceinline__ void copy4(const void *from, void *to) {
+  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 4, 0, 0);
+}
+
+// Lane l of a copy has row l / 8 of its eight; its chunk of block b.  Chunks behind in_features
+// repeat the row's last one; the products take zeros of the matrix there.
+__device__ __forceinline__ uint32_t copy_chunk(int lane, int b, int K) {
+  return (uint32_t)min(8 * b + ((lane & 7) ^ (lane >> 3)), K / 16 - 1);
+}
+
+__device__ __forceinline__ intx8 operand(const char *row, int lane) {
+  const int g = lane >> 4, r = lane & 7;
+  const u32x4 a = *reinterpret_cast<const u32x4 *>(row + ((g ^ r) << 4));
+  const u32x4 b = *reinterpret_cast<const u32x4 *>(row + (((g + 4) ^ r) << 4));
+  return intx8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+// The chunks behind `rest` channels of a block become zero.
+__device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
+  const int g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = 16 * (g + 4 * (j >> 2)) < rest ? w[j] : 0;
+}
+
+// ---------------------------------------------------------------------------------------
+// Few rows: the matrix streams through once.
+// ---------------------------------------------------------------------------------------
+
+// A wave's place for one block: 16 NT matrix rows, 16 MF tokens (or 8), their scales.
+template <int MF, int NT, bool Few>
+struct NarrowStage {
+  static constexpr int xcopies = Few ? 1 : 2 * MF, copies = 2 * NT + xcopies + 2;
+  alignas(16) char w[NT * 2048], x[xcopies * 1024];
+  float sx[64], sw[64];
+};
+
+// A workgroup takes 16 NT matrix rows by 16 MF tokens (Few: up to 8); its waves take the blocks in
+// turn, and their sums are added in the order of the waves.  `reps` tiles of matrix rows follow each
+// other.  A wave copies into D places of its own, D - 1 blocks ahead over all its tiles, and needs no
+// other wave for that; behind the last it copies that one again, so that the number of copies under
+// way is a constant.
+template <bool BF, int MF, int NT, bool Few, int D>
+__global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
+  using Stage = NarrowStage<MF, NT, Few>;
+  extern __shared__ char raw[];
   const trellis_f8_linear &L = p.g.L;
-  const int lane = threadIdx.x, i = lane & 15, g = lane >> 4;
-  const int rt = blockIdx.x / p.col_tiles, ct = blockIdx.x - rt * p.col_tiles;
-  const RowTile t = find_tile<16>(p, rt, rt == p.row_tiles - 1 && ct == 0);
+  const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128, kb = p.kb;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int i = lane & 15;
+  Stage *ring = reinterpret_cast<Stage *>(raw) + wave * D;
+  floatx4 *sums = reinterpret_cast<floatx4 *>(raw + waves * D * sizeof(Stage));  // [waves][MF][NT][64]
+  const int groups = (p.col_tiles + reps - 1) / reps;
+  const int rt = blockIdx.x / groups, c0 = (blockIdx.x - rt * groups) * reps, c1 = min(c0 + reps, p.col_tiles);
+  const RowTile t = find_tile<Few ? 8 : 16>(p, rt, rt == p.row_tiles - 1 && c0 == 0);
   if (t.e < 0) return;
-  const int K = L.in_features, N = L.out_features;
-  const int row = t.row + i, o = ct * 16 + i;
-  const bool live = row < t.end;
-  const int src = live ? source_row(p, row) : -1;
-  const uint8_t *x = p.g.q + (int64_t)max(src, 0) * p.g.q_row;
-  const float *sx = p.g.s + (int64_t)max(src, 0) * p.g.s_row;
-  const uint8_t *w = L.w + ((int64_t)t.e * N + min(o, N - 1)) * K;
-  const float *sw = L.scale + ((int64_t)t.e * ((N + 127) / 128) + ct * 16 / 128) * p.kb;
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b = 0; b < p.kb; ++b) {
-    intx8 a8, b8;
+  uint32_t xat[Stage::xcopies];  // of the lane's tokens behind q, in 16 bytes
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = b * 128 + h * 64 + 16 * g;
-      u32x4 wv = ldg(reinterpret_cast<const u32x4 *>(w + min(k, K - 16)));
-      u32x4 xv = ldg(reinterpret_cast<const u32x4 *>(x + min(k, K - 16)));
-      if (k >= K) wv = xv = u32x4{0, 0, 0, 0};
+  for (int j = 0; j < Stage::xcopies; ++j)
+    xat[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + 8 * j + (lane >> 3), t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
+  const float *sx = p.g.s + (int64_t)max(source_row(p, min(t.row + min(lane, 16 * MF - 1), t.end - 1)), 0) * p.g.s_row;
+
+  // what is copied next
+  int ct = c0, cb = wave, slot = 0;
+  const char *w;
+  const float *sw;
+  uint32_t wat[2 * NT];  // of the lane's matrix rows behind w, in 16 bytes
+  auto aim = [&]() {
+    const int n0 = ct * 16 * NT;
+    w = reinterpret_cast<const char *>(L.w) + ((int64_t)t.e * N + n0) * K;
+    sw = L.scale + ((int64_t)t.e * nb + (n0 >> 7)) * kb;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a8[4 * h + j] = (int)wv[j];
-        b8[4 * h + j] = (int)xv[j];
+    for (int j = 0; j < 2 * NT; ++j) wat[j] = (uint32_t)min(8 * j + (lane >> 3), N - 1 - n0) * (uint32_t)(K >> 4);
+  };
+  auto copy = [&]() {
+    const int b = min(cb, kb - 1);
+    const uint32_t u = copy_chunk(lane, b, K);
+    Stage &o = ring[slot];
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) copy16(w + ((uint64_t)(wat[j] + u) << 4), o.w + 1024 * j);
+#pragma unroll
+    for (int j = 0; j < Stage::xcopies; ++j) copy16(p.g.q + ((uint64_t)(xat[j] + u) << 4), o.x + 1024 * j);
+    copy4(sx + b, o.sx);
+    copy4(sw + b, o.sw);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    cb += waves;
+    if (cb >= kb && ct + 1 < c1) {
+      ++ct;
+      cb = wave;
+      aim();
+    }
+  };
+  aim();
+#pragma unroll
+  for (int d = 0; d + 1 < D; ++d) copy();
+  int now = 0;
+  for (int c = c0; c < c1; ++c) {
+    const int n0 = c * 16 * NT;
+    floatx4 acc[MF][NT];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma clang loop unroll(disable)
+    for (int b = wave; b < kb; b += waves) {
+      copy();
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * Stage::copies) : "memory");
+      const Stage &o = ring[now];
+      now = now + 1 == D ? 0 : now + 1;
+      intx8 a[NT], x[MF];
+      float f[MF];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) a[n] = operand(o.w + (16 * n + i) * 128, lane);
+#pragma unroll
+      for (int m = 0; m < MF; ++m) x[m] = operand(o.x + (Few ? i & 7 : 16 * m + i) * 128, lane);
+#pragma unroll
+      for (int m = 0; m < MF; ++m) f[m] = o.sx[16 * m + i] * o.sw[0];
+      if (K - 128 * b < 128)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) clear_behind(a[n], lane, K - 128 * b);
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+          const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[n], x[m], zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d[j], f[m], acc[m][n][j]);
+        }
+      asm volatile("" ::: "memory");  // (the place's reads are done before its next copies)
+    }
+    __builtin_amdgcn_s_barrier();  // (the sums of the tile before have been read)
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sums[((wave * MF + m) * NT + n) * 64 + lane] = acc[m][n];
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // a thread has four columns of one token
+    for (int at = threadIdx.x; at < MF * NT * 64; at += blockDim.x) {
+      floatx4 v = sums[at];
+      for (int u = 1; u < waves; ++u) {
+        const floatx4 o = sums[u * MF * NT * 64 + at];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += o[j];
+      }
+      const int l = at & 63, n = (at >> 6) % NT, m = (at >> 6) / NT;
+      const int row = t.row + 16 * m + (l & 15), col = n0 + 16 * n + 4 * (l >> 4);
+      if (row >= t.end) continue;
+      const bool zero = p.g.order && source_row(p, row) < 0;
+      uint16_t *y = p.g.y + (int64_t)row * p.g.y_row + col;
+      uint16_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = f8_narrow<BF>(zero ? 0.f : v[j]);
+      if (p.y8 && col + 4 <= N) {
+        stg(reinterpret_cast<u32x2 *>(y), u32x2{r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16});
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < N) stg(y + j, r[j]);
       }
     }
-    const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-    const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, zero, 0, 0, 0, 0, 0, 0);
-    const float f = ldg(sx + b) * ldg(sw + b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = fmaf(d[j], f, acc[j]);
   }
-  if (!live) return;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = ct * 16 + 4 * g + j;
-    if (c < N) stg(p.g.y + (int64_t)row * p.g.y_row + c, f8_narrow<BF>(src < 0 ? 0.f : acc[j]));
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (no copy is under way when the shared memory goes to another workgroup)
+}
+
+template <bool BF, int MF, int NT, bool Few, int D>
+hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
+  const trellis_f8_linear &L = p.g.L;
+  p.tile_rows = Few ? 8 : 16 * MF;
+  p.col_tiles = (L.out_features + 16 * NT - 1) / (16 * NT);
+  p.row_tiles = p.g.offsets ? p.g.rows / p.tile_rows + min(p.g.rows, L.n_experts) : (p.g.rows + p.tile_rows - 1) / p.tile_rows;
+  const long long tiles = (long long)p.row_tiles * p.col_tiles;
+  const int reps = tiles > 4096 ? 4 : 1;
+  const int each = D * (int)sizeof(NarrowStage<MF, NT, Few>) + MF * NT * 1024;
+  int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
+  if (waves > p.kb) waves = p.kb;
+  const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps);
+  const int lds = waves * each;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(narrow_kernel<BF, MF, NT, Few, D>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
   }
+  narrow_kernel<BF, MF, NT, Few, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps);
+  return hipGetLastError();
+}
+
+// `each`: rows of a matrix, about.
+template <bool BF>
+hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
+  // Two tiles of matrix rows a workgroup share what is read of the tokens; where that is little, and
+  // the tiles are few, one tile each.
+  const bool one = each <= 16 && (long long)(p.g.rows + 15) / 16 * ((p.g.L.out_features + 31) / 32) < 1024;
+  if (each <= 8) return one ? launch_narrow<BF, 1, 1, true, 3>(p, stream) : launch_narrow<BF, 1, 2, true, 3>(p, stream);
+  if (each <= 16) return one ? launch_narrow<BF, 1, 1, false, 3>(p, stream) : launch_narrow<BF, 1, 2, false, 3>(p, stream);
+  if (each <= 32) return launch_narrow<BF, 2, 2, false, 3>(p, stream);
+  if (each <= 48) return launch_narrow<BF, 3, 2, false, 2>(p, stream);
+  return launch_narrow<BF, 4, 2, false, 2>(p, stream);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -148,17 +334,6 @@ struct WideLds {
   alignas(16) char w[2][kWideOut * 128], x[2][kWideRows * 128];  // a block of 128 inputs, two in turn
   alignas(16) float sx[2][kWideRows], sw[2][64];
 };
-
-typedef __attribute__((address_space(1))) const void gbl_void;
-typedef __attribute__((address_space(3))) void lds_void;
-
-// 16 bytes a lane, copied to 16 * lane behind a place in shared memory, past the registers.
-__device__ __forceinline__ void copy16(const void *from, void *to) {
-  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 16, 0, 0);
-}
-__device__ __forceinline__ void copy4(const void *from, void *to) {
-  __builtin_amdgcn_global_load_lds((gbl_void *)from, (lds_void *)to, 4, 0, 0);
-}
 
 // Where a lane's copies come from.  A row in shared memory is 128 bytes, eight chunks of 16; chunk
 // p of row r holds the row's chunk p ^ (r & 7), so that the products' reads of one chunk from
@@ -207,19 +382,6 @@ __device__ __forceinline__ void wide_meet() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
   __builtin_amdgcn_sched_barrier(0);
-}
-
-__device__ __forceinline__ intx8 operand(const char *row, int lane) {
-  const int g = lane >> 4, r = lane & 7;
-  const u32x4 a = *reinterpret_cast<const u32x4 *>(row + ((g ^ r) << 4));
-  const u32x4 b = *reinterpret_cast<const u32x4 *>(row + (((g + 4) ^ r) << 4));
-  return intx8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-// The chunks behind `rest` channels of a block become zero.
-__device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
-  const int g = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 16 * (g + 4 * (j >> 2)) < rest ? w[j] : 0;
 }
 
 // A wave's 64 matrix rows by 16 MF tokens over all blocks.  Its tile m takes tokens 32 m + 16 wm ..
@@ -452,17 +614,13 @@ hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
   p.g = a;
   p.errword = static_cast<uint32_t *>(ws);
   p.kb = (a.L.in_features + 127) / 128;
+  p.y8 = a.y_row % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
   p.y16 = a.y_row % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-  const bool wide = a.rows >= (a.offsets ? 32LL * a.L.n_experts : 128);
-  if (!wide) {
-    p.tile_rows = 16;
-    p.col_tiles = (a.L.out_features + 15) / 16;
-    p.row_tiles = a.offsets ? a.rows / 16 + min(a.rows, a.L.n_experts) : (a.rows + 15) / 16;
-    const long long grid = (long long)p.row_tiles * p.col_tiles;
-    if (a.bf16) simple_kernel<true><<<(unsigned)grid, 64, 0, stream>>>(p);
-    else simple_kernel<false><<<(unsigned)grid, 64, 0, stream>>>(p);
-    return hipGetLastError();
-  }
+  // rows a matrix
+  const long long each = a.offsets ? (a.rows + min(a.rows, a.L.n_experts) - 1) / min(a.rows, a.L.n_experts) : a.rows;
+  long long most = a.offsets ? 32 : 128;
+  if (const char *v = getenv("F8_MOST")) most = atoi(v);
+  if (each < most) return a.bf16 ? launch_few<true>(p, each, stream) : launch_few<false>(p, each, stream);
   p.col_tiles = (a.L.out_features + kWideOut - 1) / kWideOut;
   p.tile_rows = kWideRows;
   if (!a.offsets) {

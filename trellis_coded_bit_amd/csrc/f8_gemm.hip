@@ -5,7 +5,7 @@
 // one v_mfma_f32_16x16x128_f8f6f4 forms a 16 x 16 tile of a block's products from zero, and a
 // vector fma adds it times its scales.  Matrix rows are the tile's rows and tokens its columns, so
 // a lane's four sums belong to one token and take one factor.
-#include <cstdlib>
+#include <cmath>
 
 #include "f8_device.h"
 
@@ -23,6 +23,9 @@ struct GemmArgs {
   int row_tiles;  // tiles over rows, at most
   int tile_rows;  // rows of a tile, at most
   int y8, y16;    // every row of y begins at a multiple of 8, 16 bytes
+  int splits;     // of a tile's blocks among workgroups (many rows of one matrix)
+  float *parts;   // splits > 1: their sums, [splits][rows][part_row]
+  int64_t part_row;
 };
 
 // Which rows a tile has: of expert e, rows [row, end).  e < 0: none.
@@ -393,10 +396,10 @@ constexpr int kBehind = 3;  // products between one and the use of its results (
 
 template <int MF>
 __device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_w, const WideFrom &f, int wave, WideLds &lds,
-                                            floatx4 (&acc)[MF][4]) {
+                                            int kb, int rest, floatx4 (&acc)[MF][4]) {
   const int lane = opaque_tid() & 63;
   using Part = WidePart<MF>;
-  const int i = lane & 15, wm = wave & 1, wn = wave >> 1, kb = p.kb, rest = p.g.L.in_features & 127;
+  const int i = lane & 15, wm = wave & 1, wn = wave >> 1;
   const char *wp = lds.w[0] + (64 * wn + i) * 128, *xp = lds.x[0] + (16 * wm + i) * 128;
   constexpr int kBuf = kWideOut * 128;
 #pragma unroll
@@ -465,10 +468,10 @@ __device__ __forceinline__ void wide_blocks(const GemmArgs &p, const char *from_
     for (int j = 0; j < 4; ++j) acc[MF - 1][n + 4 - kBehind][j] = fmaf(d[n][j], s[0], acc[MF - 1][n + 4 - kBehind][j]);
 }
 
-// A tile to be: its rows, its first matrix row, and where its copies come from.
+// A tile to be: its rows, its first matrix row, its blocks, and where its copies come from.
 struct WideTile {
   RowTile t;
-  int n0;
+  int n0, split, kb, rest;  // rest: channels of a last, partial block
   const char *w;
   WideFrom f;
 };
@@ -480,7 +483,10 @@ __device__ __forceinline__ void wide_begin(const GemmArgs &p, WideTile &x, int w
   const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128;
   x.w = reinterpret_cast<const char *>(L.w) + ((int64_t)x.t.e * N + x.n0) * K;
   WideFrom &f = x.f;
-  f.chunk = (lane & 7) ^ (lane >> 3);
+  const int each = (p.kb + p.splits - 1) / p.splits, b0 = x.split * each;
+  x.kb = min(each, p.kb - b0);
+  x.rest = b0 + x.kb == p.kb ? K & 127 : 0;
+  f.chunk = 8 * b0 + ((lane & 7) ^ (lane >> 3));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = 64 * j + 8 * wave + (lane >> 3);
@@ -489,8 +495,9 @@ __device__ __forceinline__ void wide_begin(const GemmArgs &p, WideTile &x, int w
   }
   if (wave < 4) f.s = p.g.s + (int64_t)max(source_row(p, min(x.t.row + 64 * wave + lane, x.t.end - 1)), 0) * p.g.s_row;
   else f.s = L.scale + ((int64_t)x.t.e * nb + min((x.n0 >> 7) + (lane & 1), nb - 1)) * p.kb;
+  f.s += b0;
   const int copies = (x.t.end - x.t.row + 63) >> 6;
-  for (int b = 0; b < min(p.kb, 2); ++b) {
+  for (int b = 0; b < min(x.kb, 2); ++b) {
     const uint32_t u = (uint32_t)min(8 * b + f.chunk, K / 16 - 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) copy16(x.w + ((uint64_t)(f.w[j] + u) << 4), lds.w[b] + (64 * j + 8 * wave) * 128);
@@ -505,9 +512,22 @@ __device__ __forceinline__ void wide_begin(const GemmArgs &p, WideTile &x, int w
 // of one token in each of its tiles; two tiles' are exchanged between neighbouring rows of lanes
 // so that it has eight of one.
 template <bool BF, int MF>
-__device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, int n0, int wave, const floatx4 (&acc)[MF][4]) {
+__device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, int n0, int split, int wave, const floatx4 (&acc)[MF][4]) {
   const int lane = opaque_tid() & 63;
   const int N = p.g.L.out_features, wm = wave & 1, wn = wave >> 1, g = lane >> 4;
+  if (p.splits > 1) {
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      const int row = t.row + 32 * m + 16 * wm + (lane & 15);
+      float *to = p.parts + ((int64_t)split * p.g.rows + row) * p.part_row;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int c = n0 + 64 * wn + 16 * n + 4 * g;
+        if (row < t.end && c < N) stg(reinterpret_cast<floatx4 *>(to + c), acc[m][n]);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
     const int row = t.row + 32 * m + 16 * wm + (lane & 15);
@@ -546,11 +566,13 @@ __device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, 
 
 // Tiles in an order that keeps what runs at a time on one XCD (every eighth workgroup) close
 // together: eight row tiles by the column tiles, row tiles first.  Each XCD has a run of the list.
-__device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int turn, int &rt, int &ct) {
-  const int total = row_tiles * p.col_tiles, per = total >> 3, rest = total & 7;
+__device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int turn, int &rt, int &ct, int &split) {
+  const int tiles = row_tiles * p.col_tiles, total = tiles * p.splits, per = total >> 3, rest = total & 7;
   const int x = blockIdx.x & 7, i = (blockIdx.x >> 3) + turn * ((int)gridDim.x >> 3);
   if (i >= per + (x < rest)) return false;
-  const int at = x * per + min(x, rest) + i;
+  int at = x * per + min(x, rest) + i;
+  split = at / tiles;
+  at -= split * tiles;
   const int band = at / (8 * p.col_tiles), in = at - band * 8 * p.col_tiles;
   const int high = min(8, row_tiles - 8 * band);
   ct = in / high;
@@ -558,21 +580,25 @@ __device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int tu
   return true;
 }
 
+// Looks up what a workgroup does in its turn, and starts its first copies.
+__device__ __forceinline__ bool wide_next(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
+  int rt, ct;
+  if (!tile_of(p, row_tiles, turn, rt, ct, x.split)) return false;
+  x.t = find_tile<32>(p, rt, false);
+  x.n0 = ct * kWideOut;
+  wide_begin(p, x, wave, lds);
+  return true;
+}
+
 // One tile's products; the next tile's first copies are under way while this one is stored.
 template <bool BF, int MF>
 __device__ __forceinline__ bool wide_tile(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
   floatx4 acc[MF][4];
-  wide_blocks<MF>(p, x.w, x.f, wave, lds, acc);
+  wide_blocks<MF>(p, x.w, x.f, wave, lds, x.kb, x.rest, acc);
   const RowTile t = x.t;
-  const int n0 = x.n0;
-  int rt, ct;
-  const bool more = tile_of(p, row_tiles, turn, rt, ct);
-  if (more) {
-    x.t = find_tile<32>(p, rt, false);
-    x.n0 = ct * kWideOut;
-    wide_begin(p, x, wave, lds);
-  }
-  wide_store<BF, MF>(p, t, n0, wave, acc);
+  const int n0 = x.n0, split = x.split;
+  const bool more = wide_next(p, row_tiles, turn, wave, x, lds);
+  wide_store<BF, MF>(p, t, n0, split, wave, acc);
   return more;
 }
 
@@ -584,12 +610,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row_tiles = find_tile<32>(p, 0x7FFFFFFF, blockIdx.x == 0).row;
   WideTile x;
-  int rt, ct;
-  if (!tile_of(p, row_tiles, 0, rt, ct)) return;
-  x.t = find_tile<32>(p, rt, false);
-  x.n0 = ct * kWideOut;
-  wide_begin(p, x, wave, lds);
-  bool more = true;
+  bool more = wide_next(p, row_tiles, 0, wave, x, lds);
   for (int turn = 1; more; ++turn) {
     wide_meet<0>();
     switch ((x.t.end - x.t.row + 31) >> 5) {
@@ -605,9 +626,74 @@ __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   }
 }
 
+// The splits' sums added in their order, rounded and stored: four columns a thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
+  const int N = p.g.L.out_features, quads = (N + 3) >> 2;
+  const int64_t split = p.g.rows * p.part_row;
+  for (uint32_t at = blockIdx.x * 256 + threadIdx.x; at < (uint32_t)p.g.rows * (uint32_t)quads; at += gridDim.x * 256) {
+    const int row = (int)(at / (uint32_t)quads), c = 4 * (int)(at - (uint32_t)row * (uint32_t)quads);
+    const float *from = p.parts + row * p.part_row + c;
+    floatx4 v = ldg(reinterpret_cast<const floatx4 *>(from));
+    for (int s = 1; s < p.splits; ++s) {
+      const floatx4 o = ldg(reinterpret_cast<const floatx4 *>(from + s * split));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += o[j];
+    }
+    uint16_t *y = p.g.y + (int64_t)row * p.g.y_row + c, r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = f8_narrow<BF>(v[j]);
+    if (p.y8 && c + 4 <= N) {
+      stg(reinterpret_cast<u32x2 *>(y), u32x2{r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16});
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < N) stg(y + j, r[j]);
+    }
+  }
+}
+
+// How a call is divided.  Times in microseconds, as measured: the narrow kernel takes 0.86 ns for a
+// block of 64 tokens by 32 matrix rows over the whole card; a wide workgroup 0.45 + 0.156 a block for
+// every 32 of its tokens, and 3 a tile; a split's sums are written and read at 5 TB/s by one launch
+// more.
+struct Plan {
+  bool narrow;
+  int tile_rows, splits;
+};
+Plan plan(const trellis_f8_linear &L, int rows, bool grouped) {
+  const long long kb = (L.in_features + 127) / 128, N = L.out_features, col_tiles = (N + kWideOut - 1) / kWideOut;
+  const long long matrices = grouped ? min(rows, L.n_experts) : 1;
+  const double each = (double)rows / matrices;
+  Plan best{true, 0, 1};
+  if (each <= 32) return best;
+  double least = 4 + 0.86e-3 * (matrices * ceil(each / 64) * ((N + 31) / 32)) * kb;
+  for (int mf = 8; mf >= 2; --mf) {
+    const double tiles = matrices * ceil(each / (32 * mf)) * col_tiles, block = 0.45 + 0.156 * mf;
+    for (int splits = 1; splits <= (grouped ? 1 : 16) && splits * 4 <= max(kb, 4LL); ++splits) {
+      const long long part = (kb + splits - 1) / splits;
+      if ((kb + part - 1) / part != splits) continue;  // (each split has blocks)
+      const double time = ceil(tiles * splits / 256) * (part * block + 3) + 1 +
+                          (splits > 1 ? 2 + splits * (double)rows * N * 8 / 5e6 : 0);
+      if (time < least) {
+        least = time;
+        best = {false, 32 * mf, splits};
+      }
+      if (tiles * splits >= 256) break;
+    }
+    if (grouped) break;  // (experts' rows are cut evenly into as few tiles as they take)
+  }
+  return best;
+}
+
+int64_t part_row(int N) { return (N + 3) & ~3; }
+
 }  // namespace
 
-size_t f8_gemm_workspace_bytes(const trellis_f8_linear &L, int rows, bool grouped) { return kWsReserved; }
+size_t f8_gemm_workspace_bytes(const trellis_f8_linear &L, int rows, bool grouped) {
+  const Plan d = rows > 0 ? plan(L, rows, grouped) : Plan{true, 0, 1};
+  return kWsReserved + (d.splits > 1 ? (size_t)d.splits * rows * part_row(L.out_features) * 4 : 0);
+}
 
 hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
   GemmArgs p{};
@@ -616,32 +702,30 @@ hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream) {
   p.kb = (a.L.in_features + 127) / 128;
   p.y8 = a.y_row % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % 8 == 0;
   p.y16 = a.y_row % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-  // rows a matrix
-  const long long each = a.offsets ? (a.rows + min(a.rows, a.L.n_experts) - 1) / min(a.rows, a.L.n_experts) : a.rows;
-  long long most = a.offsets ? 32 : 128;
-  if (const char *v = getenv("F8_MOST")) most = atoi(v);
-  if (each < most) return a.bf16 ? launch_few<true>(p, each, stream) : launch_few<false>(p, each, stream);
-  p.col_tiles = (a.L.out_features + kWideOut - 1) / kWideOut;
-  p.tile_rows = kWideRows;
-  if (!a.offsets) {
-    long long best = -1;
-    for (int mf = 8; mf >= 4; --mf) {  // rounds of 256 workgroups, each about as long as its rows
-      const long long tiles = (long long)((a.rows + 32 * mf - 1) / (32 * mf)) * p.col_tiles;
-      const long long cost = (tiles + 255) / 256 * (mf + 1);
-      if (best < 0 || cost < best) {
-        best = cost;
-        p.tile_rows = 32 * mf;
-      }
-    }
+  const Plan d = plan(a.L, a.rows, a.offsets != nullptr);
+  if (d.narrow) {
+    const long long matrices = a.offsets ? min(a.rows, a.L.n_experts) : 1, each = (a.rows + matrices - 1) / matrices;
+    return a.bf16 ? launch_few<true>(p, each, stream) : launch_few<false>(p, each, stream);
   }
+  p.col_tiles = (a.L.out_features + kWideOut - 1) / kWideOut;
+  p.tile_rows = d.tile_rows;
+  p.splits = d.splits;
+  p.part_row = part_row(a.L.out_features);
+  p.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + kWsReserved);
   p.row_tiles = a.offsets ? a.rows / p.tile_rows + min(a.rows, a.L.n_experts) : (a.rows + p.tile_rows - 1) / p.tile_rows;
   // one workgroup a CU (its shared memory holds one), whole eights of them for the XCDs
-  const long long grid = min((long long)p.row_tiles * p.col_tiles, (long long)256) + 7 & ~7LL;
+  const long long units = (long long)p.row_tiles * p.col_tiles * p.splits, grid = (min(units, 256LL) + 7) & ~7LL;
   const void *kernel = a.bf16 ? reinterpret_cast<const void *>(wide_kernel<true>) : reinterpret_cast<const void *>(wide_kernel<false>);
-  const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WideLds));
+  hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(WideLds));
   if (e != hipSuccess) return e;
   if (a.bf16) wide_kernel<true><<<(unsigned)grid, kWideThreads, sizeof(WideLds), stream>>>(p);
   else wide_kernel<false><<<(unsigned)grid, kWideThreads, sizeof(WideLds), stream>>>(p);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const long long quads = (long long)a.rows * ((a.L.out_features + 3) / 4);
+  const unsigned join = (unsigned)min((quads + 255) / 256, 1LL << 16);
+  if (a.bf16) join_kernel<true><<<join, 256, 0, stream>>>(p);
+  else join_kernel<false><<<join, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -908,27 +908,54 @@ def _f8_rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None, de
              cols: Optional[int] = None) -> int:
     """Checks a [rows, cols] tensor on the current device whose rows are contiguous (16-bit if
     no dtype is given); its row stride."""
+    # the usual case first: what is checked costs as much time as a short call's kernel
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.get_device() == torch._C._cuda_getDevice():
+        d = t.dtype
+        if d is dtype or (dtype is None and d in _F8_DTYPE):
+            rows, n = t.shape
+            row, last = t.stride()
+            if (last == 1 or n <= 1) and (cols is None or n == cols) and (device is None or t.device == device):
+                return row if rows > 1 else n
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype and (dtype is not None or t.dtype not in _F8_DTYPE):
         raise TypeError(f"{name} must be {'float16 or bfloat16' if dtype is None else dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
-    if t.device.index != torch._C._cuda_getDevice() or (device is not None and t.device != device):
+    if t.get_device() != torch._C._cuda_getDevice() or (device is not None and t.device != device):
         raise ValueError(f"{name} is on {t.device}: the current device is cuda:{torch._C._cuda_getDevice()}")
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [rows, {'n' if cols is None else cols}], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: each row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    raise ValueError(f"{name}: each row must be contiguous")
 
 
 def _f8_ws(ws: Optional[torch.Tensor], nb: int, device) -> torch.Tensor:
     return _kv4_ws(ws, nb, device, _stream())
 
 
+# A new tensor on the current device, for half of what torch.empty's argument parsing takes.
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new1(n: int, dtype: torch.dtype, device) -> torch.Tensor:
+    return _empty_cuda((n,), (1,), dtype) if _empty_cuda is not None else torch.empty((n,), dtype=dtype, device=device)
+
+
+def _new2(rows: int, n: int, dtype: torch.dtype, device) -> torch.Tensor:
+    return _empty_cuda((rows, n), (n, 1), dtype) if _empty_cuda is not None else torch.empty((rows, n), dtype=dtype, device=device)
+
+
+def _out1(t: Optional[torch.Tensor], n: int, device, dtype: torch.dtype, name: str) -> torch.Tensor:
+    return _new1(n, dtype, device) if t is None else _out(t, (n,), device, dtype, name)
+
+
+def _out2(t: Optional[torch.Tensor], rows: int, n: int, device, dtype: torch.dtype, name: str = "out") -> torch.Tensor:
+    """_out for [rows, n] on the current device."""
+    return _new2(rows, n, dtype, device) if t is None else _out(t, (rows, n), device, dtype, name)
+
+
 def _f8_out(q, scale, rows: int, n: int, device):
-    return (_out(q, (rows, n), device, _E4M3, "q"), _out(scale, (rows, _f8_blocks(n)), device, torch.float32, "scale"))
+    return (_out2(q, rows, n, device, _E4M3, "q"), _out2(scale, rows, (n + 127) // 128, device, torch.float32, "scale"))
 
 
 def trellis_f8_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, residual: Optional[torch.Tensor] = None,
@@ -942,25 +969,30 @@ def trellis_f8_norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, 
     only one (q and scale are None, y is made if not given) and takes their place: (y, h)."""
     x_row = _f8_rows(x, "x")
     rows, n = x.shape
-    dev = x.device
+    dev, dtype = x.device, x.dtype
+    r = g = None
     if residual is not None:
-        _req(residual, x.dtype, "residual", dev)
-        if tuple(residual.shape) != (rows, n):
+        _req(residual, dtype, "residual", dev)
+        if residual.shape != x.shape:
             raise ValueError(f"residual must be {(rows, n)}, got {tuple(residual.shape)}")
+        r = residual.data_ptr()
     if gamma is not None:
-        _req(gamma, x.dtype, "gamma", dev)
+        _req(gamma, dtype, "gamma", dev)
         if gamma.numel() != n:
             raise ValueError(f"gamma must have {n} elements")
+        g = gamma.data_ptr()
     if residual is not None or h is not None:
-        h = _out(h, (rows, n), dev, x.dtype, "h")
+        h = _out2(h, rows, n, dev, dtype, "h")
     if quantize:
         q, scale = _f8_out(q, scale, rows, n, dev)
     elif q is not None or scale is not None:
         raise ValueError("q and scale are not written with quantize=False")
     if y is not None or not quantize:
-        y = _out(y, (rows, n), dev, x.dtype, "y")
-    _check(lib().trellis_f8_norm(_F8_DTYPE[x.dtype], x.data_ptr(), x_row, _ptr(residual), _ptr(gamma), rows, n, eps, _ptr(h),
-                                 _ptr(q), _ptr(scale), _ptr(y), _stream()))
+        y = _out2(y, rows, n, dev, dtype, "y")
+    st = lib().trellis_f8_norm(_F8_DTYPE[dtype], x.data_ptr(), x_row, r, g, rows, n, eps, None if h is None else h.data_ptr(),
+                               _ptr(q), _ptr(scale), None if y is None else y.data_ptr(), _stream())
+    if st:
+        _check(st)
     return (q, scale, h) if quantize else (y, h)
 
 
@@ -970,16 +1002,19 @@ def trellis_f8_silu_mul(x: torch.Tensor, quantize: bool = True, q: Optional[torc
     codes with one f32 scale per 128 channels.  ``y``: optional 16-bit output; with
     ``quantize=False`` the only one, returned."""
     x_row = _f8_rows(x, "x")
-    rows, n = x.shape[0], x.shape[1] // 2
-    if x.shape[1] % 2:
-        raise ValueError(f"x must have an even number of columns, got {x.shape[1]}")
+    rows, n = x.shape
+    if n % 2:
+        raise ValueError(f"x must have an even number of columns, got {n}")
+    n //= 2
     if quantize:
         q, scale = _f8_out(q, scale, rows, n, x.device)
     elif q is not None or scale is not None:
         raise ValueError("q and scale are not written with quantize=False")
     if y is not None or not quantize:
-        y = _out(y, (rows, n), x.device, x.dtype, "y")
-    _check(lib().trellis_f8_silu_mul(_F8_DTYPE[x.dtype], x.data_ptr(), x_row, rows, n, _ptr(q), _ptr(scale), _ptr(y), _stream()))
+        y = _out2(y, rows, n, x.device, x.dtype, "y")
+    st = lib().trellis_f8_silu_mul(_F8_DTYPE[x.dtype], x.data_ptr(), x_row, rows, n, _ptr(q), _ptr(scale), _ptr(y), _stream())
+    if st:
+        _check(st)
     return (q, scale) if quantize else y
 
 
@@ -1035,7 +1070,7 @@ def _f8_product(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, rows: int
     if out is None:
         if dtype not in _F8_DTYPE:
             raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
-        out = torch.empty((rows, layer.out_features), dtype=dtype, device=layer.device)
+        out = _new2(rows, layer.out_features, dtype, layer.device)
     y_row = _f8_rows(out, "out", None, layer.device, layer.out_features)
     if out.shape[0] != rows:
         raise ValueError(f"out must have {rows} rows, got {out.shape[0]}")
@@ -1080,6 +1115,9 @@ def trellis_f8_moe_gemm(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, o
 
 
 def _moe_ids(t: torch.Tensor, name: str, device=None) -> Tuple[int, int]:
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.dtype is torch.int32 and t.is_contiguous()
+            and t.get_device() == torch._C._cuda_getDevice() and (device is None or t.device == device)):
+        return t.shape
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be [tokens, top]")
     _req(t, torch.int32, name, device)
@@ -1110,9 +1148,9 @@ def trellis_moe_sort(ids: torch.Tensor, n_experts: int, offsets: Optional[torch.
     tokens, top = _moe_ids(ids, "ids")
     i32, dev = torch.int32, ids.device
     nb = _moe_sort_bytes(tokens, top, n_experts)
-    offsets = _out(offsets, (n_experts + 1,), dev, i32, "offsets")
-    order = _out(order, (tokens * top,), dev, i32, "order")
-    inverse = _out(inverse, (tokens, top), dev, i32, "inverse")
+    offsets = _out1(offsets, n_experts + 1, dev, i32, "offsets")
+    order = _out1(order, tokens * top, dev, i32, "order")
+    inverse = _out2(inverse, tokens, top, dev, i32, "inverse")
     ws = _f8_ws(ws, nb, dev)
     _check(lib().trellis_moe_sort(ids.data_ptr(), tokens, top, n_experts, offsets.data_ptr(), order.data_ptr(),
                                   inverse.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
@@ -1129,7 +1167,7 @@ def trellis_moe_gather(x: torch.Tensor, order: torch.Tensor, per: int, out: Opti
     x_row, e = _f8_rows(x, "x", x.dtype), x.element_size()
     _kv4_int(order, "order", x.device)
     tokens, n = x.shape
-    out = _out(out, (order.numel(), n), x.device, x.dtype)
+    out = _out2(out, order.numel(), n, x.device, x.dtype)
     ws = _f8_ws(ws, _moe_rows_bytes(), x.device)
     _check(lib().trellis_moe_gather(x.data_ptr(), x_row * e, tokens, n * e, order.data_ptr(), order.numel(), per,
                                     out.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
@@ -1166,7 +1204,7 @@ def trellis_moe_combine(y: torch.Tensor, inverse: torch.Tensor, weights: Optiona
         _moe_rows(add, "add", inverse.device, y.dtype, tokens)
         if add.shape[1] != n:
             raise ValueError(f"add must be {(tokens, n)}, got {tuple(add.shape)}")
-    out = _out(out, (tokens, n), inverse.device, y.dtype)
+    out = _out2(out, tokens, n, inverse.device, y.dtype)
     ws = _f8_ws(ws, _moe_rows_bytes(), inverse.device)
     _check(lib().trellis_moe_combine(_F8_DTYPE[y.dtype], y.data_ptr(), y.shape[0], n, inverse.data_ptr(), _ptr(weights), tokens,
                                      top, _ptr(add), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
@@ -1186,8 +1224,8 @@ def trellis_moe_combine_grad(d_out: torch.Tensor, y: torch.Tensor, inverse: torc
     if d_out.shape[1] != n:
         raise ValueError(f"d_out must be {(tokens, n)}, got {tuple(d_out.shape)}")
     _moe_weights(weights, inverse)
-    out = _out(out, (rows, n), inverse.device, y.dtype)
-    d_weights = _out(d_weights, (tokens, top), inverse.device, torch.float32, "d_weights")
+    out = _out2(out, rows, n, inverse.device, y.dtype)
+    d_weights = _out2(d_weights, tokens, top, inverse.device, torch.float32, "d_weights")
     ws = _f8_ws(ws, _moe_rows_bytes(), inverse.device)
     _check(lib().trellis_moe_combine_grad(_F8_DTYPE[y.dtype], d_out.data_ptr(), y.data_ptr(), rows, n, inverse.data_ptr(),
                                           _ptr(weights), tokens, top, out.data_ptr(), d_weights.data_ptr(), ws.data_ptr(),

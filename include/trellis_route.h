@@ -37,7 +37,7 @@ size_t trellis_moe_rows_workspace_bytes(void);
  * order  : int32 out [tokens * top]: the entry at each position; -1 behind the last position.
  * inverse: int32 out [tokens][top]: each entry's position, -1 where its expert is not here.
  * 1 <= n_experts <= 2048, 1 <= top <= 1024, tokens * top <= 2^24.  No output may overlap ids.
- * One launch, two for many entries. */
+ * One launch, three for more than 65536 entries. */
 int trellis_moe_sort(const int32_t *ids, int tokens, int top, int n_experts, int32_t *offsets, int32_t *order,
                      int32_t *inverse, void *ws, size_t ws_bytes, void *stream);
 

@@ -1,8 +1,10 @@
 // Tokens sorted by expert and back (include/trellis_route.h).
 //
-// Sort: a counting sort that keeps the order of equal ids.  A workgroup takes 1024 entries, one a
+// Sort: a counting sort that keeps the order of equal ids.  A workgroup places 1024 entries, one a
 // thread.  An entry's position is: the entries of smaller ids (a scan of all counts), those of its
-// id in earlier workgroups' entries, in earlier waves, and in earlier lanes (ballots).
+// id in earlier workgroups' entries, in earlier waves, and in earlier lanes (ballots).  Up to 65536
+// entries every workgroup counts all of them itself, in one launch: 32 ids a thread cost less than
+// a launch more.  Above, two launches before count and scan.
 #include "f8_device.h"
 
 namespace trellis {
@@ -10,77 +12,98 @@ namespace trellis {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-// Entries up to which every workgroup counts all of them itself; above, a launch before counts.
 constexpr int kSortOne = 1 << 16;
 
-// The id as a key: what is not here counts as one more expert behind the others.
-__device__ __forceinline__ int sort_key(const int32_t *ids, long long i, int E, uint32_t *errword) {
-  const int id = ldg(ids + i);
+// An id, or -1 for an expert that is not here.
+__device__ __forceinline__ int sort_key(int id, int E, uint32_t *errword) {
   if (id >= 0 && id < E) return id;
   if (id != -1) f8_error(errword);
-  return E;
+  return -1;
 }
 
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t *ids, int n, int E, uint32_t *counts,
-                                                                  uint32_t *errword) {
-  extern __shared__ uint32_t c[];  // [E + 1]
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) c[e] = 0;
+// counts [E][groups]: of each id in each workgroup's entries.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t *ids, int n, int E, uint32_t *counts) {
+  extern __shared__ uint32_t c[];  // [E]
+  for (int e = threadIdx.x; e < E; e += kSortThreads) c[e] = 0;
   __syncthreads();
-  const long long i = (long long)blockIdx.x * kSortThreads + threadIdx.x;
-  if (i < n) atomicAdd(&c[sort_key(ids, i, E, errword)], 1u);
+  const int i = blockIdx.x * kSortThreads + threadIdx.x;
+  const int id = i < n ? ldg(ids + i) : -1;
+  if (id >= 0 && id < E) atomicAdd(&c[id], 1u);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) counts[(size_t)blockIdx.x * (E + 1) + e] = c[e];
+  for (int e = threadIdx.x; e < E; e += kSortThreads) counts[(size_t)e * gridDim.x + blockIdx.x] = c[e];
 }
 
-// counts: NULL, or [workgroups][E + 1] from the launch before.
+// A workgroup an id: its counts become the sums before them, its total goes to totals.
+__global__ __launch_bounds__(256) void sort_scan_kernel(uint32_t *counts, int groups, uint32_t *totals) {
+  __shared__ uint32_t sums[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t *row = counts + (size_t)blockIdx.x * groups, carry = 0;
+  for (int g0 = 0; g0 < groups; g0 += 256) {
+    const int g = g0 + threadIdx.x;
+    const uint32_t c = g < groups ? row[g] : 0;
+    uint32_t s = c;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = __shfl_up(s, d, 64);
+      if (lane >= d) s += o;
+    }
+    if (lane == 63) sums[wave] = s;
+    __syncthreads();
+    uint32_t base = carry;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) base += sums[w];
+      carry += sums[w];
+    }
+    if (g < groups) row[g] = base + s - c;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) totals[blockIdx.x] = carry;
+}
+
+// counts: NULL, or the sums and totals of the launches before.
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t *ids, int n, int E, int id_bits,
-                                                                  const uint32_t *counts, int32_t *offsets, int32_t *order,
-                                                                  int32_t *inverse, uint32_t *errword) {
+                                                                  const uint32_t *counts, const uint32_t *totals,
+                                                                  int32_t *offsets, int32_t *order, int32_t *inverse,
+                                                                  uint32_t *errword) {
   extern __shared__ uint32_t lds[];
-  uint32_t *before = lds;                // [E + 1] of the id in earlier workgroups' entries, then its first position here
-  uint32_t *all = before + E + 1;        // [E + 1] of the id at all
-  uint16_t *waves = reinterpret_cast<uint16_t *>(all + E + 1);  // [16][E + 1] of the id in this workgroup's waves
+  uint32_t *before = lds;       // [E] of the id in earlier workgroups' entries, then its first position here
+  uint32_t *after = before + E; // [E] of the id in the others
+  uint16_t *waves = reinterpret_cast<uint16_t *>(after + E);  // [16][E] of the id in this workgroup's waves
   __shared__ uint32_t sums[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= E; e += kSortThreads) before[e] = all[e] = 0;
-  for (int e = tid; e < kSortWaves * (E + 1); e += kSortThreads) waves[e] = 0;
-  __syncthreads();
   const int first = blockIdx.x * kSortThreads;
-  if (counts) {
-    for (int e = tid; e <= E; e += kSortThreads) {
-      uint32_t b = 0, t = 0;
-      for (int g = 0; g < (int)gridDim.x; ++g) {
-        const uint32_t c = ldg(counts + (size_t)g * (E + 1) + e);
-        t += c;
-        if (g < (int)blockIdx.x) b += c;
-      }
-      before[e] = b;
-      all[e] = t;
-    }
-  } else {
-    for (int i = tid; i < n; i += kSortThreads) {
-      const int key = sort_key(ids, i, E, errword);
-      atomicAdd(&all[key], 1u);
-      if (i < first) atomicAdd(&before[key], 1u);
+  const int i = first + tid;
+  const int key = i < n ? sort_key(ldg(ids + i), E, errword) : -1;
+  for (int e = tid; e < E; e += kSortThreads) {
+    before[e] = counts ? ldg(counts + (size_t)e * gridDim.x + blockIdx.x) : 0;
+    after[e] = counts ? ldg(totals + e) - before[e] : 0;
+  }
+  for (int e = tid; e < kSortWaves * E; e += kSortThreads) waves[e] = 0;
+  __syncthreads();
+  if (!counts) {
+    // (what is not here is not counted: its entries need no position)
+    for (int k0 = tid; k0 < n; k0 += 8 * kSortThreads) {
+      int id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) id[k] = k0 + k * kSortThreads < n ? ldg(ids + k0 + k * kSortThreads) : -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (id[k] >= 0 && id[k] < E) atomicAdd((k0 + k * kSortThreads < first ? before : after) + id[k], 1u);
     }
   }
   // the lanes of the wave with the same key
-  const int i = first + tid;
-  const bool live = i < n;
-  const int key = live ? sort_key(ids, i, E, errword) : E;
-  uint64_t same = __ballot(live);
+  uint64_t same = __ballot(key >= 0);
   for (int b = 0; b < id_bits; ++b) {
     const uint64_t set = __ballot((key >> b) & 1);
     same &= ((key >> b) & 1) ? set : ~set;
   }
   const int rank = __popcll(same & ((1ull << lane) - 1));
-  if (live && rank == 0) waves[wave * (E + 1) + key] = (uint16_t)__popcll(same);
+  if (key >= 0 && rank == 0) waves[wave * E + key] = (uint16_t)__popcll(same);
   __syncthreads();
   // exclusive scan of all counts over the ids, 1024 at a time
   uint32_t carry = 0;
-  for (int e0 = 0; e0 <= E; e0 += kSortThreads) {
+  for (int e0 = 0; e0 < E; e0 += kSortThreads) {
     const int e = e0 + tid;
-    const uint32_t c = e <= E ? all[e] : 0;
+    const uint32_t c = e < E ? before[e] + after[e] : 0;
     uint32_t s = c;
     for (int d = 1; d < 64; d <<= 1) {
       const uint32_t o = __shfl_up(s, d, 64);
@@ -93,64 +116,107 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
       if (w < wave) base += sums[w];
       carry += sums[w];
     }
-    if (e <= E) {
+    if (e < E) {
       const uint32_t start = base + s - c;
       before[e] += start;
       if (blockIdx.x == 0) offsets[e] = (int32_t)start;
     }
     __syncthreads();
   }
-  if (!live) return;
-  uint32_t pos = before[key] + rank;
-  for (int w = 0; w < wave; ++w) pos += waves[w * (E + 1) + key];
-  const bool here = key < E;
-  inverse[i] = here ? (int32_t)pos : -1;
-  order[pos] = here ? i : -1;
+  if (blockIdx.x == 0 && tid == 0) offsets[E] = (int32_t)carry;
+  if (i >= n) return;
+  if ((uint32_t)i >= carry) order[i] = -1;  // (positions behind the last are nobody's)
+  int32_t pos = -1;
+  if (key >= 0) {
+    uint32_t at = before[key] + rank;
+    for (int w = 0; w < wave; ++w) at += waves[w * E + key];
+    pos = (int32_t)at;
+    order[pos] = i;
+  }
+  inverse[i] = pos;
 }
 
-size_t sort_lds(int E) { return (size_t)(E + 1) * (4 + 4 + 2 * kSortWaves); }
+size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves); }
 
+// A workgroup a row, four words a thread under way.
 template <typename T>
 __global__ __launch_bounds__(256) void gather_kernel(const char *x, int64_t x_row, int tokens, int64_t row_words,
-                                                     const int32_t *order, int rows, int per, int parts, T *out,
-                                                     uint32_t *errword) {
-  const long long items = (long long)rows * parts;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int row = (int)(it / parts), part = (int)(it - (long long)row * parts);
+                                                     const int32_t *order, int rows, int per, T *out, uint32_t *errword) {
+  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
     const int entry = ldg(order + row);
     if (entry == -1) continue;
     if (entry < 0 || entry / per >= tokens) {
       if (threadIdx.x == 0) f8_error(errword);
       continue;
     }
-    const int64_t w = (int64_t)part * 256 + threadIdx.x;
-    if (w < row_words) stg(out + row * row_words + w, ldg(reinterpret_cast<const T *>(x + (entry / per) * x_row) + w));
+    const T *from = reinterpret_cast<const T *>(x + (entry / per) * x_row);
+    T *to = out + row * row_words;
+    for (int64_t w = threadIdx.x; w < row_words; w += 1024) {
+      T v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (w + 256 * k < row_words) v[k] = ldg(from + w + 256 * k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (w + 256 * k < row_words) stg(to + w + 256 * k, v[k]);
+    }
   }
 }
 
+// Eight columns a thread; a token's rows eight at a time, all under way before one is added.  The
+// entries without a position are left out first: nothing of theirs is read.
 template <bool BF>
 __global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, uint32_t *errword) {
+  const int lane = threadIdx.x & 63;
   const long long items = (long long)a.tokens * parts;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int t = (int)(it / parts), part = (int)(it - (long long)t * parts);
     const int c = (part * 256 + threadIdx.x) * 8;
-    if (c >= a.n) continue;
+    const bool live = c < a.n;
     float s[8] = {};
-    if (a.add) f8_widen8<BF>(ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + c)), s);
-    for (int j = 0; j < a.top; ++j) {
-      const int pos = ldg(a.inverse + (size_t)t * a.top + j);
-      if (pos == -1) continue;
-      if ((uint32_t)pos >= (uint32_t)a.rows) {
-        f8_error(errword);
-        continue;
+    u32x4 add = {0, 0, 0, 0};
+    if (a.add && live) add = ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + c));
+    bool first = true;
+    for (int j0 = 0; j0 < a.top; j0 += 64) {
+      int pos = -1;
+      float weight = 1.f;
+      if (j0 + lane < a.top) {
+        pos = ldg(a.inverse + (size_t)t * a.top + j0 + lane);
+        if (a.weights) weight = ldg(a.weights + (size_t)t * a.top + j0 + lane);
       }
-      const float w = a.weights ? ldg(a.weights + (size_t)t * a.top + j) : 1.f;
-      float v[8];
-      f8_widen8<BF>(ldg(reinterpret_cast<const u32x4 *>(a.y + (size_t)pos * a.n + c)), v);
+      if (pos != -1 && (uint32_t)pos >= (uint32_t)a.rows) {
+        f8_error(errword);
+        pos = -1;
+      }
+      uint64_t left = __ballot(pos >= 0);
+      while (left) {
+        u32x4 v[8];
+        float w[8];
+        int count = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = fmaf(w, v[i], s[i]);
+        for (int k = 0; k < 8; ++k) {
+          if (!left) break;
+          const int l = __builtin_ctzll(left);
+          left &= left - 1;
+          w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), l));
+          const uint16_t *row = a.y + (size_t)__builtin_amdgcn_readlane(pos, l) * a.n;
+          v[k] = ldg(reinterpret_cast<const u32x4 *>(row + (live ? c : 0)));
+          ++count;
+        }
+        if (first && a.add) f8_widen8<BF>(add, s);
+        first = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k >= count) break;
+          float x[8];
+          f8_widen8<BF>(v[k], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(w[k], x[i], s[i]);
+        }
+      }
     }
-    stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
+    if (first && a.add) f8_widen8<BF>(add, s);
+    if (live) stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
   }
 }
 
@@ -223,29 +289,31 @@ unsigned grid_of(long long items) { return (unsigned)(items < (1 << 22) ? items 
 size_t moe_sort_workspace_bytes(int tokens, int top, int n_experts) {
   const long long n = (long long)tokens * top;
   if (n <= kSortOne) return kWsReserved;
-  return kWsReserved + (size_t)((n + kSortThreads - 1) / kSortThreads) * (n_experts + 1) * 4;
+  return kWsReserved + ((size_t)(n + kSortThreads - 1) / kSortThreads + 1) * n_experts * 4;
 }
 
 hipError_t launch_moe_sort(const int32_t *ids, int tokens, int top, int n_experts, int32_t *offsets, int32_t *order,
                            int32_t *inverse, void *ws, hipStream_t stream) {
   const int n = tokens * top;
   const int grid = n ? (n + kSortThreads - 1) / kSortThreads : 1;
-  uint32_t *errword = static_cast<uint32_t *>(ws), *counts = nullptr;
+  uint32_t *errword = static_cast<uint32_t *>(ws), *counts = nullptr, *totals = nullptr;
   int bits = 1;
-  while ((1 << bits) <= n_experts) ++bits;  // keys 0 .. n_experts
+  while ((1 << bits) < n_experts) ++bits;
   const size_t lds = sort_lds(n_experts);
+  hipError_t e;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(sort_place_kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(sort_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
   if (n > kSortOne) {
     counts = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kWsReserved);
-    sort_count_kernel<<<grid, kSortThreads, (n_experts + 1) * 4, stream>>>(ids, n, n_experts, counts, errword);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    totals = counts + (size_t)grid * n_experts;
+    sort_count_kernel<<<grid, kSortThreads, n_experts * 4, stream>>>(ids, n, n_experts, counts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    sort_scan_kernel<<<n_experts, 256, 0, stream>>>(counts, grid, totals);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  sort_place_kernel<<<grid, kSortThreads, lds, stream>>>(ids, n, n_experts, bits, counts, offsets, order, inverse, errword);
+  sort_place_kernel<<<grid, kSortThreads, lds, stream>>>(ids, n, n_experts, bits, counts, totals, offsets, order, inverse, errword);
   return hipGetLastError();
 }
 
@@ -255,10 +323,9 @@ hipError_t launch_moe_gather(const void *x, int64_t x_row_bytes, int tokens, int
   const bool wide = row_bytes % 16 == 0 && x_row_bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(x) % 16) == 0 &&
                     (reinterpret_cast<uintptr_t>(out) % 16) == 0;
   const int64_t words = row_bytes / (wide ? 16 : 4);
-  const int parts = (int)((words + 255) / 256);
-  const unsigned grid = grid_of((long long)rows * parts);
-  if (wide) gather_kernel<u32x4><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, parts, static_cast<u32x4 *>(out), errword);
-  else gather_kernel<uint32_t><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, parts, static_cast<uint32_t *>(out), errword);
+  const unsigned grid = grid_of(rows);
+  if (wide) gather_kernel<u32x4><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<u32x4 *>(out), errword);
+  else gather_kernel<uint32_t><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<uint32_t *>(out), errword);
   return hipGetLastError();
 }
 

@@ -6,6 +6,10 @@
 
 namespace trellis {
 
+// Bytes of an array from which on a kernel that passes over it once leaves the caches alone (all
+// L2 caches together hold 32 MB).
+constexpr size_t kF8Once = (size_t)24 << 20;
+
 // 16-bit element types.  bf16 is rounded to nearest even; a NaN stays one.
 template <bool BF>
 __device__ __forceinline__ float f8_widen(uint16_t v) {
@@ -38,6 +42,18 @@ __device__ __forceinline__ u32x4 f8_narrow8(const float (&v)[8]) {
 template <typename T>
 __device__ __forceinline__ void stg(T *p, const T &v) {
   *(__attribute__((address_space(1))) T *)p = v;
+}
+
+// The same for what is read or written once and is more than the caches keep (NT): it leaves them to
+// what is used again.
+template <bool NT, typename T>
+__device__ __forceinline__ T ldg_once(const T *p) {
+  return NT ? __builtin_nontemporal_load((const __attribute__((address_space(1))) T *)p) : ldg(p);
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void stg_once(T *p, const T &v) {
+  if (NT) __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T *)p);
+  else stg(p, v);
 }
 
 // The largest magnitude, as bits without sign (a NaN's are above an infinity's, which are above

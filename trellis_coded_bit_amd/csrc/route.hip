@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
 size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves); }
 
 // A workgroup a row, four words a thread under way.
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void gather_kernel(const char *x, int64_t x_row, int tokens, int64_t row_words,
                                                      const int32_t *order, int rows, int per, T *out, uint32_t *errword) {
   for (int row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -158,28 +158,25 @@ __global__ __launch_bounds__(256) void gather_kernel(const char *x, int64_t x_ro
         if (w + 256 * k < row_words) v[k] = ldg(from + w + 256 * k);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (w + 256 * k < row_words) stg(to + w + 256 * k, v[k]);
+        if (w + 256 * k < row_words) stg_once<NT>(to + w + 256 * k, v[k]);
     }
   }
 }
 
-// Eight columns a thread; a token's rows eight at a time, all under way before one is added.  The
-// entries without a position are left out first: nothing of theirs is read.
-template <bool BF>
-__global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, uint32_t *errword) {
+// Eight columns a thread, `parts` times 2048 of a token a workgroup; a token's rows eight at a time,
+// all under way before one is added.  The entries without a position are left out first: nothing of
+// theirs is read.
+template <bool BF, bool NT>
+__global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, int groups, uint32_t *errword) {
   const int lane = threadIdx.x & 63;
-  const long long items = (long long)a.tokens * parts;
+  const long long items = (long long)a.tokens * groups;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int t = (int)(it / parts), part = (int)(it - (long long)t * parts);
-    const int c = (part * 256 + threadIdx.x) * 8;
-    const bool live = c < a.n;
-    float s[8] = {};
-    u32x4 add = {0, 0, 0, 0};
-    if (a.add && live) add = ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + c));
-    bool first = true;
-    for (int j0 = 0; j0 < a.top; j0 += 64) {
-      int pos = -1;
-      float weight = 1.f;
+    const int t = (int)(it / groups), c0 = (int)(it - (long long)t * groups) * parts * 2048;
+    const int c1 = min(c0 + parts * 2048, a.n);
+    int pos = -1;
+    float weight = 1.f;
+    auto look = [&](int j0) {
+      pos = -1;
       if (j0 + lane < a.top) {
         pos = ldg(a.inverse + (size_t)t * a.top + j0 + lane);
         if (a.weights) weight = ldg(a.weights + (size_t)t * a.top + j0 + lane);
@@ -188,40 +185,51 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, u
         f8_error(errword);
         pos = -1;
       }
-      uint64_t left = __ballot(pos >= 0);
-      while (left) {
-        u32x4 v[8];
-        float w[8];
-        int count = 0;
+    };
+    if (a.top <= 64) look(0);
+    for (int c = c0 + threadIdx.x * 8; c - (int)threadIdx.x * 8 < c1; c += 2048) {
+      const bool live = c < c1;
+      const int at = live ? c : c0;
+      float s[8] = {};
+      u32x4 add = {0, 0, 0, 0};
+      if (a.add) add = ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + at));
+      bool first = true;
+      for (int j0 = 0; j0 < a.top; j0 += 64) {
+        if (a.top > 64) look(j0);
+        uint64_t left = __ballot(pos >= 0);
+        while (left) {
+          u32x4 v[8];
+          float w[8];
+          int count = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (!left) break;
-          const int l = __builtin_ctzll(left);
-          left &= left - 1;
-          w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), l));
-          const uint16_t *row = a.y + (size_t)__builtin_amdgcn_readlane(pos, l) * a.n;
-          v[k] = ldg(reinterpret_cast<const u32x4 *>(row + (live ? c : 0)));
-          ++count;
-        }
-        if (first && a.add) f8_widen8<BF>(add, s);
-        first = false;
+          for (int k = 0; k < 8; ++k) {
+            if (!left) break;
+            const int l = __builtin_ctzll(left);
+            left &= left - 1;
+            w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), l));
+            v[k] = ldg_once<NT>(reinterpret_cast<const u32x4 *>(a.y + (size_t)__builtin_amdgcn_readlane(pos, l) * a.n + at));
+            ++count;
+          }
+          if (first && a.add) f8_widen8<BF>(add, s);
+          first = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (k >= count) break;
-          float x[8];
-          f8_widen8<BF>(v[k], x);
+          for (int k = 0; k < 8; ++k) {
+            if (k >= count) break;
+            float x[8];
+            f8_widen8<BF>(v[k], x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = fmaf(w[k], x[i], s[i]);
+            for (int i = 0; i < 8; ++i) s[i] = fmaf(w[k], x[i], s[i]);
+          }
         }
       }
+      if (first && a.add) f8_widen8<BF>(add, s);
+      if (live) stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
     }
-    if (first && a.add) f8_widen8<BF>(add, s);
-    if (live) stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
   }
 }
 
 // A workgroup a token; its choices eight at a time, so that d_out is read once for them.
-template <bool BF>
+template <bool BF, bool NT>
 __global__ __launch_bounds__(256) void combine_grad_kernel(MoeCombine a, uint32_t *errword) {
   __shared__ float part[4][8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -251,14 +259,14 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(MoeCombine a, uint32_
           const size_t at = (size_t)pos[j] * a.n + c;
           if (a.d_weights) {
             float v[8];
-            f8_widen8<BF>(ldg(reinterpret_cast<const u32x4 *>(a.y + at)), v);
+            f8_widen8<BF>(ldg_once<NT>(reinterpret_cast<const u32x4 *>(a.y + at)), v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], v[i], dot[j]);
           }
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = w[j] * d[i];
-          stg(reinterpret_cast<u32x4 *>(a.out + at), f8_narrow8<BF>(o));
+          stg_once<NT>(reinterpret_cast<u32x4 *>(a.out + at), f8_narrow8<BF>(o));
         }
       }
       if (!a.d_weights) continue;
@@ -324,23 +332,31 @@ hipError_t launch_moe_gather(const void *x, int64_t x_row_bytes, int tokens, int
                     (reinterpret_cast<uintptr_t>(out) % 16) == 0;
   const int64_t words = row_bytes / (wide ? 16 : 4);
   const unsigned grid = grid_of(rows);
-  if (wide) gather_kernel<u32x4><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<u32x4 *>(out), errword);
-  else gather_kernel<uint32_t><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<uint32_t *>(out), errword);
+  const bool once = (size_t)rows * row_bytes > kF8Once;
+  if (wide && once) gather_kernel<u32x4, true><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<u32x4 *>(out), errword);
+  else if (wide) gather_kernel<u32x4, false><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<u32x4 *>(out), errword);
+  else gather_kernel<uint32_t, false><<<grid, 256, 0, stream>>>(p, x_row_bytes, tokens, words, order, rows, per, static_cast<uint32_t *>(out), errword);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeCombine &a, uint32_t *errword, hipStream_t stream) {
-  const int parts = (a.n / 8 + 255) / 256;
-  const unsigned grid = grid_of((long long)a.tokens * parts);
-  if (a.bf16) combine_kernel<true><<<grid, 256, 0, stream>>>(a, parts, errword);
-  else combine_kernel<false><<<grid, 256, 0, stream>>>(a, parts, errword);
+  const int all = (a.n + 2047) / 2048, parts = a.tokens >= 1024 ? all : 1, groups = (all + parts - 1) / parts;
+  const unsigned grid = grid_of((long long)a.tokens * groups);
+  const bool once = (size_t)a.rows * a.n * 2 > kF8Once;
+  if (a.bf16 && once) combine_kernel<true, true><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
+  else if (a.bf16) combine_kernel<true, false><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
+  else if (once) combine_kernel<false, true><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
+  else combine_kernel<false, false><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_grad(const MoeCombine &a, uint32_t *errword, hipStream_t stream) {
   const unsigned grid = grid_of(a.tokens);
-  if (a.bf16) combine_grad_kernel<true><<<grid, 256, 0, stream>>>(a, errword);
-  else combine_grad_kernel<false><<<grid, 256, 0, stream>>>(a, errword);
+  const bool once = (size_t)a.rows * a.n * 2 > kF8Once;
+  if (a.bf16 && once) combine_grad_kernel<true, true><<<grid, 256, 0, stream>>>(a, errword);
+  else if (a.bf16) combine_grad_kernel<true, false><<<grid, 256, 0, stream>>>(a, errword);
+  else if (once) combine_grad_kernel<false, true><<<grid, 256, 0, stream>>>(a, errword);
+  else combine_grad_kernel<false, false><<<grid, 256, 0, stream>>>(a, errword);
   return hipGetLastError();
 }
 

@@ -155,22 +155,22 @@ __device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
 // Few rows: the matrix streams through once.
 // ---------------------------------------------------------------------------------------
 
-// A wave's place for one block: 16 NT matrix rows, 16 MF tokens (or 8), their scales.
-template <int MF, int NT, bool Few>
+// A wave's place for one block: 16 NT matrix rows, 8 XC tokens, their scales.
+template <int XC, int NT>
 struct NarrowStage {
-  static constexpr int xcopies = Few ? 1 : 2 * MF, copies = 2 * NT + xcopies + 2;
-  alignas(16) char w[NT * 2048], x[xcopies * 1024];
+  static constexpr int copies = 2 * NT + XC + 2;
+  alignas(16) char w[NT * 2048], x[XC * 1024];
   float sx[64], sw[64];
 };
 
-// A workgroup takes 16 NT matrix rows by 16 MF tokens (Few: up to 8); its waves take the blocks in
-// turn, and their sums are added in the order of the waves.  `reps` tiles of matrix rows follow each
+// A workgroup takes 16 NT matrix rows by 8 XC tokens; its waves take the blocks in turn, and their sums are added in the order of the waves.  `reps` tiles of matrix rows follow each
 // other.  A wave copies into D places of its own, D - 1 blocks ahead over all its tiles, and needs no
 // other wave for that; behind the last it copies that one again, so that the number of copies under
 // way is a constant.
-template <bool BF, int MF, int NT, bool Few, int D>
+template <bool BF, int XC, int NT, int D>
 __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
-  using Stage = NarrowStage<MF, NT, Few>;
+  using Stage = NarrowStage<XC, NT>;
+  constexpr int MF = (XC + 1) / 2;  // tiles of 16 tokens (of an odd XC the last has its eight twice)
   extern __shared__ char raw[];
   const trellis_f8_linear &L = p.g.L;
   const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128, kb = p.kb;
@@ -180,11 +180,11 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   floatx4 *sums = reinterpret_cast<floatx4 *>(raw + waves * D * sizeof(Stage));  // [waves][MF][NT][64]
   const int groups = (p.col_tiles + reps - 1) / reps;
   const int rt = blockIdx.x / groups, c0 = (blockIdx.x - rt * groups) * reps, c1 = min(c0 + reps, p.col_tiles);
-  const RowTile t = find_tile<Few ? 8 : 16>(p, rt, rt == p.row_tiles - 1 && c0 == 0);
+  const RowTile t = find_tile<8>(p, rt, rt == p.row_tiles - 1 && c0 == 0);
   if (t.e < 0) return;
-  uint32_t xat[Stage::xcopies];  // of the lane's tokens behind q, in 16 bytes
+  uint32_t xat[XC];  // of the lane's tokens behind q, in 16 bytes
 #pragma unroll
-  for (int j = 0; j < Stage::xcopies; ++j)
+  for (int j = 0; j < XC; ++j)
     xat[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + 8 * j + (lane >> 3), t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
   const float *sx = p.g.s + (int64_t)max(source_row(p, min(t.row + min(lane, 16 * MF - 1), t.end - 1)), 0) * p.g.s_row;
 
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) copy16(w + ((uint64_t)(wat[j] + u) << 4), o.w + 1024 * j);
 #pragma unroll
-    for (int j = 0; j < Stage::xcopies; ++j) copy16(p.g.q + ((uint64_t)(xat[j] + u) << 4), o.x + 1024 * j);
+    for (int j = 0; j < XC; ++j) copy16(p.g.q + ((uint64_t)(xat[j] + u) << 4), o.x + 1024 * j);
     copy4(sx + b, o.sx);
     copy4(sw + b, o.sw);
     slot = slot + 1 == D ? 0 : slot + 1;
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) a[n] = operand(o.w + (16 * n + i) * 128, lane);
 #pragma unroll
-      for (int m = 0; m < MF; ++m) x[m] = operand(o.x + (Few ? i & 7 : 16 * m + i) * 128, lane);
+      for (int m = 0; m < MF; ++m) x[m] = operand(o.x + (16 * m + (2 * m + 1 < XC ? i : i & 7)) * 128, lane);
 #pragma unroll
       for (int m = 0; m < MF; ++m) f[m] = o.sx[16 * m + i] * o.sw[0];
       if (K - 128 * b < 128)
@@ -292,25 +292,25 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (no copy is under way when the shared memory goes to another workgroup)
 }
 
-template <bool BF, int MF, int NT, bool Few, int D>
+template <bool BF, int XC, int NT, int D>
 hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   const trellis_f8_linear &L = p.g.L;
-  p.tile_rows = Few ? 8 : 16 * MF;
+  p.tile_rows = 8 * XC;
   p.col_tiles = (L.out_features + 16 * NT - 1) / (16 * NT);
   p.row_tiles = p.g.offsets ? p.g.rows / p.tile_rows + min(p.g.rows, L.n_experts) : (p.g.rows + p.tile_rows - 1) / p.tile_rows;
   const long long tiles = (long long)p.row_tiles * p.col_tiles;
   const int reps = tiles > 4096 ? 4 : 1;
-  const int each = D * (int)sizeof(NarrowStage<MF, NT, Few>) + MF * NT * 1024;
+  const int each = D * (int)sizeof(NarrowStage<XC, NT>) + (XC + 1) / 2 * NT * 1024;
   int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
   if (waves > p.kb) waves = p.kb;
   const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps);
   const int lds = waves * each;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(narrow_kernel<BF, MF, NT, Few, D>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(narrow_kernel<BF, XC, NT, D>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  narrow_kernel<BF, MF, NT, Few, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps);
+  narrow_kernel<BF, XC, NT, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps);
   return hipGetLastError();
 }
 
@@ -320,11 +320,16 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
   // Two tiles of matrix rows a workgroup share what is read of the tokens; where that is little, and
   // the tiles are few, one tile each.
   const bool one = each <= 16 && (long long)(p.g.rows + 15) / 16 * ((p.g.L.out_features + 31) / 32) < 1024;
-  if (each <= 8) return one ? launch_narrow<BF, 1, 1, true, 3>(p, stream) : launch_narrow<BF, 1, 2, true, 3>(p, stream);
-  if (each <= 16) return one ? launch_narrow<BF, 1, 1, false, 3>(p, stream) : launch_narrow<BF, 1, 2, false, 3>(p, stream);
-  if (each <= 32) return launch_narrow<BF, 2, 2, false, 3>(p, stream);
-  if (each <= 48) return launch_narrow<BF, 3, 2, false, 2>(p, stream);
-  return launch_narrow<BF, 4, 2, false, 2>(p, stream);
+  switch (each <= 64 ? (each + 7) / 8 : 8) {
+    case 1: return one ? launch_narrow<BF, 1, 1, 3>(p, stream) : launch_narrow<BF, 1, 2, 3>(p, stream);
+    case 2: return one ? launch_narrow<BF, 2, 1, 3>(p, stream) : launch_narrow<BF, 2, 2, 3>(p, stream);
+    case 3: return launch_narrow<BF, 3, 2, 3>(p, stream);
+    case 4: return launch_narrow<BF, 4, 2, 3>(p, stream);
+    case 5: return launch_narrow<BF, 5, 2, 2>(p, stream);
+    case 6: return launch_narrow<BF, 6, 2, 2>(p, stream);
+    case 7: return launch_narrow<BF, 7, 2, 2>(p, stream);
+    default: return launch_narrow<BF, 8, 2, 2>(p, stream);
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -568,7 +573,8 @@ __device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, 
 // together: eight row tiles by the column tiles, row tiles first.  Each XCD has a run of the list.
 __device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int turn, int &rt, int &ct, int &split) {
   const int tiles = row_tiles * p.col_tiles, total = tiles * p.splits, per = total >> 3, rest = total & 7;
-  const int x = blockIdx.x & 7, i = (blockIdx.x >> 3) + turn * ((int)gridDim.x >> 3);
+  // (a turn's tiles move on by one workgroup: the band's tall row tiles would be the same ones' every time)
+  const int x = blockIdx.x & 7, n = (int)gridDim.x >> 3, i = turn * n + ((int)(blockIdx.x >> 3) + turn) % n;
   if (i >= per + (x < rest)) return false;
   int at = x * per + min(x, rest) + i;
   split = at / tiles;

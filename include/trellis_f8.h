@@ -53,7 +53,7 @@ typedef struct {
  * q, scale: E4M3 out [rows][n] and f32 out [rows][ceil(n / 128)]; both or neither (NULL).
  * y       : out [rows][n] for products that take 16 bits, or NULL; one of q and y is given.
  * h_out   : out [rows][n], the next residual, or NULL; may be x (if dense) or residual.
- * n a multiple of 16, at most 32768; eps at least the smallest normal f32 and finite; arrays
+ * n a multiple of 16, at most 32768; rows below 2^22; eps at least the smallest normal f32 and finite; arrays
  * 16-byte aligned.  Outputs may not overlap each other, nor inputs except as said.  One launch. */
 int trellis_f8_norm(int dtype, const void *x, int64_t x_row, const void *residual, const void *gamma, int rows, int n,
                     float eps, void *h_out, uint8_t *q, float *scale, void *y, void *stream);
@@ -79,7 +79,7 @@ size_t trellis_f8_moe_gemm_workspace_bytes(const trellis_f8_linear *L, int rows)
  * y    : out [M][out] of `dtype` at row stride y_row (at least out); must not overlap an input.
  * M >= 0 (0 is a no-op), any out_features; ws: >= trellis_f8_gemm_workspace_bytes().
  * The result does not depend on timing: sums that several workgroups share are joined in a fixed
- * order.  One launch. */
+ * order.  One launch, two where the blocks of few tiles are shared among workgroups. */
 int trellis_f8_gemm(const trellis_f8_linear *L, const uint8_t *q, int64_t q_row, const float *s, int64_t s_row, int M,
                     int dtype, void *y, int64_t y_row, void *ws, size_t ws_bytes, void *stream);
 

@@ -97,6 +97,8 @@ int main() {
   EXPECT(norm(0, x, 248, r, 4, 256, 1e-6f, h, q, s, y) == TRELLIS_EINVAL);
   EXPECT(norm(0, x, -256, r, 4, 256, 1e-6f, h, q, s, y) == TRELLIS_EINVAL);
   EXPECT(norm(0, x, 256, r, -1, 256, 1e-6f, h, q, s, y) == TRELLIS_EINVAL);
+  EXPECT(norm(0, at<void>(big), 32768, nullptr, (1 << 22) - 1, 32768, 1e-6f, nullptr, nullptr, nullptr, at<void>(4 * big)) == TRELLIS_OK && --g_launches == 5);
+  EXPECT(norm(0, at<void>(big), 32768, nullptr, 1 << 22, 32768, 1e-6f, nullptr, nullptr, nullptr, at<void>(4 * big)) == TRELLIS_EINVAL);
   EXPECT(norm(0, x, 256, r, 4, 250, 1e-6f, h, q, s, y) == TRELLIS_EINVAL);
   EXPECT(norm(0, x, 40000, r, 4, 32784, 1e-6f, h, q, s, y) == TRELLIS_EINVAL);
   EXPECT(norm(0, x, 256, r, 4, 256, 0.f, h, q, s, y) == TRELLIS_EINVAL && norm(0, x, 256, r, 4, 256, NAN, h, q, s, y) == TRELLIS_EINVAL);

@@ -224,6 +224,9 @@ def check_product(y, q, s, w, sw, dtype):
     (15, 512, 512), (16, 136, 640), (17, 1000, 400), (31, 384, 1024), (33, 264, 2048), (64, 2048, 1024), (65, 300, 784),
     (100, 1032, 1296), (127, 128, 128), (128, 640, 128), (129, 257, 16), (200, 1288, 2064), (255, 768, 640), (256, 1024, 1152),
     (257, 513, 1024), (300, 256, 4096), (513, 2050, 528), (1000, 264, 272), (2048, 384, 512),
+    # eights of tokens in odd numbers; blocks shared among workgroups
+    (9, 48, 144), (18, 264, 640), (24, 300, 1040), (37, 520, 400), (40, 136, 2048), (50, 257, 656), (56, 640, 272),
+    (70, 4104, 6160), (130, 1544, 16400), (70, 2050, 16400), (300, 1032, 4112),
 ])
 def test_gemm(dtype, m, n, k):
     log_case(f"f8 gemm {dtype} m={m} n={n} k={k}")
@@ -285,6 +288,42 @@ def test_gemm_of_special_values(m):
     assert torch.isnan(z[m - 1]).all() and torch.isnan(z[:, 299]).all() and not torch.isfinite(z[:, 128:256]).any()
 
 
+@pytest.mark.parametrize("m,n,k", [(70, 4099, 6160), (200, 2051, 8208)])
+def test_gemm_of_shared_blocks(m, n, k):
+    """Sums joined from several workgroups: into a slice, of rows inside wider ones, with infinities
+    and NaN, by two graphs that share a workspace with each other and with eager calls."""
+    log_case(f"f8 gemm shared blocks m={m} n={n} k={k}")
+    g = torch.Generator().manual_seed(m)
+    L = make_matrix(n, k, g)
+    q, s = make_rows(m, k, g, 48, 3)
+    ws = torch.zeros(tb.trellis_f8_workspace_bytes(L, m), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > tb.trellis_f8_workspace_bytes(L, 1)
+    wide = torch.full((m, n + 9), 3.0, dtype=torch.float16, device="cuda")
+    y = wide[:, 5:5 + n]
+    tb.trellis_f8_gemm(L, q, s, out=y, ws=ws)
+    check_product(y, q, s, L.w, L.scale, "fp16")
+    want = y.clone()
+    y.fill_(3.0)
+    assert (wide == 3.0).all()
+    outs, graphs = [torch.empty((m, n), dtype=torch.float16, device="cuda") for _ in range(2)], []
+    for o in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            tb.trellis_f8_gemm(L, q, s, out=o, ws=ws)
+    for _ in range(3):
+        for o, graph in zip(outs, graphs):
+            o.fill_(9.0)
+            graph.replay()
+        tb.trellis_f8_gemm(L, q, s, out=y, ws=ws)
+        assert all(torch.equal(o, want) for o in outs) and torch.equal(y, want)
+    s[m - 1, k // 256] = float("nan")
+    w = L.w.clone()
+    w.view(torch.uint8)[n - 1, k - 1] = 0x7F
+    z = tb.trellis_f8_gemm(tb.F8Linear(w, L.scale), q, s, ws=ws)
+    assert torch.isnan(z[m - 1]).all() and torch.isnan(z[:, n - 1]).all() and torch.equal(z[:-1, :-1], want[:-1, :-1])
+    assert tb.error_word(ws) == 0
+
+
 def test_gemm_overflow_is_infinite():
     log_case("f8 gemm overflow")
     L = tb.F8Linear(torch.full((16, 128), 448.0).to(torch.float8_e4m3fn).cuda(), torch.ones((1, 1), device="cuda"))
@@ -317,6 +356,7 @@ def grouped(counts, n, k, g, per=0, tokens=0):
     ([1], 128, 128, 0), ([0, 0, 3, 0], 136, 144, 0), ([5, 0, 1, 17, 16, 0, 33, 2], 264, 272, 4),
     ([130, 1, 0, 257, 128, 64], 392, 656, 2), ([1] * 70 + [0] * 30 + [2] * 30, 160, 384, 8), ([300, 700], 512, 1024, 0),
     ([0] * 199 + [40], 128, 256, 8), ([2, 3, 1, 2, 0, 4, 2, 2], 1024, 2048, 8),
+    ([20, 40, 0, 7], 264, 400, 2), ([60, 1, 30], 136, 640, 0), ([1] * 300, 32, 144, 4),
 ])
 def test_moe_gemm(dtype, counts, n, k, per):
     log_case(f"f8 moe_gemm {dtype} experts={len(counts)} rows={sum(counts)} n={n} k={k} per={per}")
@@ -370,6 +410,19 @@ def test_moe_gemm_bad_offsets(offsets, done):
     tb.trellis_f8_moe_gemm(L, q, s, ints(offsets), out=out)
     assert torch.equal(out[:done], good[:done]) and (out[done:] == 5.0).all()
     assert tb.error_word() == (0 if done == 9 else 1)
+    tb.clear_error_word()
+
+
+@pytest.mark.parametrize("rows,offsets,done", [(1, [0, 1, 5], 1), (1, [0, 1, 0], 1), (40, [0, 20, 40, 41], 40), (200, [0, 100, 200, 100], 200)])
+def test_moe_gemm_bad_offsets_behind_the_last_row(rows, offsets, done):
+    """They are found also where every row has its expert before them."""
+    log_case(f"f8 moe_gemm rows={rows} offsets={offsets}")
+    g = torch.Generator().manual_seed(1)
+    L = make_matrix(128, 256, g, len(offsets) - 1)
+    q, s = make_rows(rows, 256, g)
+    good = tb.trellis_f8_moe_gemm(L, q, s, ints(offsets[:-1] + [rows]))
+    tb.clear_error_word()
+    assert torch.equal(tb.trellis_f8_moe_gemm(L, q, s, ints(offsets))[:done], good[:done]) and tb.error_word() == 1
     tb.clear_error_word()
 
 

@@ -28,7 +28,7 @@ def routing(tokens, top, experts, g, share=1.0):
 @pytest.mark.parametrize("tokens,top,experts,share", [
     (1, 1, 1, 1.0), (1, 8, 256, 1.0), (3, 5, 2, 1.0), (64, 1, 64, 1.0), (65, 8, 7, 0.5), (33, 8, 256, 1.0), (128, 8, 2048, 1.0),
     (513, 8, 256, 0.25), (1024, 3, 63, 1.0), (5000, 6, 65, 0.9), (4, 1024, 100, 0.7), (20, 4, 16, 0.0), (8193, 8, 256, 1.0),
-    (20000, 8, 64, 1.0), (16384, 4, 2048, 0.5), (100001, 8, 130, 0.6),
+    (20000, 8, 64, 1.0), (16384, 4, 2048, 0.5), (100001, 8, 130, 0.6), (8192, 8, 64, 1.0), (65537, 1, 300, 0.9),
 ])
 def test_sort(tokens, top, experts, share):
     log_case(f"moe sort tokens={tokens} top={top} experts={experts} share={share}")

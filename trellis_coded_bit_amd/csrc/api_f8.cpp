@@ -159,7 +159,8 @@ int trellis_f8_norm(int dtype, const void *x, int64_t x_row, const void *residua
   abi_clear();
   int st = check_dtype(dtype);
   if (st) return st;
-  if (rows < 0 || rows > (1 << 22)) return abi_fail(TRELLIS_EINVAL, "rows=%d not in 0..2^22", rows);
+  // (a workgroup of up to 1024 threads a row, below 2^32 threads in all)
+  if (rows < 0 || rows >= (1 << 22)) return abi_fail(TRELLIS_EINVAL, "rows=%d not in 0..2^22-1", rows);
   if (n < 16 || n % 16 || n > trellis::kF8MaxNorm)
     return abi_fail(TRELLIS_EINVAL, "n=%d must be a multiple of 16 in 16..%d", n, trellis::kF8MaxNorm);
   if (!std::isfinite(eps) || eps < FLT_MIN) return abi_fail(TRELLIS_EINVAL, "eps=%g must be a normal positive number", (double)eps);

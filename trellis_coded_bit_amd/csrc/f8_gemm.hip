@@ -5,6 +5,7 @@
 // one v_mfma_f32_16x16x128_f8f6f4 forms a 16 x 16 tile of a block's products from zero, and a
 // vector fma adds it times its scales.  Matrix rows are the tile's rows and tokens its columns, so
 // a lane's four sums belong to one token and take one factor.
+#include <climits>
 #include <cmath>
 
 #include "f8_device.h"
@@ -46,9 +47,8 @@ __device__ __forceinline__ Cut cut_rows(int n, int T) {
 }
 
 // Tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert after expert.
-// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  Called by whole waves.
-// The list ends at the first pair of offsets that is out of
-// order or out of range.
+// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  The list ends at the
+// first pair of offsets that is out of order or out of range.  Called by whole waves.
 template <int U>
 __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool report) {
   if (!p.g.offsets) {
@@ -180,7 +180,8 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   floatx4 *sums = reinterpret_cast<floatx4 *>(raw + waves * D * sizeof(Stage));  // [waves][MF][NT][64]
   const int groups = (p.col_tiles + reps - 1) / reps;
   const int rt = blockIdx.x / groups, c0 = (blockIdx.x - rt * groups) * reps, c1 = min(c0 + reps, p.col_tiles);
-  const RowTile t = find_tile<8>(p, rt, rt == p.row_tiles - 1 && c0 == 0);
+  const bool checks = rt == p.row_tiles;  // (the last of a grouped call: the offsets, to their end)
+  const RowTile t = find_tile<8>(p, checks ? INT_MAX : rt, checks);
   if (t.e < 0) return;
   uint32_t xat[XC];  // of the lane's tokens behind q, in 16 bytes
 #pragma unroll
@@ -299,11 +300,13 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   p.col_tiles = (L.out_features + 16 * NT - 1) / (16 * NT);
   p.row_tiles = p.g.offsets ? p.g.rows / p.tile_rows + min(p.g.rows, L.n_experts) : (p.g.rows + p.tile_rows - 1) / p.tile_rows;
   const long long tiles = (long long)p.row_tiles * p.col_tiles;
-  const int reps = tiles > 4096 ? 4 : 1;
+  // (in long calls a workgroup's first copies and its look at the offsets serve four tiles: a decode
+  // batch's experts 674 -> 629 us)
+  const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
   const int each = D * (int)sizeof(NarrowStage<XC, NT>) + (XC + 1) / 2 * NT * 1024;
   int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
   if (waves > p.kb) waves = p.kb;
-  const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps);
+  const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps) + (p.g.offsets ? 1 : 0);
   const int lds = waves * each;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(narrow_kernel<BF, XC, NT, D>),
@@ -614,7 +617,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   extern __shared__ char raw[];
   WideLds &lds = *reinterpret_cast<WideLds *>(raw);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row_tiles = find_tile<32>(p, 0x7FFFFFFF, blockIdx.x == 0).row;
+  const int row_tiles = find_tile<32>(p, INT_MAX, blockIdx.x == 0).row;
   WideTile x;
   bool more = wide_next(p, row_tiles, 0, wave, x, lds);
   for (int turn = 1; more; ++turn) {

@@ -320,10 +320,16 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
 // `each`: rows of a matrix, about.
 template <bool BF>
 hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
+  int xc = each <= 64 ? (int)(each + 7) / 8 : 8;
+  const long long cols = (p.g.L.out_features + 31) / 32;
+  // Fewer tokens a workgroup where that gives less than a workgroup to half of the CUs (64 x 256 x 16384:
+  // 18.1 -> 8.2 us, 64 x 1024 x 16384: 18.0 -> 9.0); up to 192 it costs as often as it gives (33 x 5120 x
+  // 6144: 8.5 -> 12.2, 48 x 4096 x 6144: 9.8 -> 7.8).
+  while (!p.g.offsets && xc > 1 && (p.g.rows + 8 * xc - 1) / (8 * xc) * cols < 128) xc = (xc + 1) / 2;
   // Two tiles of matrix rows a workgroup share what is read of the tokens; where that is little, and
   // the tiles are few, one tile each.
-  const bool one = each <= 16 && (long long)(p.g.rows + 15) / 16 * ((p.g.L.out_features + 31) / 32) < 1024;
-  switch (each <= 64 ? (each + 7) / 8 : 8) {
+  const bool one = xc <= 2 && (p.g.rows + 15) / 16 * cols < 1024;
+  switch (xc) {
     case 1: return one ? launch_narrow<BF, 1, 1, 3>(p, stream) : launch_narrow<BF, 1, 2, 3>(p, stream);
     case 2: return one ? launch_narrow<BF, 2, 1, 3>(p, stream) : launch_narrow<BF, 2, 2, 3>(p, stream);
     case 3: return launch_narrow<BF, 3, 2, 3>(p, stream);

@@ -34,6 +34,12 @@ struct RowTile {
   int e, row, end;
 };
 
+// An expert's rows [row, end) in tiles of `size`, `first` tiles of earlier experts before them.
+struct RowTiles {
+  int e, row, end, size, tiles, first;
+  __device__ __forceinline__ RowTile operator[](int i) const { return {e, row + i * size, min(end, row + (i + 1) * size)}; }
+};
+
 // n rows as tiles of at most T rows, T a multiple of U: as few as that takes, of the same size (a
 // multiple of U) but for the last.
 struct Cut {
@@ -46,15 +52,14 @@ __device__ __forceinline__ Cut cut_rows(int n, int T) {
   return {(n + size - 1) / size, size};
 }
 
-// Tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert after expert.
-// Behind the last (at = INT_MAX, say) e is -1 and row the number of tiles.  The list ends at the
-// first pair of offsets that is out of order or out of range.  Called by whole waves.
+// The expert of tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert
+// after expert.  Behind the last (at = INT_MAX, say) e is -1 and `first` the number of tiles.  The
+// list ends at the first pair of offsets that is out of order or out of range.  Called by whole waves.
 template <int U>
-__device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool report) {
+__device__ __forceinline__ RowTiles find_tiles(const GemmArgs &p, int at, bool report) {
   if (!p.g.offsets) {
     const Cut c = cut_rows<U>(p.g.rows, p.tile_rows);
-    if (at >= c.tiles) return {-1, c.tiles, 0};
-    return {0, at * c.size, min(p.g.rows, (at + 1) * c.size)};
+    return {at < c.tiles ? 0 : -1, 0, p.g.rows, c.size, c.tiles, at < c.tiles ? 0 : c.tiles};
   }
   const int lane = opaque_tid() & 63, E = p.g.L.n_experts;
   int passed = 0;
@@ -82,23 +87,21 @@ __device__ __forceinline__ RowTile find_tile(const GemmArgs &p, int at, bool rep
     const uint64_t has = __ballot(at < passed + s);
     if (has) {
       const int l = __builtin_ctzll(has);
-      int i = at - passed - (s - sum), e = e0 + 4 * lane, row = 0, end = 0;
+      int first = passed + s - sum;
+      RowTiles r = {e0 + 4 * lane, 0, 0, U, 0, first};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (i >= 0 && i < c[k].tiles) {
-          row = o[k] + i * c[k].size;
-          end = min(o[k + 1], row + c[k].size);
-          e = e0 + 4 * lane + k;
-        }
-        i -= c[k].tiles;
+        if (at >= first && at - first < c[k].tiles) r = {e0 + 4 * lane + k, o[k], o[k + 1], c[k].size, c[k].tiles, first};
+        first += c[k].tiles;
       }
-      return {__builtin_amdgcn_readlane(e, l), __builtin_amdgcn_readlane(row, l), __builtin_amdgcn_readlane(end, l)};
+      return {__builtin_amdgcn_readlane(r.e, l),    __builtin_amdgcn_readlane(r.row, l),   __builtin_amdgcn_readlane(r.end, l),
+              __builtin_amdgcn_readlane(r.size, l), __builtin_amdgcn_readlane(r.tiles, l), __builtin_amdgcn_readlane(r.first, l)};
     }
     passed += __builtin_amdgcn_readlane(s, 63);
     wrong = bads != 0;
   }
   if (wrong && report && lane == 0) f8_error(p.errword);
-  return {-1, passed, 0};
+  return {-1, 0, 0, U, 0, passed};
 }
 
 // The row of q that a row reads, or -1.
@@ -181,8 +184,9 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   const int groups = (p.col_tiles + reps - 1) / reps;
   const int rt = blockIdx.x / groups, c0 = (blockIdx.x - rt * groups) * reps, c1 = min(c0 + reps, p.col_tiles);
   const bool checks = rt == p.row_tiles;  // (the last of a grouped call: the offsets, to their end)
-  const RowTile t = find_tile<8>(p, checks ? INT_MAX : rt, checks);
-  if (t.e < 0) return;
+  const RowTiles tiles = find_tiles<8>(p, checks ? INT_MAX : rt, checks);
+  if (tiles.e < 0) return;
+  const RowTile t = tiles[rt - tiles.first];
   uint32_t xat[XC];  // of the lane's tokens behind q, in 16 bytes
 #pragma unroll
   for (int j = 0; j < XC; ++j)
@@ -578,28 +582,24 @@ __device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, 
   }
 }
 
-// Tiles in an order that keeps what runs at a time on one XCD (every eighth workgroup) close
-// together: eight row tiles by the column tiles, row tiles first.  Each XCD has a run of the list.
-__device__ __forceinline__ bool tile_of(const GemmArgs &p, int row_tiles, int turn, int &rt, int &ct, int &split) {
-  const int tiles = row_tiles * p.col_tiles, total = tiles * p.splits, per = total >> 3, rest = total & 7;
-  // (a turn's tiles move on by one workgroup: the band's tall row tiles would be the same ones' every time)
-  const int x = blockIdx.x & 7, n = (int)gridDim.x >> 3, i = turn * n + ((int)(blockIdx.x >> 3) + turn) % n;
-  if (i >= per + (x < rest)) return false;
-  int at = x * per + min(x, rest) + i;
-  split = at / tiles;
-  at -= split * tiles;
-  const int band = at / (8 * p.col_tiles), in = at - band * 8 * p.col_tiles;
-  const int high = min(8, row_tiles - 8 * band);
-  ct = in / high;
-  rt = 8 * band + in - ct * high;
-  return true;
-}
-
-// Looks up what a workgroup does in its turn, and starts its first copies.
+// Looks up what a workgroup does in its turn, and starts its first copies.  Tiles come in an order
+// that keeps what runs at a time on one XCD (every eighth workgroup, with a run of the list) close
+// together: expert after expert; of an expert up to eight row tiles by the column tiles, row tiles
+// first, so that they share the matrix's rows while these are in the XCD's cache.
 __device__ __forceinline__ bool wide_next(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
-  int rt, ct;
-  if (!tile_of(p, row_tiles, turn, rt, ct, x.split)) return false;
-  x.t = find_tile<32>(p, rt, false);
+  const int tiles = row_tiles * p.col_tiles, total = tiles * p.splits, per = total >> 3, rest = total & 7;
+  // (a turn's tiles move on by one workgroup: a band's tall row tiles would be the same ones' every time)
+  const int xcd = blockIdx.x & 7, n = (int)gridDim.x >> 3, i = turn * n + ((int)(blockIdx.x >> 3) + turn) % n;
+  if (i >= per + (xcd < rest)) return false;
+  int at = xcd * per + min(xcd, rest) + i;
+  x.split = at / tiles;
+  at -= x.split * tiles;
+  const RowTiles r = find_tiles<32>(p, at / p.col_tiles, false);
+  at -= r.first * p.col_tiles;
+  const int bands = (r.tiles + 7) >> 3, band_rows = (r.tiles + bands - 1) / bands, band = at / (band_rows * p.col_tiles);
+  at -= band * band_rows * p.col_tiles;
+  const int high = min(band_rows, r.tiles - band * band_rows), ct = at / high;
+  x.t = r[band * band_rows + at - ct * high];
   x.n0 = ct * kWideOut;
   wide_begin(p, x, wave, lds);
   return true;
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   extern __shared__ char raw[];
   WideLds &lds = *reinterpret_cast<WideLds *>(raw);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row_tiles = find_tile<32>(p, INT_MAX, blockIdx.x == 0).row;
+  const int row_tiles = find_tiles<32>(p, INT_MAX, blockIdx.x == 0).first;
   WideTile x;
   bool more = wide_next(p, row_tiles, 0, wave, x, lds);
   for (int turn = 1; more; ++turn) {

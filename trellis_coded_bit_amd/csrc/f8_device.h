@@ -7,7 +7,8 @@
 namespace trellis {
 
 // Bytes of an array from which on a kernel that passes over it once leaves the caches alone (all
-// L2 caches together hold 32 MB).
+// L2 caches together hold 32 MB).  Rows gathered and combined for 4097 tokens: 117 us so, 140 without;
+// the gradients for 4096: 214 and 233.
 constexpr size_t kF8Once = (size_t)24 << 20;
 
 // 16-bit element types.  bf16 is rounded to nearest even; a NaN stays one.

@@ -4,7 +4,13 @@
 // y[m][o] = sum over blocks b of 128 inputs of s[m][b] sw[o / 128][b] (q[m] . w[o] over the block):
 // one v_mfma_f32_16x16x128_f8f6f4 forms a 16 x 16 tile of a block's products from zero, and a
 // vector fma adds it times its scales.  Matrix rows are the tile's rows and tokens its columns, so
-// a lane's four sums belong to one token and take one factor.
+// a lane's four sums belong to one token and take one factor.  The scales are not put into the
+// instruction's own: those are powers of two.
+//
+// Rounding: the instruction adds the products of eight neighbouring channels in steps of 2^-13 of the
+// power of two of the largest one's factors, cut off towards zero, and the eights in about 24 bits
+// (measured; the form without scales does the same), which leaves a block's sum off by 2e-5 rms.
+// All else is f32, rounded once to 16 bits at the end.
 #include <climits>
 #include <cmath>
 
@@ -155,7 +161,7 @@ __device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Few rows: the matrix streams through once.
+// Few rows: the matrix streams through once, and its bytes bound the kernel.
 // ---------------------------------------------------------------------------------------
 
 // A wave's place for one block: 16 NT matrix rows, 8 XC tokens, their scales.
@@ -166,10 +172,13 @@ struct NarrowStage {
   float sx[64], sw[64];
 };
 
-// A workgroup takes 16 NT matrix rows by 8 XC tokens; its waves take the blocks in turn, and their sums are added in the order of the waves.  `reps` tiles of matrix rows follow each
-// other.  A wave copies into D places of its own, D - 1 blocks ahead over all its tiles, and needs no
-// other wave for that; behind the last it copies that one again, so that the number of copies under
-// way is a constant.
+// A workgroup takes 16 NT matrix rows by 8 XC tokens; its waves take the blocks in turn, and their sums
+// are added in the order of the waves.  `reps` tiles of matrix rows follow each other.  A wave copies
+// into D places of its own, D - 1 blocks ahead over all its tiles, and needs no other wave for that;
+// behind the last it copies that one again, so that the number of copies under way is a constant.
+// One token over 17408 x 5120 takes 15.4 us (5.8 TB/s of the 6.4 that a stream reads at; 18 where the
+// matrix is in no cache), 37 tokens over 5120 x 6144 9.6 (tokens in sixteens: 10.7), 33 tokens' 264
+// entries over 256 experts' 4096 x 6144 605 to 640.
 template <bool BF, int XC, int NT, int D>
 __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   using Stage = NarrowStage<XC, NT>;
@@ -305,9 +314,11 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   p.row_tiles = p.g.offsets ? p.g.rows / p.tile_rows + min(p.g.rows, L.n_experts) : (p.g.rows + p.tile_rows - 1) / p.tile_rows;
   const long long tiles = (long long)p.row_tiles * p.col_tiles;
   // (in long calls a workgroup's first copies and its look at the offsets serve four tiles: a decode
-  // batch's experts 674 -> 629 us)
+  // batch's experts 678 -> 632 us)
   const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
   const int each = D * (int)sizeof(NarrowStage<XC, NT>) + (XC + 1) / 2 * NT * 1024;
+  // (few tiles of long rows: 4 tokens over 256 x 16384 8.1 us with four waves, 7.3 with eight; elsewhere
+  // within 0.2)
   int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
   if (waves > p.kb) waves = p.kb;
   const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps) + (p.g.offsets ? 1 : 0);
@@ -330,9 +341,13 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
   // 18.1 -> 8.2 us, 64 x 1024 x 16384: 18.0 -> 9.0); up to 192 it costs as often as it gives (33 x 5120 x
   // 6144: 8.5 -> 12.2, 48 x 4096 x 6144: 9.8 -> 7.8).
   while (!p.g.offsets && xc > 1 && (p.g.rows + 8 * xc - 1) / (8 * xc) * cols < 128) xc = (xc + 1) / 2;
-  // Two tiles of matrix rows a workgroup share what is read of the tokens; where that is little, and
-  // the tiles are few, one tile each.
-  const bool one = xc <= 2 && (p.g.rows + 15) / 16 * cols < 1024;
+  // Two tiles of matrix rows a workgroup share what is read of the tokens.  Where that is little, one
+  // tile each, unless two come to a workgroup a CU or the tiles are many (us of one | two, K = 5120 to
+  // 8192: 16 rows of 2048 7.7 | 8.9, of 5120 12.2 | 10.3, of 8192 11.9 | 11.0, of 9216 15.0 | 17.2, of
+  // 17408 24.1 | 25.6, of 69632 90 | 80; one row 7.9 | 8.7, 9.3 | 9.4, 9.9 | 10.2, 12.0 | 13.7, 18.2 |
+  // 19.9, 65 | 59).
+  const long long two = (p.g.rows + 15) / 16 * cols;
+  const bool one = xc <= 2 && two < 1024 && (two < 128 || two > 256);
   switch (xc) {
     case 1: return one ? launch_narrow<BF, 1, 1, 3>(p, stream) : launch_narrow<BF, 1, 2, 3>(p, stream);
     case 2: return one ? launch_narrow<BF, 2, 1, 3>(p, stream) : launch_narrow<BF, 2, 2, 3>(p, stream);
@@ -347,6 +362,16 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
 
 // ---------------------------------------------------------------------------------------
 // Many rows: 256 matrix rows by up to 256 tokens a workgroup of eight waves, 64 by up to 128 a wave.
+//
+// A block of 128 inputs takes a workgroup 1.70 to 1.85 us at 256 tokens (2300 to 2580 TFLOP/s over the
+// card).  Of copies of the kernel that leave something out, the one without copies from memory takes
+// 1.40, without the meetings 1.37 then, without the reads of shared memory 1.30, with the matrix
+// instructions alone 1.10 to 1.26.  So no single part bounds it: the matrix unit is busy 45 % of the
+// time, and fmas (half as many cycles as the products), operand reads and copies (together half of
+// shared memory's cycles, without conflicts) do not all fit beside it with two waves a SIMD; a third
+// would not have the registers for its sums, which vector instructions must reach.
+// 2048 x 5120 by 17408: 186 to 190 us (1950 TFLOP/s; two turns of tiles and one of an eighth of them,
+// cut as three turns of 224 tokens).  64 experts with 32768 rows, 4096 x 6144: 910 to 930 us (1790).
 // ---------------------------------------------------------------------------------------
 
 constexpr int kWideThreads = 512, kWideOut = 256, kWideRows = 256;
@@ -356,10 +381,7 @@ struct WideLds {
   alignas(16) float sx[2][kWideRows], sw[2][64];
 };
 
-// Where a lane's copies come from.  A row in shared memory is 128 bytes, eight chunks of 16; chunk
-// p of row r holds the row's chunk p ^ (r & 7), so that the products' reads of one chunk from
-// eight rows fall on eight places.  Lane l of a copy has row l / 8 of its eight rows.  Chunks
-// behind in_features repeat the row's last one; the products take zeros of the matrix there.
+// Where a lane's copies come from.
 struct WideFrom {
   uint32_t w[4], x[4];  // rows 64 j + 8 wave + l / 8: in 16 bytes from the tile's first row, from q
   const float *s;       // waves 0..3: the scales of row 64 wave + l; 4..7: of the tile's matrix blocks
@@ -406,10 +428,12 @@ __device__ __forceinline__ void wide_meet() {
 }
 
 // A wave's 64 matrix rows by 16 MF tokens over all blocks.  Its tile m takes tokens 32 m + 16 wm ..
-// A product's results are added to the sums while the next four products run, and operands are
-// read one tile ahead, the next block's first ones too: what they wait for was met half a block
-// before.  On entry blocks 0 and 1 are in shared memory.  Two meetings a block: at the middle all waves have read the block's matrix and first
-// tokens, whose places then take the block after next; at the end the rest.
+// A product's results are added to the sums while the next ones run, and operands are read one tile
+// ahead, the next block's first ones too: what they wait for was met half a block before.  On entry
+// blocks 0 and 1 are in shared memory.  Two meetings a block: at the middle all waves have read the
+// block's matrix and first tokens, whose places then take the block after next; at the end the rest.
+// (One meeting a block, results used at once and operands read within a block: 219 us for the 195 that
+// this gave 2048 x 17408 x 5120.)
 constexpr int kBehind = 3;  // products between one and the use of its results (at most 4)
 
 template <int MF>
@@ -526,9 +550,9 @@ __device__ __forceinline__ void wide_begin(const GemmArgs &p, WideTile &x, int w
   }
 }
 
-// The sums of a tile, rounded and stored.  A lane has four neighbouring columns
-// of one token in each of its tiles; two tiles' are exchanged between neighbouring rows of lanes
-// so that it has eight of one.
+// The sums of a tile, rounded and stored, or as they are where others are to be added.  A lane has four
+// neighbouring columns of one token in each of its tiles; two tiles' are exchanged between neighbouring
+// rows of lanes so that it has eight of one.
 template <bool BF, int MF>
 __device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, int n0, int split, int wave, const floatx4 (&acc)[MF][4]) {
   const int lane = opaque_tid() & 63;
@@ -585,7 +609,8 @@ __device__ __forceinline__ void wide_store(const GemmArgs &p, const RowTile &t, 
 // Looks up what a workgroup does in its turn, and starts its first copies.  Tiles come in an order
 // that keeps what runs at a time on one XCD (every eighth workgroup, with a run of the list) close
 // together: expert after expert; of an expert up to eight row tiles by the column tiles, row tiles
-// first, so that they share the matrix's rows while these are in the XCD's cache.
+// first, so that they share the matrix's rows while these are in the XCD's cache (the experts above:
+// 26.0 M lines missed there, 35.5 M where eight row tiles were taken whatever their experts; 2 to 6 %).
 __device__ __forceinline__ bool wide_next(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
   const int tiles = row_tiles * p.col_tiles, total = tiles * p.splits, per = total >> 3, rest = total & 7;
   // (a turn's tiles move on by one workgroup: a band's tall row tiles would be the same ones' every time)
@@ -617,7 +642,7 @@ __device__ __forceinline__ bool wide_tile(const GemmArgs &p, int row_tiles, int 
   return more;
 }
 
-// One workgroup a CU, tile after tile.
+// One workgroup a CU, tile after tile.  The number of a tile's tokens, in 32s, picks the code for it.
 template <bool BF>
 __global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(GemmArgs p) {
   extern __shared__ char raw[];
@@ -671,7 +696,9 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
 // How a call is divided.  Times in microseconds, as measured: the narrow kernel takes 0.86 ns for a
 // block of 64 tokens by 32 matrix rows over the whole card; a wide workgroup 0.45 + 0.156 a block for
 // every 32 of its tokens, and 3 a tile; a split's sums are written and read at 5 TB/s by one launch
-// more.
+// more.  Matrices in no cache, narrow | wide, blocks whole | wide, blocks shared: 5120 x 6144 with 32
+// rows 12.4 | 56 | 18, 64 rows 17.7 | 57 | 20, 128 rows 25 | 54 | 23, 256 rows 36 | 52 | 29, 512 rows
+// 58 | 50 | 37; 17408 x 5120 with 32 rows 31 | - | 30, 64 rows 43 | 54 | 32, 128 rows 60 | 53 | 39.
 struct Plan {
   bool narrow;
   int tile_rows, splits;

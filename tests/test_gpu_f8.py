@@ -466,6 +466,23 @@ def test_refusals():
             f()
 
 
+def test_sizes_above_32_bits_are_refused():
+    """Not cut off to the small sizes that their lower 32 bits are."""
+    log_case("f8 sizes above 32 bits")
+    g = torch.Generator().manual_seed(0)
+    L, E = make_matrix(128, 128, g), make_matrix(128, 128, g, 2)
+    q, s = make_rows(4, 128, g)
+    many = 2 ** 32 + 4
+    x = torch.zeros((1, 32), dtype=torch.float16, device="cuda").expand(many, 32)
+    ids = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    for f in (lambda: tb.trellis_f8_norm(x, None, 1e-6), lambda: tb.trellis_f8_silu_mul(x), lambda: tb.trellis_moe_sort(ids, many),
+              lambda: tb.trellis_f8_gemm(L, q[:1].expand(many, 128), s[:1].expand(many, 1)),
+              lambda: tb.trellis_f8_moe_gemm(E, q, s, ints([0, 2, 4]), order=ints([0, 1, 2, 3]), per=2 ** 32 + 1),
+              lambda: tb.trellis_moe_gather(x, ints([0, 1]), 1), lambda: tb.trellis_moe_gather(q, ints([0, 1]), 2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            f()
+
+
 @pytest.mark.parametrize("m", [1, 48, 300])
 def test_gemm_in_a_graph_and_on_streams(m):
     """Captured with a workspace of its own and replayed with other inputs, beside eager calls on

@@ -904,6 +904,13 @@ def _f8_blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _i31(n: int, name: str) -> int:
+    """A size that the C call takes in 32 bits (ctypes would cut it off)."""
+    if n >> 31:
+        raise ValueError(f"{name}={n} not in 0..2^31-1")
+    return n
+
+
 def _f8_rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None, device=None,
              cols: Optional[int] = None) -> int:
     """Checks a [rows, cols] tensor on the current device whose rows are contiguous (16-bit if
@@ -914,7 +921,8 @@ def _f8_rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None, de
         if d is dtype or (dtype is None and d in _F8_DTYPE):
             rows, n = t.shape
             row, last = t.stride()
-            if (last == 1 or n <= 1) and (cols is None or n == cols) and (device is None or t.device == device):
+            if ((last == 1 or n <= 1) and (cols is None or n == cols) and (device is None or t.device == device)
+                    and not (rows | n) >> 31):
                 return row if rows > 1 else n
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -926,6 +934,8 @@ def _f8_rows(t: torch.Tensor, name: str, dtype: Optional[torch.dtype] = None, de
         raise ValueError(f"{name} is on {t.device}: the current device is cuda:{torch._C._cuda_getDevice()}")
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [rows, {'n' if cols is None else cols}], got {tuple(t.shape)}")
+    _i31(t.shape[0], f"rows of {name}")
+    _i31(t.shape[1], f"columns of {name}")
     raise ValueError(f"{name}: each row must be contiguous")
 
 
@@ -1105,29 +1115,32 @@ def trellis_f8_moe_gemm(layer: F8Linear, q: torch.Tensor, scale: torch.Tensor, o
         raise ValueError(f"offsets must have {layer.experts + 1} entries, got {offsets.numel()}")
     if order is not None:
         _kv4_int(order, "order", layer.device)
-    rows = q.shape[0] if order is None else order.numel()
+    rows = q.shape[0] if order is None else _i31(order.numel(), "entries of order")
     q_row, s_row, out, y_row = _f8_product(layer, q, scale, rows, dtype, out)
     ws = _f8_ws(ws, _f8_bytes(layer, rows), layer.device)
     _check(lib().trellis_f8_moe_gemm(layer._ref, q.data_ptr(), q_row, scale.data_ptr(), s_row, q.shape[0], offsets.data_ptr(),
-                                     _ptr(order), per, rows, _F8_DTYPE[out.dtype], out.data_ptr(), y_row, ws.data_ptr(),
+                                     _ptr(order), _i31(per, "per"), rows, _F8_DTYPE[out.dtype], out.data_ptr(), y_row, ws.data_ptr(),
                                      ws.numel(), _stream()))
     return out
 
 
 def _moe_ids(t: torch.Tensor, name: str, device=None) -> Tuple[int, int]:
     if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.dtype is torch.int32 and t.is_contiguous()
-            and t.get_device() == torch._C._cuda_getDevice() and (device is None or t.device == device)):
+            and t.get_device() == torch._C._cuda_getDevice() and (device is None or t.device == device)
+            and not t.numel() >> 31):
         return t.shape
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be [tokens, top]")
     _req(t, torch.int32, name, device)
     if t.device.index != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}: the current device is cuda:{torch._C._cuda_getDevice()}")
+    _i31(t.numel(), f"entries of {name}")
     return t.shape[0], t.shape[1]
 
 
 @functools.lru_cache(maxsize=4096)
 def _moe_sort_bytes(tokens: int, top: int, experts: int) -> int:
+    _i31(tokens | top | experts, "a size of the sort")
     nb = lib().trellis_moe_sort_workspace_bytes(tokens, top, experts)
     if nb == 0:
         raise TrellisError(-1, lib().trellis_last_error().decode() or f"n_experts={experts} not in 1..2048")
@@ -1167,9 +1180,10 @@ def trellis_moe_gather(x: torch.Tensor, order: torch.Tensor, per: int, out: Opti
     x_row, e = _f8_rows(x, "x", x.dtype), x.element_size()
     _kv4_int(order, "order", x.device)
     tokens, n = x.shape
-    out = _out2(out, order.numel(), n, x.device, x.dtype)
+    rows = _i31(order.numel(), "entries of order")
+    out = _out2(out, rows, n, x.device, x.dtype)
     ws = _f8_ws(ws, _moe_rows_bytes(), x.device)
-    _check(lib().trellis_moe_gather(x.data_ptr(), x_row * e, tokens, n * e, order.data_ptr(), order.numel(), per,
+    _check(lib().trellis_moe_gather(x.data_ptr(), x_row * e, tokens, n * e, order.data_ptr(), rows, _i31(per, "per"),
                                     out.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
     return out
 

@@ -518,3 +518,28 @@ def test_gemm_in_a_graph_and_on_streams(m):
             assert torch.equal(a, y) and torch.equal(b, z)
         check_product(y, q2, s2, L.w, L.scale, "fp16")
     assert tb.error_word() == 0 and tb.error_word(ws) == 0
+
+
+@pytest.mark.parametrize("m", [20, 1100])
+def test_rows_past_4_gib(m):
+    """Rows whose strides carry them past 2^32 bytes: read and written where they are."""
+    log_case(f"f8 rows past 4 GiB m={m}")
+    g = torch.Generator().manual_seed(m)
+    n, k = 272, 400
+    stride = (2 ** 32 // (m - 2) // 16 + 1) * 16
+    L, E = make_matrix(n, k, g), make_matrix(n, k, g, 2)
+    q, s = make_rows(m, k, g)
+    far = torch.empty((m, stride), dtype=torch.float8_e4m3fn, device="cuda")[:, :k]
+    far.copy_(q)
+    out = torch.empty((m, stride // 2), dtype=torch.float16, device="cuda")[:, :n]
+    tb.trellis_f8_gemm(L, far, s, out=out)
+    assert torch.equal(out, tb.trellis_f8_gemm(L, q, s))
+    off = ints([0, m // 2, m])
+    tb.trellis_f8_moe_gemm(E, far, s, off, out=out)
+    assert torch.equal(out, tb.trellis_f8_moe_gemm(E, q, s, off))
+    x = out[:, :256]
+    for a, b in ((tb.trellis_f8_norm(x, None, 1e-6), tb.trellis_f8_norm(x.contiguous(), None, 1e-6)),
+                 (tb.trellis_f8_silu_mul(x), tb.trellis_f8_silu_mul(x.contiguous()))):
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+    order = ints([m - 1, 0, m - 2])
+    assert torch.equal(tb.trellis_moe_gather(x, order, 1), x[order.long()])

@@ -241,3 +241,58 @@ def test_routed_expert_step(dtype, tokens, top, experts, hidden, inter, gain):
         torch.cuda.synchronize()
         assert torch.equal(cap, step(x, res, gamma, ids, w, up, down, top)[0])
     assert tb.error_word() == 0
+
+
+def test_rows_past_4_gib():
+    log_case("moe rows past 4 GiB")
+    rows, n, tokens, top = 2 ** 21 + 5, 1024, 3, 4
+    g = torch.Generator().manual_seed(0)
+    y = torch.empty((rows, n), dtype=torch.float16, device="cuda")
+    inv = ints([rows - 1 - i for i in range(tokens * top)]).view(tokens, top)
+    few, w = torch.randn((tokens * top, n), generator=g).half().cuda(), torch.rand((tokens, top), generator=g).cuda()
+    d = torch.randn((tokens, n), generator=g).half().cuda()
+    y[rows - tokens * top:] = few
+    back = (tokens * top - 1 - torch.arange(tokens * top, dtype=torch.int32)).view(tokens, top).cuda()
+    assert torch.equal(tb.trellis_moe_combine(y, inv, w), tb.trellis_moe_combine(few, back, w))
+    want, dw = tb.trellis_moe_combine_grad(d, few, back, w)
+    got, dv = tb.trellis_moe_combine_grad(d, y, inv, w, out=y)
+    assert got is y and torch.equal(y[rows - tokens * top:], want) and torch.equal(dv, dw)
+    order = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    order[rows - 2:] = ints([2, 1])
+    tb.trellis_moe_gather(d, order, 1, out=y)
+    assert torch.equal(y[rows - 2:], d[[2, 1]]) and torch.equal(y[rows - tokens * top:rows - 2], want[:-2])
+    assert tb.error_word() == 0
+
+
+@pytest.mark.parametrize("tokens", [40, 9000])
+def test_routing_and_its_gradients_in_a_graph(tokens):
+    """Captured with a workspace of its own and replayed with other routings (9000 tokens: the sort's
+    three launches), between eager calls."""
+    log_case(f"moe routing graph tokens={tokens}")
+    g = torch.Generator().manual_seed(tokens)
+    top, experts, n = 8, 64, 136
+    x, d = (torch.randn((tokens, n), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w, ids = torch.rand((tokens, top), generator=g).cuda(), routing(tokens, top, experts, g, 0.8)
+    xs, dy = (torch.zeros((tokens * top, n), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def run(ws=None):
+        xs.zero_()
+        dy.zero_()
+        off, order, inv = tb.trellis_moe_sort(ids, experts, ws=ws)
+        tb.trellis_moe_gather(x, order, top, out=xs, ws=ws)
+        out = tb.trellis_moe_combine(xs, inv, w, add=x, ws=ws)
+        _, dw = tb.trellis_moe_combine_grad(d, xs, inv, w, out=dy, ws=ws)
+        return off, order, inv, out, dw, tb.trellis_moe_combine(dy, inv, ws=ws)
+
+    run()
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(ws)
+    for _ in range(4):
+        ids.copy_(routing(tokens, top, experts, g, 0.8))
+        graph.replay()
+        kept = [t.clone() for t in got] + [xs.clone(), dy.clone()]
+        assert all(torch.equal(a, b) for a, b in zip(kept, list(run()) + [xs, dy]))
+    assert tb.error_word() == 0 and tb.error_word(ws) == 0

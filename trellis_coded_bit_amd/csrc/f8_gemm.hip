@@ -164,12 +164,21 @@ __device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
 // Few rows: the matrix streams through once, and its bytes bound the kernel.
 // ---------------------------------------------------------------------------------------
 
-// A wave's place for one block: 16 NT matrix rows, 8 XC tokens, their scales.
+// A wave's place for one block: 16 NT matrix rows and their scale, 8 XC tokens.
 template <int XC, int NT>
 struct NarrowStage {
-  static constexpr int copies = 2 * NT + XC + 2;
+  static constexpr int copies = 2 * NT + XC + 1;
   alignas(16) char w[NT * 2048], x[XC * 1024];
-  float sx[64], sw[64];
+  float sw[64];
+};
+
+// A wave's places, and its tokens' scales for eight blocks, two eights in turn: [token][block], a copy
+// eight tokens.  (One block's scales are a line a token, as many as its codes: 37 rows by 5120 x 6144
+// took 13.4 us so and take 12.6, 64 rows 17.5 and 15.3, in no cache.)
+template <int XC, int NT, int D>
+struct NarrowWave {
+  NarrowStage<XC, NT> ring[D];
+  float sx[2][XC * 64];
 };
 
 // A workgroup takes 16 NT matrix rows by 8 XC tokens; its waves take the blocks in turn, and their sums
@@ -180,28 +189,39 @@ struct NarrowStage {
 // matrix is in no cache), 37 tokens over 5120 x 6144 9.6 (tokens in sixteens: 10.7), 33 tokens' 264
 // entries over 256 experts' 4096 x 6144 605 to 640.
 template <bool BF, int XC, int NT, int D>
-__global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
+__global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps, int whole, int rest) {
   using Stage = NarrowStage<XC, NT>;
+  using Wave = NarrowWave<XC, NT, D>;
   constexpr int MF = (XC + 1) / 2;  // tiles of 16 tokens (of an odd XC the last has its eight twice)
   extern __shared__ char raw[];
   const trellis_f8_linear &L = p.g.L;
   const int K = L.in_features, N = L.out_features, nb = (N + 127) / 128, kb = p.kb;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int i = lane & 15;
-  Stage *ring = reinterpret_cast<Stage *>(raw) + wave * D;
-  floatx4 *sums = reinterpret_cast<floatx4 *>(raw + waves * D * sizeof(Stage));  // [waves][MF][NT][64]
+  Wave &mine = reinterpret_cast<Wave *>(raw)[wave];
+  floatx4 *sums = reinterpret_cast<floatx4 *>(raw + waves * sizeof(Wave));  // [waves][MF][NT][64]
   const int groups = (p.col_tiles + reps - 1) / reps;
   const int rt = blockIdx.x / groups, c0 = (blockIdx.x - rt * groups) * reps, c1 = min(c0 + reps, p.col_tiles);
   const bool checks = rt == p.row_tiles;  // (the last of a grouped call: the offsets, to their end)
   const RowTiles tiles = find_tiles<8>(p, checks ? INT_MAX : rt, checks);
   if (tiles.e < 0) return;
   const RowTile t = tiles[rt - tiles.first];
-  uint32_t xat[XC];  // of the lane's tokens behind q, in 16 bytes
+  int src[XC];  // rows of q of the lane's tokens
+  uint32_t xat[XC];  // and where they begin, in 16 bytes
 #pragma unroll
-  for (int j = 0; j < XC; ++j)
-    xat[j] = (uint32_t)((uint64_t)max(source_row(p, min(t.row + 8 * j + (lane >> 3), t.end - 1)), 0) * (uint64_t)(p.g.q_row >> 4));
-  const float *sx = p.g.s + (int64_t)max(source_row(p, min(t.row + min(lane, 16 * MF - 1), t.end - 1)), 0) * p.g.s_row;
-
+  for (int j = 0; j < XC; ++j) {
+    src[j] = max(source_row(p, min(t.row + 8 * j + (lane >> 3), t.end - 1)), 0);
+    xat[j] = (uint32_t)((uint64_t)src[j] * (uint64_t)(p.g.q_row >> 4));
+  }
+  const int turns = whole + (wave < rest), all = turns * (c1 - c0);  // of this wave: a tile's, all tiles'
+  int turn = 0;
+  auto copy_scales = [&](int eight) {
+    // (after a tile's last turn its first one follows again, for the next tile)
+    const int of = 8 * eight + (lane & 7), u = reps == 1 ? min(of, turns - 1) : of % turns;
+#pragma unroll
+    for (int j = 0; j < XC; ++j)
+      copy4(p.g.s + (int64_t)src[j] * p.g.s_row + wave + waves * u, mine.sx[eight & 1] + 64 * j);
+  };
   // what is copied next
   int ct = c0, cb = wave, slot = 0;
   const char *w;
@@ -217,12 +237,11 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
   auto copy = [&]() {
     const int b = min(cb, kb - 1);
     const uint32_t u = copy_chunk(lane, b, K);
-    Stage &o = ring[slot];
+    Stage &o = mine.ring[slot];
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) copy16(w + ((uint64_t)(wat[j] + u) << 4), o.w + 1024 * j);
 #pragma unroll
     for (int j = 0; j < XC; ++j) copy16(p.g.q + ((uint64_t)(xat[j] + u) << 4), o.x + 1024 * j);
-    copy4(sx + b, o.sx);
     copy4(sw + b, o.sw);
     slot = slot + 1 == D ? 0 : slot + 1;
     cb += waves;
@@ -233,8 +252,10 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
     }
   };
   aim();
+  copy();
+  copy_scales(0);  // (arrived with the first block)
 #pragma unroll
-  for (int d = 0; d + 1 < D; ++d) copy();
+  for (int d = 1; d + 1 < D; ++d) copy();
   int now = 0;
   for (int c = c0; c < c1; ++c) {
     const int n0 = c * 16 * NT;
@@ -247,7 +268,10 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
     for (int b = wave; b < kb; b += waves) {
       copy();
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * Stage::copies) : "memory");
-      const Stage &o = ring[now];
+      if ((turn & 7) == 4 && turn + 4 < all) copy_scales((turn >> 3) + 1);
+      const float *sx = mine.sx[(turn >> 3) & 1] + (turn & 7);
+      ++turn;
+      const Stage &o = mine.ring[now];
       now = now + 1 == D ? 0 : now + 1;
       intx8 a[NT], x[MF];
       float f[MF];
@@ -256,7 +280,7 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps) {
 #pragma unroll
       for (int m = 0; m < MF; ++m) x[m] = operand(o.x + (16 * m + (2 * m + 1 < XC ? i : i & 7)) * 128, lane);
 #pragma unroll
-      for (int m = 0; m < MF; ++m) f[m] = o.sx[16 * m + i] * o.sw[0];
+      for (int m = 0; m < MF; ++m) f[m] = sx[128 * m + 8 * (2 * m + 1 < XC ? i : i & 7)] * o.sw[0];
       if (K - 128 * b < 128)
 #pragma unroll
         for (int n = 0; n < NT; ++n) clear_behind(a[n], lane, K - 128 * b);
@@ -316,7 +340,7 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   // (in long calls a workgroup's first copies and its look at the offsets serve four tiles: a decode
   // batch's experts 678 -> 632 us)
   const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
-  const int each = D * (int)sizeof(NarrowStage<XC, NT>) + (XC + 1) / 2 * NT * 1024;
+  const int each = (int)sizeof(NarrowWave<XC, NT, D>) + (XC + 1) / 2 * NT * 1024;
   // (few tiles of long rows: 4 tokens over 256 x 16384 8.1 us with four waves, 7.3 with eight; elsewhere
   // within 0.2)
   int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
@@ -328,7 +352,7 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  narrow_kernel<BF, XC, NT, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps);
+  narrow_kernel<BF, XC, NT, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps, p.kb / waves, p.kb % waves);
   return hipGetLastError();
 }
 

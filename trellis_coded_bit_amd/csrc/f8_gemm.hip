@@ -187,7 +187,9 @@ struct NarrowWave {
 // behind the last it copies that one again, so that the number of copies under way is a constant.
 // One token over 17408 x 5120 takes 15.4 us (5.8 TB/s of the 6.4 that a stream reads at; 18 where the
 // matrix is in no cache), 37 tokens over 5120 x 6144 9.6 (tokens in sixteens: 10.7), 33 tokens' 264
-// entries over 256 experts' 4096 x 6144 605 to 640.
+// entries over 256 experts' 4096 x 6144 605 to 640.  With more tokens it is what a CU copies: of 64 by
+// 5120 x 6144, 15.3 us in no cache, a copy of the kernel that reads the same few token lines takes 11.8,
+// and one with five or six waves in flight instead of four no less.
 template <bool BF, int XC, int NT, int D>
 __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps, int whole, int rest) {
   using Stage = NarrowStage<XC, NT>;
@@ -341,8 +343,8 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   // batch's experts 678 -> 632 us)
   const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
   const int each = (int)sizeof(NarrowWave<XC, NT, D>) + (XC + 1) / 2 * NT * 1024;
-  // (few tiles of long rows: 4 tokens over 256 x 16384 8.1 us with four waves, 7.3 with eight; elsewhere
-  // within 0.2)
+  // (few tiles: 4 tokens by 256 x 16384 9.4 us with four waves, 7.5 with eight, 1 by 2048 x 8192 6.9 and
+  // 6.2; elsewhere within 0.6)
   int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
   if (waves > p.kb) waves = p.kb;
   const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps) + (p.g.offsets ? 1 : 0);
@@ -366,10 +368,10 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
   // 6144: 8.5 -> 12.2, 48 x 4096 x 6144: 9.8 -> 7.8).
   while (!p.g.offsets && xc > 1 && (p.g.rows + 8 * xc - 1) / (8 * xc) * cols < 128) xc = (xc + 1) / 2;
   // Two tiles of matrix rows a workgroup share what is read of the tokens.  Where that is little, one
-  // tile each, unless two come to a workgroup a CU or the tiles are many (us of one | two, K = 5120 to
-  // 8192: 16 rows of 2048 7.7 | 8.9, of 5120 12.2 | 10.3, of 8192 11.9 | 11.0, of 9216 15.0 | 17.2, of
-  // 17408 24.1 | 25.6, of 69632 90 | 80; one row 7.9 | 8.7, 9.3 | 9.4, 9.9 | 10.2, 12.0 | 13.7, 18.2 |
-  // 19.9, 65 | 59).
+  // tile each, unless two come to a workgroup a CU or the tiles are many (us of one | two, in a graph,
+  // matrices in no cache: 1 row by 512 x 8192 5.5 | 6.3, 2048 x 8192 6.2 | 7.9, 9216 x 5120 12.2 | 13.7,
+  // 17408 x 5120 18.2 | 19.9, 69632 x 5120 65 | 59; 16 rows by 2048 x 8192 7.3 | 8.6, 5120 x 5120 11.1 |
+  // 9.7, 8192 x 5120 11.8 | 10.5, 9216 x 5120 14.8 | 16.6, 69632 x 5120 87 | 79).
   const long long two = (p.g.rows + 15) / 16 * cols;
   const bool one = xc <= 2 && two < 1024 && (two < 128 || two > 256);
   switch (xc) {
@@ -721,8 +723,8 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
 // block of 64 tokens by 32 matrix rows over the whole card; a wide workgroup 0.45 + 0.156 a block for
 // every 32 of its tokens, and 3 a tile; a split's sums are written and read at 5 TB/s by one launch
 // more.  Matrices in no cache, narrow | wide, blocks whole | wide, blocks shared: 5120 x 6144 with 32
-// rows 12.4 | 56 | 18, 64 rows 17.7 | 57 | 20, 128 rows 25 | 54 | 23, 256 rows 36 | 52 | 29, 512 rows
-// 58 | 50 | 37; 17408 x 5120 with 32 rows 31 | - | 30, 64 rows 43 | 54 | 32, 128 rows 60 | 53 | 39.
+// rows 12.3 | 56 | 18, 64 rows 16.0 | 57 | 20, 128 rows 23 | 54 | 23, 256 rows 34 | 52 | 29, 512 rows
+// 54 | 50 | 37; 17408 x 5120 with 32 rows 30 | 53 | 29, 64 rows 40 | 54 | 32, 128 rows 57 | 53 | 40.
 struct Plan {
   bool narrow;
   int tile_rows, splits;

@@ -543,3 +543,20 @@ def test_rows_past_4_gib(m):
         assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
     order = ints([m - 1, 0, m - 2])
     assert torch.equal(tb.trellis_moe_gather(x, order, 1), x[order.long()])
+
+
+def test_moe_gemm_of_very_many_tiles():
+    """More tiles than a launch has workgroups: each takes a row of them."""
+    log_case("f8 moe_gemm very many tiles")
+    experts, n, k, each = 65536, 4112, 16, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.randint(0, 0x7F, (experts, n, k), dtype=torch.uint8, device="cuda", generator=g).view(torch.float8_e4m3fn)
+    L = tb.F8Linear(w, torch.rand((experts, n // 128 + 1, 1), device="cuda", generator=g))
+    q = torch.randint(0, 0x7F, (experts * each, k), dtype=torch.uint8, device="cuda", generator=g).view(torch.float8_e4m3fn)
+    s = torch.rand((experts * each, 1), device="cuda", generator=g) / 256
+    off = torch.arange(0, experts * each + 1, each, dtype=torch.int32, device="cuda")
+    y = tb.trellis_f8_moe_gemm(L, q, s, off, dtype=torch.bfloat16)
+    for e in (0, 1, 31337, experts - 1):
+        at = slice(e * each, (e + 1) * each)
+        check_product(y[at], q[at], s[at], L.w[e], L.scale[e], "bf16")
+    assert tb.error_word() == 0

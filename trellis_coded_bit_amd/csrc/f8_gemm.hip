@@ -396,8 +396,8 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
 // time, and fmas (half as many cycles as the products), operand reads and copies (together half of
 // shared memory's cycles, without conflicts) do not all fit beside it with two waves a SIMD; a third
 // would not have the registers for its sums, which vector instructions must reach.
-// 2048 x 5120 by 17408: 186 to 190 us (1950 TFLOP/s; two turns of tiles and one of an eighth of them,
-// cut as three turns of 224 tokens).  64 experts with 32768 rows, 4096 x 6144: 910 to 930 us (1790).
+// 2048 rows by 17408 x 5120: 186 to 190 us (1950 TFLOP/s; 680 tiles of up to 224 tokens, 2.66 turns in
+// the time of 3).  64 experts' 32768 rows by 4096 x 6144: 910 to 940 us (1790).
 // ---------------------------------------------------------------------------------------
 
 constexpr int kWideThreads = 512, kWideOut = 256, kWideRows = 256;

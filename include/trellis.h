@@ -32,7 +32,8 @@
  *     header whose first uint32 is the ERROR WORD, and the next 64 KiB hold the small-batch
  *     products' counters, which each call leaves at zero again and no entry point leaves
  *     dirty.  So one zero-filled buffer, large enough for the largest request, serves any
- *     number of back-to-back calls of every entry point, in any order, on ONE stream.
+ *     number of back-to-back calls of every entry point, in any order, on ONE stream, from
+ *     any number of host threads: a call's launches reach the stream together.
  *     Calls that overlap in time (several streams) need separate workspaces.
  *   - The error word is sticky: kernels only OR bits into it (1: a routed id out of range
  *     or a table entry with an invalid K/cb was skipped; 2: a prefill workgroup's bounded

@@ -39,6 +39,7 @@ int abi_hip_status(hipError_t e, const char *what) {
 using trellis::abi_clear;
 using trellis::abi_fail;
 using trellis::abi_hip_status;
+using trellis::WorkspaceTurn;
 
 namespace {
 
@@ -221,6 +222,7 @@ int trellis_gemv_list(const trellis_gemv_item *items, int n, int B, void *ws, si
                 trellis::kMaxFinishGroups);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return abi_fail(TRELLIS_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_gemv(a, ws, ws_bytes, as_stream(stream)), "trellis_gemv launch");
 }
 
@@ -256,6 +258,7 @@ int trellis_gemm(const trellis_linear *L, const uint16_t *x, int M, uint16_t *y,
   const size_t need = trellis::gemm_workspace_bytes(L->in_features, L->out_features, M);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return abi_fail(TRELLIS_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_gemm(*L, x, M, y, ws, ws_bytes, as_stream(stream)),
                     "trellis_gemm launch");
 }
@@ -274,6 +277,7 @@ int trellis_gemm_fp8(const trellis_linear *L, const uint16_t *x, int M, uint16_t
   const size_t need = trellis::gemm_fp8_workspace_bytes(L->in_features, L->out_features, M);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return abi_fail(TRELLIS_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_gemm_fp8(*L, x, M, y, ws, ws_bytes, as_stream(stream)),
                     "trellis_gemm_fp8 launch");
 }
@@ -328,6 +332,7 @@ int trellis_moe_gemv(const trellis_linear *experts, int E, const int32_t *routed
   a.shared_r = shared_r;
   a.shared_s = shared_s;
   a.shared_side = shared_side;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_gemv(a, ws, ws_bytes, as_stream(stream)), "trellis_moe_gemv launch");
 }
 
@@ -380,6 +385,7 @@ int trellis_moe_mlp(const trellis_linear *gate_up, const trellis_linear *down, i
   m.s_hidden_out = s_hidden_out;
   m.act = act;
   m.y = y;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_moe_mlp(m, ws, ws_bytes, as_stream(stream)), "trellis_moe_mlp launch");
 }
 
@@ -401,6 +407,7 @@ int trellis_encode_tiles(const float *targets, int n_tiles, int K, int cb, int16
   const size_t need = trellis::encode_workspace_bytes(n_tiles);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return abi_fail(TRELLIS_EWORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_encode_tiles(targets, n_tiles, K, cb, code, states, ws, ws_bytes,
                                                  as_stream(stream)),
                     "trellis_encode_tiles launch");

@@ -15,6 +15,7 @@
 using trellis::abi_clear;
 using trellis::abi_fail;
 using trellis::abi_hip_status;
+using trellis::WorkspaceTurn;
 
 namespace {
 
@@ -129,6 +130,7 @@ int product(trellis::F8Gemm &a, int n_q, const char *what, void *ws, size_t ws_b
                          {"order", a.order, a.order ? (size_t)4 * a.rows : 0}})))
     return st;
   if ((st = check_ws(ws, ws_bytes, trellis::f8_gemm_workspace_bytes(a.L, a.rows, a.offsets != nullptr)))) return st;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_f8_gemm(a, ws, as_stream(stream)), what);
 }
 
@@ -269,6 +271,7 @@ int trellis_moe_sort(const int32_t *ids, int tokens, int top, int n_experts, int
                         {{"ids", ids, entries}})))
     return st;
   if ((st = check_ws(ws, ws_bytes, trellis::moe_sort_workspace_bytes(tokens, top, n_experts)))) return st;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_moe_sort(ids, tokens, top, n_experts, offsets, order, inverse, ws, as_stream(stream)),
                         "trellis_moe_sort launch");
 }

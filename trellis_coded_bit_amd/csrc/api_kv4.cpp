@@ -12,6 +12,7 @@
 using trellis::abi_clear;
 using trellis::abi_fail;
 using trellis::abi_hip_status;
+using trellis::WorkspaceTurn;
 
 namespace {
 
@@ -195,6 +196,7 @@ int trellis_kv4_attn(const trellis_kv4_cache *c, int layer, const trellis_kv4_ba
   a.scale = scale;
   a.y = y;
   a.lse = lse;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_kv4_attn(a, ws, as_stream(stream)), "trellis_kv4_attn launch");
 }
 
@@ -211,6 +213,7 @@ int trellis_kv4_reserve(const trellis_kv4_cache *c, int32_t *table, int32_t *len
   trellis::Kv4Pages p = pages_of(c, table, lens, n_slots, max_pages, ref, n);
   p.dst = slots;
   p.add = add;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_kv4_reserve(p, ws, as_stream(stream)), "trellis_kv4_reserve launch");
 }
 
@@ -226,6 +229,7 @@ int trellis_kv4_fork(const trellis_kv4_cache *c, int32_t *table, int32_t *lens, 
   trellis::Kv4Pages p = pages_of(c, table, lens, n_slots, max_pages, ref, n);
   p.src = src;
   p.dst = dst;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_kv4_fork(p, ws, as_stream(stream)), "trellis_kv4_fork launch");
 }
 
@@ -247,6 +251,7 @@ int trellis_kv4_compact(const trellis_kv4_cache *c, int32_t *table, int32_t *len
   p.keep = keep;
   p.keep_cu = keep_cu;
   p.n_keep = n_keep;
+  const WorkspaceTurn turn(ws);
   return abi_hip_status(trellis::launch_kv4_compact(p, ws, as_stream(stream)), "trellis_kv4_compact launch");
 }
 

@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 import threading
+import time
 
 import pytest
 import torch
@@ -28,6 +29,61 @@ def test_calls_with_one_workspace_take_turns(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def _host_workspaces(monkeypatch):
+    for name in ("_ws", "_ws_outgrown", "_ws_held"):
+        monkeypatch.setattr(tb, name, {}, raising=False)
+    monkeypatch.setattr(tb, "_stream", lambda: 7)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return torch.device("cpu", 0)
+
+
+def test_errors_of_a_call_whose_workspace_is_outgrown_meanwhile(monkeypatch):
+    """A thread looks its workspace up, another one's call replaces it, then the first one's kernel
+    sets its error word: it is known, until it is cleared, and the buffer does not stay for good."""
+    cpu = _host_workspaces(monkeypatch)
+    a = tb.workspace(1000, cpu)
+    b = tb.workspace(2000, cpu)
+    a[:4].view(torch.int32)[0] = 8
+    assert b is not a and tb.error_word() == 8
+    del a
+    c = tb.workspace(3000, cpu)  # (b is held now)
+    assert tb.error_word() == 8 and int(c[:4].view(torch.int32)) == 8 and sum(map(len, tb._ws_held.values())) == 1
+    b[:4].view(torch.int32)[0] = 1
+    del b, c
+    d = tb.workspace(4000, cpu)
+    assert tb.error_word() == 9 and int(d[:4].view(torch.int32)) == 9 and not tb._ws_held
+    tb.clear_error_word()
+    assert tb.error_word() == 0
+
+
+@pytest.mark.parametrize("first", [0, 500])
+def test_threads_that_need_a_workspace_at_once_get_the_same(monkeypatch, first):
+    cpu = _host_workspaces(monkeypatch)
+    if first:
+        tb.workspace(first, cpu)
+    zeros, got, start = torch.zeros, [], threading.Barrier(4)
+
+    def slow(*args, **kw):
+        w = zeros(*args, **kw)
+        time.sleep(0.05)
+        return w
+
+    monkeypatch.setattr(torch, "zeros", slow)
+
+    def call():
+        start.wait()
+        got.append(tb.workspace(1000, cpu))
+
+    threads = [threading.Thread(target=call) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4 and all(w is got[0] for w in got)
+    got[2][:4].view(torch.int32)[0] = 1
+    assert tb.error_word() == 1
 
 
 @pytest.mark.gpu

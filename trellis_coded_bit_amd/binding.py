@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import re
+import sys
 import threading
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -202,24 +203,49 @@ _ws: Dict[Tuple[int, int], torch.Tensor] = {}
 # Buffers that a capture outgrew: nothing of them is recorded into the graph, and their error words
 # count until they are cleared.
 _ws_outgrown: Dict[Tuple[int, int], List[torch.Tensor]] = {}
+# Buffers outgrown while a call of another thread (or the program) held them: what such a call is yet
+# to set in an error word counts too.
+_ws_held: Dict[Tuple[int, int], List[torch.Tensor]] = {}
+_ws_lock = threading.Lock()
+
+
+def _ws_replace(key: Tuple[int, int], w: torch.Tensor, old: List[torch.Tensor]) -> None:
+    """w takes the place of old buffers; the error words of those that nobody else holds go on in it.
+    (A call holds its workspace until it has reached the stream, and the fill that adds the word
+    comes behind it there.)"""
+    _ws[key] = w
+    old += _ws_held.pop(key, [])
+    held = []
+    while old:
+        o = old.pop()
+        if sys.getrefcount(o) > 2:
+            held.append(o)
+        else:
+            w[:4].bitwise_or_(o[:4])
+        del o
+    if held:
+        _ws_held[key] = held
 
 
 def workspace(nbytes: int, device: torch.device, op: int = 0) -> torch.Tensor:
     """One zero-filled workspace per (device, stream), grown on demand.  Every entry point
     leaves the reserved region at the start of a workspace as it found it, so all of them
-    share one buffer (``op`` is accepted for compatibility and ignored).  Its error word goes on
-    with it when it grows.  (A graph should be given a workspace of the program's own: one made
-    during a capture is cleared by every replay.)"""
+    share one buffer (``op`` is accepted for compatibility and ignored), host threads on one
+    stream too.  Its error word goes on with it when it grows.  (A graph should be given a
+    workspace of the program's own: one made during a capture is cleared by every replay.)"""
     key = (device.index if device.index is not None else torch.cuda.current_device(), _stream())
     w = _ws.get(key)
     if w is None or w.numel() < nbytes:
-        old, w = w, torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        if old is not None:
-            if torch.cuda.is_current_stream_capturing():
-                _ws_outgrown.setdefault(key, []).append(old)
+        del w
+        with _ws_lock:
+            if key in _ws and _ws[key].numel() >= nbytes:  # (another thread's)
+                return _ws[key]
+            w = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            if key in _ws and torch.cuda.is_current_stream_capturing():
+                _ws_outgrown.setdefault(key, []).append(_ws[key])
+                _ws[key] = w
             else:
-                w[:4].copy_(old[:4])
-        _ws[key] = w
+                _ws_replace(key, w, [_ws.pop(key)] if key in _ws else [])
     return w
 
 
@@ -523,7 +549,8 @@ def _error_words(ws: Optional[torch.Tensor], device) -> List[torch.Tensor]:
     if ws is not None:
         return [ws]
     key = (torch.device(device).index or 0, _stream())
-    return ([_ws[key]] if key in _ws else []) + _ws_outgrown.get(key, [])
+    with _ws_lock:
+        return ([_ws[key]] if key in _ws else []) + _ws_outgrown.get(key, []) + _ws_held.get(key, [])
 
 
 def error_word(ws: Optional[torch.Tensor] = None, device="cuda") -> int:

@@ -40,6 +40,20 @@ def test_sort(tokens, top, experts, share):
     assert tb.error_word() == 0
 
 
+@pytest.mark.parametrize("experts", [1636, 1637, 1638, 1639, 2047])
+@pytest.mark.parametrize("tokens", [7, 16500])
+def test_sort_where_its_shared_memory_passes_64_kib(tokens, experts):
+    """Which takes an opt-in that every byte of the kernel's counts for."""
+    log_case(f"moe sort tokens={tokens} experts={experts}")
+    g = torch.Generator().manual_seed(tokens + experts)
+    ids = torch.randint(-1, experts, (tokens, 4), generator=g, dtype=torch.int32)
+    ids[0, 0], ids[-1, -1] = experts - 1, 0
+    off, order, inv = tb.trellis_moe_sort(ids.cuda(), experts)
+    ro, rr, ri, _ = FO.sort(ids.numpy(), experts)
+    assert np.array_equal(off.cpu().numpy(), ro) and np.array_equal(order.cpu().numpy(), rr) and np.array_equal(inv.cpu().numpy(), ri)
+    assert tb.error_word() == 0
+
+
 @pytest.mark.parametrize("tokens", [1, 500, 20000])
 def test_sort_of_one_expert_and_of_bad_ids(tokens):
     log_case(f"moe sort special tokens={tokens}")

@@ -72,8 +72,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
   extern __shared__ uint32_t lds[];
   uint32_t *before = lds;       // [E] of the id in earlier workgroups' entries, then its first position here
   uint32_t *after = before + E; // [E] of the id in the others
-  uint16_t *waves = reinterpret_cast<uint16_t *>(after + E);  // [16][E] of the id in this workgroup's waves
-  __shared__ uint32_t sums[kSortWaves];
+  uint32_t *sums = after + E;   // [16] the scan's, of each wave
+  uint16_t *waves = reinterpret_cast<uint16_t *>(sums + kSortWaves);  // [16][E] of the id in this workgroup's waves
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int first = blockIdx.x * kSortThreads;
   const int i = first + tid;
@@ -141,7 +141,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
   inverse[i] = pos;
 }
 
-size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves); }
+// All that sort_place_kernel has in shared memory.
+size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves) + 4 * kSortWaves; }
 
 // A workgroup a row, four words a thread under way.  16411 rows of 6144 16-bit channels (252 MB moved at
 // most, a token's row up to four times from a cache): 62 us; one word a thread: 78.

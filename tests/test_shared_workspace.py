@@ -86,6 +86,29 @@ def test_threads_that_need_a_workspace_at_once_get_the_same(monkeypatch, first):
     assert tb.error_word() == 1
 
 
+def _in_threads(calls, want, rounds):
+    """Every call from a thread of its own, all on the default stream: (call, wrong results or error)."""
+    errors, start = [], threading.Barrier(len(calls))
+
+    def loop(i):
+        try:
+            start.wait()
+            got = [calls[i]() for _ in range(rounds)]
+            torch.cuda.synchronize()
+            wrong = sum(not all(torch.equal(a, b) for a, b in zip(r, want[i])) for r in got)
+            if wrong:
+                errors.append((i, wrong))
+        except Exception as e:  # noqa: BLE001
+            errors.append((i, repr(e)))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return errors
+
+
 @pytest.mark.gpu
 def test_threads_on_one_stream():
     """Four threads on the default stream with its one workspace: products whose blocks are shared
@@ -95,31 +118,33 @@ def test_threads_on_one_stream():
     from test_gpu_route import routing
     log_case("threads on one stream")
     g = torch.Generator().manual_seed(0)
-    work = []
+    calls = []
     for i, (m, n, k) in enumerate(((70, 4099, 6160), (130, 1544, 16400), (200, 2051, 8208), (70, 2050, 16400))):
         L = make_matrix(n, k, g)
         q, s = make_rows(m, k, g)
         assert tb.trellis_f8_workspace_bytes(L, m) > tb.trellis_f8_workspace_bytes(L, 1)
-        work.append((L, q, s, routing(9000 + 1000 * i, 8, 40 + i, g, 0.9), 40 + i))
-    run = lambda w: (tb.trellis_f8_gemm(*w[:3]), *tb.trellis_moe_sort(w[3], w[4]))  # noqa: E731
-    want = [run(w) for w in work]
+        ids = routing(9000 + 1000 * i, 8, 40 + i, g, 0.9)
+        calls.append(lambda L=L, q=q, s=s, ids=ids, e=40 + i: (tb.trellis_f8_gemm(L, q, s), *tb.trellis_moe_sort(ids, e)))
+    want = [c() for c in calls]
     torch.cuda.synchronize()
-    errors, start = [], threading.Barrier(len(work))
+    assert not _in_threads(calls, want, 50) and tb.error_word() == 0
 
-    def loop(i):
-        try:
-            start.wait()
-            got = [run(work[i]) for _ in range(50)]
-            torch.cuda.synchronize()
-            wrong = sum(not all(torch.equal(a, b) for a, b in zip(r, want[i])) for r in got)
-            if wrong:
-                errors.append((i, wrong))
-        except Exception as e:  # noqa: BLE001
-            errors.append((i, repr(e)))
 
-    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(work))]
-    for t in threads:
-        t.start()
-    for t in threads:
-        t.join()
-    assert not errors and tb.error_word() == 0
+@pytest.mark.gpu
+def test_threads_at_one_kernel_with_more_and_less_shared_memory():
+    """Each launch has what it needs, whatever another thread's call of the same kernel asked for."""
+    from gpu_util import log_case
+    from test_gpu_f8 import make_matrix, make_rows
+    log_case("threads at one kernel")
+    g = torch.Generator().manual_seed(1)
+    calls = []
+    for experts in (1700, 2048):
+        ids = torch.randint(-1, experts, (500, 4), generator=g, dtype=torch.int32).cuda()
+        calls.append(lambda ids=ids, e=experts: tb.trellis_moe_sort(ids, e))
+    for n in (4096, 32768):  # (128 and 1024 tiles of 32 rows: eight waves, four)
+        L = make_matrix(n, 1024, g)
+        q, s = make_rows(3, 1024, g)
+        calls.append(lambda L=L, q=q, s=s: (tb.trellis_f8_gemm(L, q, s),))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    assert not _in_threads(calls, want, 200) and tb.error_word() == 0

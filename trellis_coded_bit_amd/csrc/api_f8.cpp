@@ -252,7 +252,7 @@ int trellis_f8_moe_gemm(const trellis_f8_linear *L, const uint8_t *q, int64_t q_
 
 size_t trellis_moe_sort_workspace_bytes(int tokens, int top, int n_experts) {
   abi_clear();
-  if (check_route(tokens, top) || n_experts < 1 || n_experts > 2048) return 0;
+  if (check_route(tokens, top) || n_experts < 1 || n_experts > trellis::kMoeExperts) return 0;
   return trellis::moe_sort_workspace_bytes(tokens, top, n_experts);
 }
 
@@ -263,7 +263,8 @@ int trellis_moe_sort(const int32_t *ids, int tokens, int top, int n_experts, int
   abi_clear();
   int st = check_route(tokens, top);
   if (st) return st;
-  if (n_experts < 1 || n_experts > 2048) return abi_fail(TRELLIS_EINVAL, "n_experts=%d not in 1..2048", n_experts);
+  if (n_experts < 1 || n_experts > trellis::kMoeExperts)
+    return abi_fail(TRELLIS_EINVAL, "n_experts=%d not in 1..%d", n_experts, trellis::kMoeExperts);
   if ((st = check_4("offsets", offsets))) return st;
   if (tokens > 0 && ((st = check_4("ids", ids)) || (st = check_4("order", order)) || (st = check_4("inverse", inverse)))) return st;
   const size_t entries = (size_t)4 * tokens * top;

@@ -22,6 +22,8 @@ namespace {
 
 typedef int intx8 __attribute__((ext_vector_type(8)));
 
+constexpr int kLds = 163840;  // bytes of shared memory of a CU
+
 struct GemmArgs {
   F8Gemm g;
   uint32_t *errword;
@@ -342,16 +344,18 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   // (in long calls a workgroup's first copies and its look at the offsets serve four tiles: a decode
   // batch's experts 678 -> 632 us)
   const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
-  const int each = (int)sizeof(NarrowWave<XC, NT, D>) + (XC + 1) / 2 * NT * 1024;
+  constexpr int each = (int)sizeof(NarrowWave<XC, NT, D>) + (XC + 1) / 2 * NT * 1024, most = (8 * each <= kLds ? 8 : 4) * each;
+  static_assert(most <= kLds, "four waves fit");
   // (few tiles: 4 tokens by 256 x 16384 9.4 us with four waves, 7.5 with eight, 1 by 2048 x 8192 6.9 and
   // 6.2; elsewhere within 0.6)
-  int waves = tiles < 256 && 8 * each <= 163840 ? 8 : 4;
+  int waves = tiles < 256 && most == 8 * each ? 8 : 4;
   if (waves > p.kb) waves = p.kb;
   const long long grid = (long long)p.row_tiles * ((p.col_tiles + reps - 1) / reps) + (p.g.offsets ? 1 : 0);
   const int lds = waves * each;
   if (lds > 65536) {
+    // (the most of any call: another thread's may be between this and its launch)
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(narrow_kernel<BF, XC, NT, D>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != hipSuccess) return e;
   }
   narrow_kernel<BF, XC, NT, D><<<(unsigned)grid, 64 * waves, lds, stream>>>(p, reps, p.kb / waves, p.kb % waves);

@@ -57,6 +57,7 @@ struct F8Gemm {
 size_t f8_gemm_workspace_bytes(const trellis_f8_linear &L, int rows, bool grouped);
 hipError_t launch_f8_gemm(const F8Gemm &a, void *ws, hipStream_t stream);
 
+constexpr int kMoeExperts = 2048;  // of a sort, at most
 size_t moe_sort_workspace_bytes(int tokens, int top, int n_experts);
 hipError_t launch_moe_sort(const int32_t *ids, int tokens, int top, int n_experts, int32_t *offsets, int32_t *order,
                            int32_t *inverse, void *ws, hipStream_t stream);

@@ -321,7 +321,9 @@ hipError_t launch_moe_sort(const int32_t *ids, int tokens, int top, int n_expert
   const size_t lds = sort_lds(n_experts);
   hipError_t e;
   if (lds > 65536) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void *>(sort_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    // (the most of any call: another thread's may be between this and its launch)
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(sort_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)sort_lds(kMoeExperts));
     if (e != hipSuccess) return e;
   }
   if (n > kSortOne) {

@@ -177,6 +177,49 @@ def test_silu_mul_of_special_values(dtype):
     assert abs(s[2, 0] * 448 / v[2, 0] - 1) < 2.0 ** -20 and abs(s[1, 1] * 448 / v[1, 200] - 1) < 2.0 ** -20
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_silu_mul_of_far_gates(dtype):
+    """Gates whose sigmoid is below f32's normal numbers, times numbers that are not small: a row is one
+    block of gates within 1 of each other.  Every result and scale that 16 bits and f32 hold is there."""
+    log_case(f"f8 silu_mul far gates {dtype}")
+    g = torch.Generator().manual_seed(11)
+    top = torch.arange(-60.0, -192.0, -0.75)[:, None]
+    gates = top - torch.rand((len(top), 128), generator=g)
+    big = torch.finfo(DT[dtype]).max
+    for size in (big, big ** 0.75, 1.0):
+        u = (torch.rand((len(top), 128), generator=g) - 0.5) * 2 * size
+        u[:, 5] = size
+        x = torch.cat((gates, u), 1).to(DT[dtype]).cuda()
+        y = torch.empty((len(top), 128), dtype=DT[dtype], device="cuda")
+        q, s = tb.trellis_f8_silu_mul(x, y=y)
+        v = FO.silu_mul(host(x))
+        _, rs = FO.quantize(v)
+        assert dtype == "fp16" or size < big or (rs > 0).sum() > 80
+        check_quantized(host(q), host(s), v, 2.0 ** -20, 2.0 ** -20)
+        check_rounded(host(y), v, dtype, 2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_silu_mul_of_far_gates_and_special_values(dtype):
+    log_case(f"f8 silu_mul far gates, special {dtype}")
+    inf, nan = float("inf"), float("nan")
+    gates = torch.tensor([-79.5, -80.5, -100, -186, -190, -300, -6e4, -inf, -100, nan, -100, -300, -85, 3.0, -inf, -100])
+    ups = torch.tensor([inf, inf, inf, -inf, inf, -inf, inf, 1.0, nan, 1.0, 0.0, 0.0, 1.0, 2.0, 0.0, -6e4])
+    x = torch.cat((gates.repeat_interleave(128), ups.repeat_interleave(128)))[None].to(DT[dtype]).cuda()
+    y = torch.empty((1, 16 * 128), dtype=DT[dtype], device="cuda")
+    q, s = tb.trellis_f8_silu_mul(x, y=y)
+    y, q, s = host(y).reshape(16, 128), host(q).reshape(16, 128), host(s)[0]
+    want = [-inf, -inf, -inf, inf, -inf, inf, -inf, nan, nan, nan, 0, 0, None, None, nan, None]
+    for i, w in enumerate(want):
+        if w is not None:
+            assert (np.isnan(y[i]) if w is nan else y[i] == w).all(), (i, y[i, 0])
+            assert (np.isnan(s[i]) if w else s[i] == 0) and (q[i] == 0).all(), (i, s[i])
+    v = FO.silu_mul(host(x)).reshape(16, 128)
+    live = [12, 13, 15]
+    check_rounded(y[live], v[live], dtype, 2.0 ** -20)
+    check_quantized(q[live], s[live, None], v[live], 2.0 ** -20, 2.0 ** -20)
+
+
 # ---------------------------------------------------------------------------------------
 # Products
 # ---------------------------------------------------------------------------------------

@@ -127,24 +127,53 @@ __global__ __launch_bounds__(1024) void norm_kernel(F8Norm a) {
   }
 }
 
-// 1 / (1 + e^-z) within about 2 ulp, in ten instructions (the library's exponential and division
-// take three times that, and bound the kernel: 46 us for 2048 x 17408).  e^-z = 2^t (1 + r ln 2)
-// with t = -z log2 e rounded and r what that lost; the reciprocal gets one Newton step where the
-// sum is finite.
-__device__ __forceinline__ float sigmoid(float z) {
+// e^-z 2^-less: e^-z = 2^t (1 + r ln 2) with t = -z log2 e rounded and r what that lost (so t is not to
+// be formed anew, unrounded, where less is subtracted).
+__device__ __forceinline__ float exp_neg(float z, float less) {
+#pragma clang fp contract(off)
   constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;  // log2 e - kLog2e
-  z = fminf(fmaxf(z, -200.f), 200.f);  // (0 and 1 from there on; a NaN's result is multiplied by it)
   const float t = -z * kLog2e;
-  const float r = fmaf(-z, kLog2e, -t) - z * kLog2eRest;
-  float e = __builtin_amdgcn_exp2f(t);
-  e = t < 128.f ? fmaf(e * 0.693147181f, r, e) : INFINITY;
-  const float d = 1.0f + e, q = __builtin_amdgcn_rcpf(d);
-  return d < INFINITY ? fmaf(fmaf(-d, q, 1.0f), q, q) : 0.f;
+  const float r = fmaf(-z, kLog2eRest, fmaf(-z, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t - less);
+  return fmaf(e * 0.693147181f, r, e);
+}
+
+// 1 / (1 + e^-z) within about 2 ulp for z >= kLowGate, in ten instructions (the library's exponential
+// and division take three times that, and bound the kernel: 46 us for 2048 x 17408).  The reciprocal
+// gets one Newton step.
+constexpr float kLowGate = -80.f;
+constexpr uint32_t kLowBitsF16 = 0xD500, kLowBitsBf16 = 0xC2A0;  // its bits
+__device__ __forceinline__ float sigmoid(float z) {
+  const float d = 1.0f + exp_neg(fminf(fmaxf(z, kLowGate), 200.f), 0.f);  // (1 from there on; a NaN's result is multiplied by it)
+  const float q = __builtin_amdgcn_rcpf(d);
+  return fmaf(fmaf(-d, q, 1.0f), q, q);
+}
+
+// z / (1 + e^-z) u for z below kLowGate, where the sigmoid leaves f32's normal numbers, but not its
+// product with a large u: 1 + e^-z is e^-z there, to 2^-115, and is formed without a factor of 2^144 that the
+// product in 64 bits gets back.  From z = -187 on the result is below 2^-134, half of the smallest
+// number that 16 bits hold, whatever u; it keeps its sign, and u = infinity stays one.
+__device__ __forceinline__ float silu_mul_low(float z, float u) {
+  const float d = exp_neg(fmaxf(z, -187.f), 144.f);
+  float q = __builtin_amdgcn_rcpf(d);
+  q = fmaf(fmaf(-d, q, 1.0f), q, q);
+  const double f = z < -187.f ? (double)(z - z) - 0x1p-300 : (double)z * (double)q * 0x1p-144;  // (-infinity: NaN)
+  return (float)(f * (double)u);
+}
+
+// The largest of eight 16-bit words as whole numbers.
+__device__ __forceinline__ uint32_t top_u16(const u32x4 &w) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = __builtin_bit_cast(u16x2, w[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i]));
+  return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
 // One chunk of eight channels a thread; the rows' blocks, each 16 threads, follow each other, two
 // blocks of a thread under way.  2048 x 17408 (179 MB): 34 us, 5.3 TB/s; its sigmoids and conversions
-// are about as long.
+// are about as long.  A wave that has a gate below kLowGate forms its blocks again (a choice between
+// the two for each channel took 38 us); it reads them again, which leaves the registers as they are.
 template <bool BF>
 __global__ __launch_bounds__(256) void silu_mul_kernel(F8Act a, int blocks, uint32_t items) {
   for (uint32_t first = blockIdx.x * 32; first < items; first += gridDim.x * 32) {
@@ -162,6 +191,7 @@ __global__ __launch_bounds__(256) void silu_mul_kernel(F8Act a, int blocks, uint
       gs[k] = ldg(reinterpret_cast<const u32x4 *>(p));
       us[k] = ldg(reinterpret_cast<const u32x4 *>(p + a.n));
     }
+    uint32_t far = 0;  // gates below kLowGate are above its bits
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float g[8], u[8];
@@ -170,6 +200,25 @@ __global__ __launch_bounds__(256) void silu_mul_kernel(F8Act a, int blocks, uint
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] *= g[i] * sigmoid(g[i]);
       put_block<BF>(a.out, u, 1.f, live[k], row[k], a.n, chunk[k]);
+      far = max(far, top_u16(gs[k]));
+    }
+    if (__any(far > (BF ? kLowBitsBf16 : kLowBitsF16))) {  // (hardly ever)
+#pragma clang loop unroll(disable)
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t it = first + 16 * k + (threadIdx.x >> 4);
+        const uint32_t r = min(it, items - 1) / (uint32_t)blocks;
+        const int c = (int)(min(it, items - 1) - r * blocks) * 16 + (threadIdx.x & 15);
+        const uint16_t *p = a.x + (size_t)r * a.x_row + 8 * (c * 8 < a.n ? c : 0);
+        float g[8], u[8];
+        f8_widen8<BF>(ldg(reinterpret_cast<const u32x4 *>(p)), g);
+        f8_widen8<BF>(ldg(reinterpret_cast<const u32x4 *>(p + a.n)), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[i] = g[i] < kLowGate ? silu_mul_low(g[i], u[i]) : u[i] * (g[i] * sigmoid(g[i]));
+          asm volatile("" : "+v"(u[i]));  // (not all at once: registers)
+        }
+        put_block<BF>(a.out, u, 1.f, it < items && c * 8 < a.n, r, a.n, c);
+      }
     }
   }
 }

@@ -73,6 +73,9 @@ size_t trellis_f8_moe_gemm_workspace_bytes(const trellis_f8_linear *L, int rows)
 /* y[m][o] = sum_b s[m][b] sw[o / 128][b] sum_{c in block b} q[m][c] w[o][c], summed in f32 but
  * for the matrix instruction's sums of eight neighbouring channels' products, whose terms are held
  * in steps of 2^-13 of the largest one's power of two.
+ * s sw is formed in f32: a product below its smallest normal number is held in steps of 2^-149, which
+ * moves a result by less than 2^-125 for each block; one above its largest is no part of the result
+ * (s and sw meet the block's sum one after the other there).
  * L    : HOST pointer, n_experts = 1.
  * q    : E4M3 [M][in] at row stride q_row (a multiple of 16), 16-byte aligned; s: f32 [M]
  *        [ceil(in / 128)] at row stride s_row.

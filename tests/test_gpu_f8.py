@@ -367,6 +367,97 @@ def test_gemm_of_shared_blocks(m, n, k):
     assert tb.error_word(ws) == 0
 
 
+def scaled_far(m, n, k, g):
+    """Rows, a matrix and scales whose products leave f32: rows of zeros (0, 4, ..), of one smallest code
+    where the product is 1e39 (1, 5, ..), of ordinary codes that stay off those blocks (2, 6, ..), of
+    codes that carry the result out of every type (3, 7, ..)."""
+    q, s = make_rows(m, k, g)
+    L = make_matrix(n, k, g)
+    w, sw, block = L.w, L.scale, slice(128, min(k, 256))
+    q = q.float()
+    s[:, 1] = 1e20
+    sw[:, 1] = 1e19
+    for kind in (0, 1, 2):
+        q[kind::4, block] = 0
+    q[0::4] = 0
+    q[1::4] = 0
+    q[1::4, 130] = 2.0 ** -9
+    q[3::4, block] = 300
+    w.view(torch.uint8)[:, 130] = torch.arange(n, device="cuda", dtype=torch.int64).remainder(7).to(torch.uint8)  # 0 .. 7 * 2^-9
+    w.view(torch.uint8)[:, 131] = 0x70  # (128: the rows of 300 overflow)
+    return L, q.to(torch.float8_e4m3fn), s
+
+
+def check_far(y, q, s, w, sw, dtype):
+    """A block's sum is off by up to 7 * 2^-13 of the eights' largest products (see above), whatever its
+    scales: where these carry that much out of the type, a sum that nearly cancels may leave the type on
+    either side, and only sums that are further from zero say on which."""
+    ref, _ = FO.product(host(q), host(s), host(w), host(sw))
+    y, kb, big = host(y), s.shape[1], torch.finfo(DT[dtype]).max
+    eights = 2.0 ** 80 * largest_of_eights(q, s * 2.0 ** -40, w, sw * 2.0 ** -40)  # (within f32)
+    extra = 7 * 2.0 ** -13 * (1 + 2.0 ** -10) * eights + 2 * (16 + kb + 32) * U * np.abs(ref)
+    over, within = np.abs(ref) - extra > 1.01 * big, np.abs(ref) + extra < big
+    assert over.any() and (y[over] == np.copysign(np.inf, ref[over])).all()
+    assert over[3::4].mean() > 0.5 and within[0::4].all() and within[2::4].all() and (dtype == "fp16" or within[1::4].all())
+    check_rounded(np.where(within, y, 0.0), np.where(within, ref, 0.0), dtype, 0.0, np.where(within, extra, 0.0))
+    assert (y[0::4] == 0).all() and np.isfinite(y[2::4]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 256), (4, 300, 272), (37, 257, 400), (64, 160, 1040), (100, 1032, 1296), (300, 513, 400), (300, 1032, 4112),
+                                   (1000, 300, 272)])
+def test_gemm_of_scales_whose_product_leaves_f32(dtype, m, n, k):
+    log_case(f"f8 gemm far scales {dtype} m={m} n={n} k={k}")
+    L, q, s = scaled_far(max(m, 4), n, k, torch.Generator().manual_seed(m + n))
+    y = tb.trellis_f8_gemm(L, q, s, dtype=DT[dtype])
+    check_far(y, q, s, L.w, L.scale, dtype)
+    if m == 1:  # a row of zeros alone, and the one of one code
+        assert (tb.trellis_f8_gemm(L, q[:1], s[:1], dtype=DT[dtype]) == 0).all()
+        assert torch.equal(tb.trellis_f8_gemm(L, q[1:2], s[1:2], dtype=DT[dtype]), y[1:2])
+    # results that need no second look have the bits that they have without one
+    s2 = s.clone()
+    s2[:, 1] = 1.0
+    z = tb.trellis_f8_gemm(tb.F8Linear(L.w, torch.ones_like(L.scale).where(torch.arange(L.scale.shape[1], device="cuda") == 1, L.scale)), q, s2,
+                           dtype=DT[dtype])
+    assert torch.equal(z[2::4], y[2::4])
+
+
+@pytest.mark.parametrize("each", [3, 40, 170])
+def test_moe_gemm_of_scales_whose_product_leaves_f32(each):
+    log_case(f"f8 moe_gemm far scales each={each}")
+    g = torch.Generator().manual_seed(each)
+    n, k = 264, 400
+    parts = [scaled_far(4 * each, n, k, g) for _ in range(3)]
+    E = tb.F8Linear(torch.stack([p[0].w.view(torch.uint8) for p in parts]).view(torch.float8_e4m3fn), torch.stack([p[0].scale for p in parts]))
+    q, s = torch.cat([p[1].view(torch.uint8) for p in parts]), torch.cat([p[2] for p in parts])
+    back = torch.randperm(len(q), generator=g).cuda()  # the rows of q in another order
+    at = torch.empty_like(back)
+    at[back] = torch.arange(len(q), device="cuda")
+    off = ints([0, 4 * each, 8 * each, 12 * each])
+    y = tb.trellis_f8_moe_gemm(E, q[back].view(torch.float8_e4m3fn), s[back], off, order=at.int(), per=1, dtype=torch.bfloat16)
+    for e, (L, qe, se) in enumerate(parts):
+        check_far(y[4 * each * e:4 * each * (e + 1)], qe, se, L.w, L.scale, "bf16")
+
+
+@pytest.mark.parametrize("m", [4, 300])
+def test_gemm_of_scales_whose_product_is_hardly_normal(m):
+    """Below the smallest normal number the product of two scales has steps of 2^-149: half of one, times
+    a block's sum of at most 128 * 448^2, is less than 2^-125."""
+    log_case(f"f8 gemm small scales m={m}")
+    g = torch.Generator().manual_seed(m)
+    n, k = 300, 656
+    L = make_matrix(n, k, g)
+    q, s = make_rows(m, k, g)
+    for a, b in ((-60.0, -66.0), (-60.0, -80.0), (-110.0, -20.0), (-126.0, -10.0), (0.0, -126.0)):
+        sx, sw = torch.full_like(s, 2.0 ** a) * (1 + torch.rand(s.shape, generator=g).cuda()), torch.full_like(L.scale, 2.0 ** b) * 1.5
+        y = tb.trellis_f8_gemm(tb.F8Linear(L.w, sw), q, sx, dtype=torch.bfloat16)
+        ref, mass = FO.product(host(q), host(sx), host(L.w), host(sw))
+        eights = 2.0 ** -100 * largest_of_eights(q, sx * 2.0 ** 50, L.w, sw * 2.0 ** 50)
+        extra = 7 * 2.0 ** -13 * (1 + 2.0 ** -10) * eights + 2 * (16 + 6 + 32) * U * mass
+        check_rounded(host(y), ref, "bf16", 0.0, extra + 6 * 2.0 ** -125)
+        assert (host(y) != 0).mean() > 0.9
+
+
 def test_gemm_overflow_is_infinite():
     log_case("f8 gemm overflow")
     L = tb.F8Linear(torch.full((16, 128), 448.0).to(torch.float8_e4m3fn).cuda(), torch.ones((1, 1), device="cuda"))

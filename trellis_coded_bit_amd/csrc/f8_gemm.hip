@@ -162,6 +162,82 @@ __device__ __forceinline__ void clear_behind(intx8 &w, int lane, int rest) {
   for (int j = 0; j < 8; ++j) w[j] = 16 * (g + 4 * (j >> 2)) < rest ? w[j] : 0;
 }
 
+// Whether one of a wave's sums is infinite or not a number (which a maximum is if an operand is).
+template <int MF, int NT>
+__device__ __forceinline__ bool any_far(const floatx4 (&acc)[MF][NT]) {
+  float top = 0.f;
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(acc[m][n][j]), fabsf(acc[m][n][j + 1])), top);
+  return __any(!(top < INFINITY));
+}
+
+// Whether a row's and the matrix's scale of one of a wave's blocks are numbers whose product is none in f32.
+template <int MF>
+__device__ __forceinline__ bool far_scales(const GemmArgs &p, const float *sw, const int (&src)[MF], int first, int step, int end) {
+  bool far = false;
+#pragma clang loop unroll(disable)
+  for (int b = first + step * ((int)(opaque_tid() & 63) >> 4); b < end; b += 4 * step) {  // (16 rows a tile, a quarter of the blocks a lane)
+    const float t = ldg(sw + b);
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      const float s = ldg(p.g.s + (int64_t)src[m] * p.g.s_row + b);
+      far |= fabsf(s) < INFINITY && fabsf(t) < INFINITY && !(fabsf(s * t) < INFINITY);
+    }
+  }
+  return __any(far);
+}
+
+// A wave's sums again, for what the kernels' loops do not: they multiply a block's two scales first,
+// and where that leaves f32 the block's sum may be zero or small and the result finite.  There the sum
+// meets one scale after the other (both are above 1, so the first product is infinite only if the
+// result is); every other block gives the same bits as in the loops.  w: the tile's first matrix row, n0;
+// row: the lane's first behind it; sw: the matrix's scales; src: rows of q; blocks first, first + step
+// ..., below end.  Done only where sums are not finite and the scales ask for it: the test of the sums
+// costs the wide kernel up to 0.3 % (experts' tiles; 1.2 % by a comparison for each sum), and a row that
+// stands for NaN no more than its noise (2048 x 17408 x 5120; 505 us for the 209 without the look at the scales).
+template <int MF, int NT>
+__device__ __forceinline__ void sums_again(const GemmArgs &p, const char *w, int n0, int row, const float *sw, const int (&src)[MF],
+                                           int first, int step, int end, floatx4 (&acc)[MF][NT]) {
+  const int K = p.g.L.in_features, lane = opaque_tid() & 63, g = lane >> 4;
+  auto load = [&](const char *at, int b) {
+    const int c = 8 * b + g, last = K / 16 - 1;
+    const u32x4 x = ldg(reinterpret_cast<const u32x4 *>(at + 16 * min(c, last))), y = ldg(reinterpret_cast<const u32x4 *>(at + 16 * min(c + 4, last)));
+    return intx8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+  };
+#pragma unroll
+  for (int m = 0; m < MF; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma clang loop unroll(disable)
+  for (int b = first; b < end; b += step) {
+    const float t = ldg(sw + b);
+    intx8 a[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      a[n] = load(w + (int64_t)min(row + 16 * n, p.g.L.out_features - 1 - n0) * K, b);
+      clear_behind(a[n], lane, K - 128 * b);
+    }
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      const intx8 x = load(reinterpret_cast<const char *>(p.g.q) + (int64_t)src[m] * p.g.q_row, b);
+      const float s = ldg(p.g.s + (int64_t)src[m] * p.g.s_row + b), f = s * t;
+      const bool far = !(fabsf(f) < INFINITY);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+        const floatx4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[n], x, zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(far ? d[j] * s : d[j], far ? t : f, acc[m][n][j]);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------------------
 // Few rows: the matrix streams through once, and its bytes bound the kernel.
 // ---------------------------------------------------------------------------------------
@@ -298,6 +374,14 @@ __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps, int w
           for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(d[j], f[m], acc[m][n][j]);
         }
       asm volatile("" ::: "memory");  // (the place's reads are done before its next copies)
+    }
+    if (any_far(acc)) {
+      int rows[MF];
+#pragma unroll
+      for (int m = 0; m < MF; ++m) rows[m] = max(source_row(p, min(t.row + 16 * m + (2 * m + 1 < XC ? i : i & 7), t.end - 1)), 0);
+      const float *scales = L.scale + ((int64_t)t.e * nb + (n0 >> 7)) * kb;
+      if (far_scales(p, scales, rows, wave, waves, kb))
+        sums_again<MF, NT>(p, reinterpret_cast<const char *>(L.w) + ((int64_t)t.e * N + n0) * K, n0, i, scales, rows, wave, waves, kb, acc);
     }
     __builtin_amdgcn_s_barrier();  // (the sums of the tile before have been read)
     asm volatile("" ::: "memory");
@@ -665,6 +749,16 @@ template <bool BF, int MF>
 __device__ __forceinline__ bool wide_tile(const GemmArgs &p, int row_tiles, int turn, int wave, WideTile &x, WideLds &lds) {
   floatx4 acc[MF][4];
   wide_blocks<MF>(p, x.w, x.f, wave, lds, x.kb, x.rest, acc);
+  if (any_far(acc)) {
+    const trellis_f8_linear &L = p.g.L;
+    const int i = opaque_tid() & 15, wm = wave & 1, wn = wave >> 1, nb = (L.out_features + 127) / 128;
+    const int b0 = x.split * ((p.kb + p.splits - 1) / p.splits);
+    int rows[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) rows[m] = max(source_row(p, min(x.t.row + 32 * m + 16 * wm + i, x.t.end - 1)), 0);
+    const float *scales = L.scale + ((int64_t)x.t.e * nb + min((x.n0 >> 7) + (wn >> 1), nb - 1)) * p.kb;
+    if (far_scales(p, scales, rows, b0, 1, b0 + x.kb)) sums_again<MF, 4>(p, x.w, x.n0, 64 * wn + i, scales, rows, b0, 1, b0 + x.kb, acc);
+  }
   const RowTile t = x.t;
   const int n0 = x.n0, split = x.split;
   const bool more = wide_next(p, row_tiles, turn, wave, x, lds);

@@ -55,6 +55,19 @@ def test_binding_refuses_before_the_library():
         tb.trellis_moe_sort(torch.zeros(4, dtype=torch.int32), 4)
 
 
+@pytest.mark.parametrize("shape", [(2 ** 32 + 128, 16), (128, 2 ** 32 + 16), (2 ** 32 + 2, 128, 128), (2 ** 31, 16)])
+def test_matrices_above_32_bits_are_refused(monkeypatch, shape):
+    """Not cut off to the small sizes that their lower 32 bits are.  (Tensors without storage stand for
+    those on a GPU.)"""
+    monkeypatch.setattr(tb, "_req", lambda *args, **kw: None)
+    w = torch.empty(shape, dtype=torch.float8_e4m3fn, device="meta")
+    scale = torch.empty((*shape[:-2], -(-shape[-2] // 128), -(-shape[-1] // 128)), device="meta")
+    with pytest.raises(ValueError):
+        tb.F8Linear(w, scale)
+    L = tb.F8Linear(w[..., :16, :16], scale[..., :1, :1]) if len(shape) == 2 else None
+    assert L is None or (L._c.n_experts, L._c.in_features, L._c.out_features) == (1, 16, 16)
+
+
 def test_oracle_e4m3_by_hand():
     v = FO.E4M3
     assert v[0x7E] == 448 and v[0x08] == 2.0 ** -6 and v[0x01] == 2.0 ** -9 and v[0xB8] == -1.0 and np.isnan(v[0x7F])

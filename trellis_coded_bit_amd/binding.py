@@ -1069,9 +1069,9 @@ class F8Linear:
         if tuple(scale.shape) != want:
             raise ValueError(f"scale must be {want}, got {tuple(scale.shape)}")
         self.w, self.scale, self.device = w, scale, w.device
-        self.experts = w.shape[0] if w.dim() == 3 else None
-        self.in_features, self.out_features = inn, out
-        self._c = CF8Linear(w.data_ptr(), scale.data_ptr(), w.shape[0] if w.dim() == 3 else 1, inn, out)
+        self.experts = _i31(w.shape[0], "experts") if w.dim() == 3 else None
+        self.in_features, self.out_features = _i31(inn, "in"), _i31(out, "out")
+        self._c = CF8Linear(w.data_ptr(), scale.data_ptr(), 1 if self.experts is None else self.experts, inn, out)
         self._ref = ctypes.byref(self._c)
 
 

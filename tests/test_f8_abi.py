@@ -68,6 +68,38 @@ def test_matrices_above_32_bits_are_refused(monkeypatch, shape):
     assert L is None or (L._c.n_experts, L._c.in_features, L._c.out_features) == (1, 16, 16)
 
 
+def test_new_outputs_are_seen_by_modes(monkeypatch):
+    """New outputs are made by torch.empty where a mode or deterministic algorithms want to see them."""
+    from torch.overrides import TorchFunctionMode
+    from torch.utils._python_dispatch import TorchDispatchMode
+    seen = []
+
+    class Dispatch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(func)
+            return func(*args, **(kwargs or {}))
+
+    class Function(TorchFunctionMode):
+        def __torch_function__(self, func, types, args=(), kwargs=None):
+            seen.append(func)
+            return func(*args, **(kwargs or {}))
+
+    monkeypatch.setattr(tb, "_empty_cuda", lambda shape, stride, dtype: None)
+    cpu = torch.device("cpu")
+    assert tb._new1(3, torch.int32, cpu) is None and tb._new2(3, 4, torch.int32, cpu) is None
+    for mode in (Dispatch, Function):
+        with mode():
+            t = tb._new2(3, 4, torch.float16, cpu)
+        assert seen and t.shape == (3, 4) and t.dtype == torch.float16 and t.stride() == (4, 1)
+        seen.clear()
+    torch.use_deterministic_algorithms(True)
+    try:
+        assert torch.isnan(tb._new1(5, torch.float32, cpu)).all()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert tb._new1(3, torch.int32, cpu) is None
+
+
 def test_oracle_e4m3_by_hand():
     v = FO.E4M3
     assert v[0x7E] == 448 and v[0x08] == 2.0 ** -6 and v[0x01] == 2.0 ** -9 and v[0xB8] == -1.0 and np.isnan(v[0x7F])

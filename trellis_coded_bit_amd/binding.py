@@ -970,16 +970,32 @@ def _f8_ws(ws: Optional[torch.Tensor], nb: int, device) -> torch.Tensor:
     return _kv4_ws(ws, nb, device, _stream())
 
 
-# A new tensor on the current device, for half of what torch.empty's argument parsing takes.
-_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+# A new tensor on the current device, for half of what torch.empty's argument parsing takes.  It passes
+# by what a program may put between: modes that see every call, and the fill of new memory that
+# deterministic algorithms ask for.  Where one of these is on, torch.empty is called.
+def _find_empty_cuda():
+    try:
+        C = torch._C
+        return C._dynamo.guards._empty_strided_cuda, C._len_torch_dispatch_stack, C._len_torch_function_stack, C._get_deterministic_algorithms
+    except AttributeError:
+        return None, None, None, None
+
+
+_empty_cuda, _dispatch_modes, _function_modes, _deterministic = _find_empty_cuda()
+
+
+def _new(shape: Tuple[int, ...], stride: Tuple[int, ...], dtype: torch.dtype, device) -> torch.Tensor:
+    if _empty_cuda is None or _dispatch_modes() or _function_modes() or _deterministic():
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _empty_cuda(shape, stride, dtype)
 
 
 def _new1(n: int, dtype: torch.dtype, device) -> torch.Tensor:
-    return _empty_cuda((n,), (1,), dtype) if _empty_cuda is not None else torch.empty((n,), dtype=dtype, device=device)
+    return _new((n,), (1,), dtype, device)
 
 
 def _new2(rows: int, n: int, dtype: torch.dtype, device) -> torch.Tensor:
-    return _empty_cuda((rows, n), (n, 1), dtype) if _empty_cuda is not None else torch.empty((rows, n), dtype=dtype, device=device)
+    return _new((rows, n), (n, 1), dtype, device)
 
 
 def _out1(t: Optional[torch.Tensor], n: int, device, dtype: torch.dtype, name: str) -> torch.Tensor:

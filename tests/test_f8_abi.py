@@ -164,3 +164,18 @@ def test_oracle_gradients_are_the_differences():
     live = order >= 0
     lhs = (x[order[live] // 3] * dxs[live]).sum()
     assert np.isclose(lhs, (x * FO.combine(dxs, inv)[0]).sum())
+
+
+def test_tiles_of_sorted_rows(tmp_path):
+    """The kernels' look at the offsets, run on the host lane by lane: also offsets that change under it
+    lead to no expert and no row that is not there."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host C++ compiler")
+    exe = str(tmp_path / "tiles_driver")
+    cmd = [gxx, "-std=c++17", "-O1", "-g", "-Wall", "-Wextra", "-Werror", "-Wno-unknown-pragmas", "-Wno-clobbered", "-fsanitize=undefined",
+           "-fno-sanitize-recover=all", os.path.join(ROOT, "tests", "sanitize", "tiles_driver.cpp"), "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "failures 0" in r.stdout, r.stdout + r.stderr

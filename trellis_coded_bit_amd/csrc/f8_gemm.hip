@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "f8_device.h"
+#include "f8_tiles.h"
 
 namespace trellis {
 
@@ -37,79 +38,9 @@ struct GemmArgs {
   int64_t part_row;
 };
 
-// Which rows a tile has: of expert e, rows [row, end).  e < 0: none.
-struct RowTile {
-  int e, row, end;
-};
-
-// An expert's rows [row, end) in tiles of `size`, `first` tiles of earlier experts before them.
-struct RowTiles {
-  int e, row, end, size, tiles, first;
-  __device__ __forceinline__ RowTile operator[](int i) const { return {e, row + i * size, min(end, row + (i + 1) * size)}; }
-};
-
-// n rows as tiles of at most T rows, T a multiple of U: as few as that takes, of the same size (a
-// multiple of U) but for the last.
-struct Cut {
-  int tiles, size;
-};
-template <int U>
-__device__ __forceinline__ Cut cut_rows(int n, int T) {
-  const int tiles = (n + T - 1) / T;
-  const int size = tiles ? ((n + tiles - 1) / tiles + U - 1) / U * U : U;
-  return {(n + size - 1) / size, size};
-}
-
-// The expert of tile `at` of the list: every expert's rows in tiles of at most p.tile_rows, expert
-// after expert.  Behind the last (at = INT_MAX, say) e is -1 and `first` the number of tiles.  The
-// list ends at the first pair of offsets that is out of order or out of range.  Called by whole waves.
 template <int U>
 __device__ __forceinline__ RowTiles find_tiles(const GemmArgs &p, int at, bool report) {
-  if (!p.g.offsets) {
-    const Cut c = cut_rows<U>(p.g.rows, p.tile_rows);
-    return {at < c.tiles ? 0 : -1, 0, p.g.rows, c.size, c.tiles, at < c.tiles ? 0 : c.tiles};
-  }
-  const int lane = opaque_tid() & 63, E = p.g.L.n_experts;
-  int passed = 0;
-  bool wrong = ldg(p.g.offsets) != 0;
-  for (int e0 = 0; e0 < E && !wrong; e0 += 256) {
-    // four neighbouring experts a lane, their tiles summed, then over the lanes
-    int o[5], sum = 0;
-    Cut c[4];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) o[k] = ldg(p.g.offsets + min(e0 + 4 * lane + k, E));
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      bad |= o[k] < 0 || o[k + 1] < o[k] || o[k + 1] > p.g.rows;
-      c[k] = cut_rows<U>(bad ? 0 : o[k + 1] - o[k], p.tile_rows);
-      sum += c[k].tiles;
-    }
-    const uint64_t bads = __ballot(bad);
-    if (bads && lane > __builtin_ctzll(bads)) sum = 0;
-    int s = sum;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int t = __shfl_up(s, d, 64);
-      if (lane >= d) s += t;
-    }
-    const uint64_t has = __ballot(at < passed + s);
-    if (has) {
-      const int l = __builtin_ctzll(has);
-      int first = passed + s - sum;
-      RowTiles r = {e0 + 4 * lane, 0, 0, U, 0, first};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (at >= first && at - first < c[k].tiles) r = {e0 + 4 * lane + k, o[k], o[k + 1], c[k].size, c[k].tiles, first};
-        first += c[k].tiles;
-      }
-      return {__builtin_amdgcn_readlane(r.e, l),    __builtin_amdgcn_readlane(r.row, l),   __builtin_amdgcn_readlane(r.end, l),
-              __builtin_amdgcn_readlane(r.size, l), __builtin_amdgcn_readlane(r.tiles, l), __builtin_amdgcn_readlane(r.first, l)};
-    }
-    passed += __builtin_amdgcn_readlane(s, 63);
-    wrong = bads != 0;
-  }
-  if (wrong && report && lane == 0) f8_error(p.errword);
-  return {-1, 0, 0, U, 0, passed};
+  return row_tiles_at<U>(p.g.offsets, p.g.L.n_experts, p.g.rows, p.tile_rows, at, report ? p.errword : nullptr);
 }
 
 // The row of q that a row reads, or -1.
@@ -734,6 +665,7 @@ __device__ __forceinline__ bool wide_next(const GemmArgs &p, int row_tiles, int 
   x.split = at / tiles;
   at -= x.split * tiles;
   const RowTiles r = find_tiles<32>(p, at / p.col_tiles, false);
+  if (r.e < 0) return false;
   at -= r.first * p.col_tiles;
   const int bands = (r.tiles + 7) >> 3, band_rows = (r.tiles + bands - 1) / bands, band = at / (band_rows * p.col_tiles);
   at -= band * band_rows * p.col_tiles;

@@ -135,8 +135,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
   if (key >= 0) {
     uint32_t at = before[key] + rank;
     for (int w = 0; w < wave; ++w) at += waves[w * E + key];
-    pos = (int32_t)at;
-    order[pos] = i;
+    // (below n, unless the ids change while they are read, or another call writes the counts)
+    if (at < (uint32_t)n) {
+      pos = (int32_t)at;
+      order[pos] = i;
+    }
   }
   inverse[i] = pos;
 }

@@ -168,3 +168,26 @@ def test_one_expert_with_nearly_all_rows(experts):
         if a < b:
             check_product(y[a:b], q[a:b], s[a:b], L.w[e], L.scale[e], "bf16")
     assert tb.error_word() == 0
+
+
+@pytest.mark.parametrize("experts,n,k", [(64, 4096, 1040), (200, 2056, 784)])
+def test_many_experts_with_few_and_many_rows(experts, n, k):
+    """Calls that are planned for wide tiles, with experts of every number of rows between 0 and 600."""
+    log_case(f"f8 moe_gemm uneven experts={experts} n={n} k={k}")
+    g = torch.Generator().manual_seed(experts)
+    counts = (torch.rand(experts, generator=g) ** 3 * 600).int().tolist()
+    counts[:8] = [1, 0, 31, 32, 33, 64, 65, 600]
+    off = np.concatenate([[0], np.cumsum(counts)])
+    rows, per = int(off[-1]), 4
+    gd = torch.Generator(device="cuda").manual_seed(experts)
+    w = torch.randint(0, 0x7F, (experts, n, k), dtype=torch.uint8, device="cuda", generator=gd).view(torch.float8_e4m3fn)
+    L = tb.F8Linear(w, torch.rand((experts, -(-n // 128), -(-k // 128)), device="cuda", generator=gd))
+    q, s = make_rows(-(-rows // per), k, g)
+    order = torch.randperm(len(q) * per, generator=g)[:rows].to(torch.int32).cuda()
+    y = tb.trellis_f8_moe_gemm(L, q, s, ints(off.tolist()), order=order, per=per, dtype=torch.bfloat16)
+    src = order.long() // per
+    for e in [*range(8), 17, experts - 1]:
+        at = src[off[e]:off[e + 1]]
+        if counts[e]:
+            check_product(y[off[e]:off[e + 1]], q.view(torch.uint8)[at].view(torch.float8_e4m3fn), s[at], L.w[e], L.scale[e], "bf16")
+    assert tb.error_word() == 0

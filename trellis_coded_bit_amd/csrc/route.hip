@@ -173,22 +173,27 @@ __global__ __launch_bounds__(256) void gather_kernel(const char *x, int64_t x_ro
   }
 }
 
-// Eight columns a thread, `parts` times 2048 of a token a workgroup; a token's rows eight at a time,
-// all under way before one is added.  The entries without a position are left out first: nothing of
-// theirs is read.  4097 tokens of 6144 channels with half of 8 entries here (252 MB): 48 us, as a copy;
-// row after row with cached reads it took 95.  A token's columns are one workgroup's where there are
-// tokens enough, and spread where there are few.
+// Eight columns a thread, 2048 of a token a workgroup; a token's rows eight at a time, all under way before
+// one is added.  The entries without a position are left out first: nothing of theirs is read.  4097
+// tokens of 6144 channels with half of 8 entries here (252 MB): 45 us, as a copy; row after row with cached
+// reads it took 95.  (All of a token's columns by one workgroup, one after the other, in us for the time
+// here: 256 tokens of 8 with 6144 channels 8.8 for 7.8, 4096 with 5120 channels 72.9 for 69.5, 2048 with
+// 20480 143 for 130; never less by more than 2 %.)
 template <bool BF, bool NT>
-__global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, int groups, uint32_t *errword) {
+__global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int groups, uint32_t *errword) {
   const int lane = threadIdx.x & 63;
   const long long items = (long long)a.tokens * groups;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int t = (int)(it / groups), c0 = (int)(it - (long long)t * groups) * parts * 2048;
-    const int c1 = min(c0 + parts * 2048, a.n);
-    int pos = -1;
-    float weight = 1.f;
-    auto look = [&](int j0) {
-      pos = -1;
+    const int t = (int)(it / groups), c0 = (int)(it - (long long)t * groups) * 2048, c = c0 + threadIdx.x * 8;
+    const bool live = c < a.n;
+    const int at = live ? c : c0;
+    float s[8] = {};
+    u32x4 add = {0, 0, 0, 0};
+    if (a.add) add = ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + at));
+    bool first = true;
+    for (int j0 = 0; j0 < a.top; j0 += 64) {
+      int pos = -1;
+      float weight = 1.f;
       if (j0 + lane < a.top) {
         pos = ldg(a.inverse + (size_t)t * a.top + j0 + lane);
         if (a.weights) weight = ldg(a.weights + (size_t)t * a.top + j0 + lane);
@@ -197,46 +202,34 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeCombine a, int parts, i
         f8_error(errword);
         pos = -1;
       }
-    };
-    if (a.top <= 64) look(0);
-    for (int c = c0 + threadIdx.x * 8; c - (int)threadIdx.x * 8 < c1; c += 2048) {
-      const bool live = c < c1;
-      const int at = live ? c : c0;
-      float s[8] = {};
-      u32x4 add = {0, 0, 0, 0};
-      if (a.add) add = ldg(reinterpret_cast<const u32x4 *>(a.add + (size_t)t * a.n + at));
-      bool first = true;
-      for (int j0 = 0; j0 < a.top; j0 += 64) {
-        if (a.top > 64) look(j0);
-        uint64_t left = __ballot(pos >= 0);
-        while (left) {
-          u32x4 v[8];
-          float w[8];
-          int count = 0;
+      uint64_t left = __ballot(pos >= 0);
+      while (left) {
+        u32x4 v[8];
+        float w[8];
+        int count = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (!left) break;
-            const int l = __builtin_ctzll(left);
-            left &= left - 1;
-            w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), l));
-            v[k] = ldg_once<NT>(reinterpret_cast<const u32x4 *>(a.y + (size_t)__builtin_amdgcn_readlane(pos, l) * a.n + at));
-            ++count;
-          }
-          if (first && a.add) f8_widen8<BF>(add, s);
-          first = false;
+        for (int k = 0; k < 8; ++k) {
+          if (!left) break;
+          const int l = __builtin_ctzll(left);
+          left &= left - 1;
+          w[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), l));
+          v[k] = ldg_once<NT>(reinterpret_cast<const u32x4 *>(a.y + (size_t)__builtin_amdgcn_readlane(pos, l) * a.n + at));
+          ++count;
+        }
+        if (first && a.add) f8_widen8<BF>(add, s);
+        first = false;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k >= count) break;
-            float x[8];
-            f8_widen8<BF>(v[k], x);
+        for (int k = 0; k < 8; ++k) {
+          if (k >= count) break;
+          float x[8];
+          f8_widen8<BF>(v[k], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = fmaf(w[k], x[i], s[i]);
-          }
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(w[k], x[i], s[i]);
         }
       }
-      if (first && a.add) f8_widen8<BF>(add, s);
-      if (live) stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
     }
+    if (first && a.add) f8_widen8<BF>(add, s);
+    if (live) stg(reinterpret_cast<u32x4 *>(a.out + (size_t)t * a.n + c), f8_narrow8<BF>(s));
   }
 }
 
@@ -356,13 +349,13 @@ hipError_t launch_moe_gather(const void *x, int64_t x_row_bytes, int tokens, int
 }
 
 hipError_t launch_moe_combine(const MoeCombine &a, uint32_t *errword, hipStream_t stream) {
-  const int all = (a.n + 2047) / 2048, parts = a.tokens >= 1024 ? all : 1, groups = (all + parts - 1) / parts;
+  const int groups = (a.n + 2047) / 2048;
   const unsigned grid = grid_of((long long)a.tokens * groups);
   const bool once = (size_t)a.rows * a.n * 2 > kF8Once;
-  if (a.bf16 && once) combine_kernel<true, true><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
-  else if (a.bf16) combine_kernel<true, false><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
-  else if (once) combine_kernel<false, true><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
-  else combine_kernel<false, false><<<grid, 256, 0, stream>>>(a, parts, groups, errword);
+  if (a.bf16 && once) combine_kernel<true, true><<<grid, 256, 0, stream>>>(a, groups, errword);
+  else if (a.bf16) combine_kernel<true, false><<<grid, 256, 0, stream>>>(a, groups, errword);
+  else if (once) combine_kernel<false, true><<<grid, 256, 0, stream>>>(a, groups, errword);
+  else combine_kernel<false, false><<<grid, 256, 0, stream>>>(a, groups, errword);
   return hipGetLastError();
 }
 

@@ -72,8 +72,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
   extern __shared__ uint32_t lds[];
   uint32_t *before = lds;       // [E] of the id in earlier workgroups' entries, then its first position here
   uint32_t *after = before + E; // [E] of the id in the others
-  uint32_t *sums = after + E;   // [16] the scan's, of each wave
-  uint16_t *waves = reinterpret_cast<uint16_t *>(sums + kSortWaves);  // [16][E] of the id in this workgroup's waves
+  uint16_t *waves = reinterpret_cast<uint16_t *>(after + E);  // [16][E] of the id in this workgroup's waves
+  __shared__ uint32_t sums[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int first = blockIdx.x * kSortThreads;
   const int i = first + tid;
@@ -144,8 +144,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t 
   inverse[i] = pos;
 }
 
-// All that sort_place_kernel has in shared memory.
-size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves) + 4 * kSortWaves; }
+// What sort_place_kernel has in shared memory besides its waves' sums.  (Those at the end of it, where
+// their place is not a constant: 33 tokens' 264 entries 4.4 us for 3.75, 32776 entries 8.0 for 7.35.)
+size_t sort_lds(int E) { return (size_t)E * (4 + 4 + 2 * kSortWaves); }
 
 // A workgroup a row, four words a thread under way.  16411 rows of 6144 16-bit channels (252 MB moved at
 // most, a token's row up to four times from a cache): 62 us; one word a thread: 78.
@@ -316,7 +317,7 @@ hipError_t launch_moe_sort(const int32_t *ids, int tokens, int top, int n_expert
   while ((1 << bits) < n_experts) ++bits;
   const size_t lds = sort_lds(n_experts);
   hipError_t e;
-  if (lds > 65536) {
+  if (lds + 4 * kSortWaves > 65536) {
     // (the most of any call: another thread's may be between this and its launch)
     e = hipFuncSetAttribute(reinterpret_cast<const void *>(sort_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)sort_lds(kMoeExperts));

@@ -9,7 +9,8 @@
  * Quantising a block: a = max |v|, scale = a / 448, code = v / scale to the nearest E4M3 value,
  * ties to even.  A block whose scale is below the smallest normal f32 (a block of zeros, too) is
  * stored as scale 0 and codes 0; one with an infinity or NaN as scale NaN and codes 0: it stands
- * for NaN.
+ * for NaN.  Values are formed in f32 before they are quantised or rounded: one above its largest
+ * number (products of bf16's largest) is an infinity.
  *
  * Conventions as in trellis.h: device pointers unless stated otherwise, `stream` a hipStream_t
  * as void*, calls only enqueue, nothing is allocated, validation on the host before anything is

@@ -220,6 +220,30 @@ def test_silu_mul_of_far_gates_and_special_values(dtype):
     check_quantized(q[live], s[live, None], v[live], 2.0 ** -20, 2.0 ** -20)
 
 
+def test_values_above_f32_are_infinite():
+    """Their blocks stand for NaN; the blocks beside them are as they are."""
+    log_case("f8 values above f32")
+    x = torch.zeros((2, 512))
+    x[:, :256], x[:, 256:] = 1e30, 1.0
+    x[0, 256:384], x[1, 256:384] = 1e30, -1e30
+    x = x.bfloat16().cuda()
+    y = torch.empty((2, 256), dtype=torch.bfloat16, device="cuda")
+    q, s = tb.trellis_f8_silu_mul(x, y=y)
+    inf = float("inf")
+    assert (y[0, :128] == inf).all() and (y[1, :128] == -inf).all() and torch.equal(y[:, 128:], x[:, :128])
+    assert torch.isnan(s[:, 0]).all() and (host(q)[:, :128] == 0).all() and torch.isfinite(s[:, 1]).all()
+    g = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    g[:128] = torch.finfo(torch.bfloat16).max
+    x = torch.zeros((1, 256), dtype=torch.bfloat16, device="cuda")
+    x[0, 5], x[0, 200] = 4.0, 1.0  # 4 / sqrt(17 / 256) times the largest number
+    y = torch.empty_like(x)
+    q, s, _ = tb.trellis_f8_norm(x, g, 1e-6, y=y)
+    assert y[0, 5] == inf and torch.isnan(s[0, 0]) and (host(q)[0, :128] == 0).all()
+    v, _ = FO.norm(host(x), float(np.float32(1e-6)), host(g))
+    check_rounded(host(y)[:, 128:], v[:, 128:], "bf16", 2.0 ** -19)
+    check_quantized(host(q)[:, 128:], host(s)[:, 1:], v[:, 128:], 2.0 ** -20, 2.0 ** -19)
+
+
 # ---------------------------------------------------------------------------------------
 # Products
 # ---------------------------------------------------------------------------------------

@@ -3,7 +3,8 @@
 Every computation runs in the HIP library; this module checks dtypes, devices and
 contiguity, allocates outputs and workspaces with torch, and passes raw device pointers
 and the current HIP stream.  If the library is not built, loading fails loudly: there is
-no fallback path.
+no fallback path.  Autograd records none of these calls: a result requires no gradient,
+whatever its inputs do, and a program that trains calls the gradients' entry points itself.
 """
 from __future__ import annotations
 

@@ -8,7 +8,10 @@ namespace trellis {
 
 // Bytes of an array from which on a kernel that passes over it once leaves the caches alone (all
 // L2 caches together hold 32 MB).  Rows gathered and combined for 4097 tokens: 117 us so, 140 without;
-// the gradients for 4096: 214 and 233.
+// the gradients for 4096: 214 and 233.  On either side of the bound, us through the caches | past them: rows
+// gathered 6.6 | 5.8 (16 MB), 9.3 | 7.6 (24 MB), 11.3 | 10.0 (32 MB), combined 5.9 | 5.7, 7.7 | 6.9, 9.3 | 8.2,
+// one after the other 12.0 | 11.3, 16.0 | 14.3, 18.9 | 17.9.  Past them is no slower below the bound
+// either; there the rows are left in the caches for a product that reads them next, which these leave out.
 constexpr size_t kF8Once = (size_t)24 << 20;
 
 // 16-bit element types.  bf16 is rounded to nearest even; a NaN stays one.

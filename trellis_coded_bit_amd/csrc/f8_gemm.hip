@@ -196,9 +196,12 @@ struct NarrowWave {
 // behind the last it copies that one again, so that the number of copies under way is a constant.
 // One token over 17408 x 5120 takes 15.4 us (5.8 TB/s of the 6.4 that a stream reads at; 18 where the
 // matrix is in no cache), 37 tokens over 5120 x 6144 9.6 (tokens in sixteens: 10.7), 33 tokens' 264
-// entries over 256 experts' 4096 x 6144 605 to 640.  With more tokens it is what a CU copies: of 64 by
-// 5120 x 6144, 15.3 us in no cache, a copy of the kernel that reads the same few token lines takes 11.8,
-// and one with five or six waves in flight instead of four no less.
+// entries over 256 experts' 4096 x 6144 605 to 645.  With more tokens it is far from the matrix's bytes,
+// and what bounds it is not shown.  Of 64 tokens by 5120 x 6144, 15.7 us in no cache, a copy of the kernel
+// that reads the same few token lines takes 11.8, the bytes alone 5; five or six waves in flight instead
+// of four take no less.  Nor is it the CUs without a workgroup: 37 tokens by 2560, 5120, 8192 and 10240 x
+// 6144 (80, 160, 256 and 320 workgroups) take 9.6, 12.8, 21.4 and 23.7 us in no cache, the matrix's
+// and the tokens' copies together 5 to 6 TB/s from 160 workgroups on.
 template <bool BF, int XC, int NT, int D>
 __global__ __launch_bounds__(512) void narrow_kernel(GemmArgs p, int reps, int whole, int rest) {
   using Stage = NarrowStage<XC, NT>;
@@ -357,7 +360,9 @@ hipError_t launch_narrow(GemmArgs p, hipStream_t stream) {
   p.row_tiles = p.g.offsets ? p.g.rows / p.tile_rows + min(p.g.rows, L.n_experts) : (p.g.rows + p.tile_rows - 1) / p.tile_rows;
   const long long tiles = (long long)p.row_tiles * p.col_tiles;
   // (in long calls a workgroup's first copies and its look at the offsets serve four tiles: a decode
-  // batch's experts 678 -> 632 us)
+  // batch's experts 678 -> 632 us.  Two rows an expert, us with one | four: 64 experts' 1024 x 6144, 2560
+  // tiles, 72 | 73, 64 of 2048 x 6144, 5120 tiles, 138 | 141, 128 of 2048 x 4096, 10240 tiles, 201 | 182, 256 of
+  // 1024 x 2048, as many, 116 | 92)
   const int reps = tiles > (1 << 24) ? (int)min((tiles + (1 << 22) - 1) >> 22, (long long)p.col_tiles) : tiles > 4096 ? 4 : 1;
   constexpr int each = (int)sizeof(NarrowWave<XC, NT, D>) + (XC + 1) / 2 * NT * 1024, most = (8 * each <= kLds ? 8 : 4) * each;
   static_assert(most <= kLds, "four waves fit");
@@ -408,7 +413,7 @@ hipError_t launch_few(const GemmArgs &p, long long each, hipStream_t stream) {
 // ---------------------------------------------------------------------------------------
 // Many rows: 256 matrix rows by up to 256 tokens a workgroup of eight waves, 64 by up to 128 a wave.
 //
-// A block of 128 inputs takes a workgroup 1.70 to 1.85 us at 256 tokens (2300 to 2580 TFLOP/s over the
+// A block of 128 inputs takes a workgroup 1.70 to 1.85 us at 256 tokens (2320 to 2530 TFLOP/s over the
 // card).  Of copies of the kernel that leave something out, the one without copies from memory takes
 // 1.40, without the meetings 1.37 then, without the reads of shared memory 1.30, with the matrix
 // instructions alone 1.10 to 1.26.  So no single part bounds it: the matrix unit is busy 45 % of the
@@ -753,8 +758,16 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs p) {
 // block of 64 tokens by 32 matrix rows over the whole card; a wide workgroup 0.45 + 0.156 a block for
 // every 32 of its tokens, and 3 a tile; a split's sums are written and read at 5 TB/s by one launch
 // more.  Matrices in no cache, narrow | wide, blocks whole | wide, blocks shared: 5120 x 6144 with 32
-// rows 12.3 | 56 | 18, 64 rows 16.0 | 57 | 20, 128 rows 23 | 54 | 23, 256 rows 34 | 52 | 29, 512 rows
-// 54 | 50 | 37; 17408 x 5120 with 32 rows 30 | 53 | 29, 64 rows 40 | 54 | 32, 128 rows 57 | 53 | 40.
+// rows 12.0 | 56 | 18, 64 rows 15.7 | 57 | 20, 128 rows 23.3 | 57 | 23.4, 256 rows 35 | 57 | 31, 512 rows
+// 58 | 56 | 40; 17408 x 5120 with 32 rows 30 | 54 | 30, 64 rows 40 | 55 | 33, 128 rows 56 | 53 | 40.
+//
+// Experts' wide tiles are priced as full ones (256 rows, 1.70 a block) although they run at the rows that
+// they have, up to 32 rows an expert are not weighed, and rows whose expert is not here count as if it
+// were.  So few rows an expert stay narrow longer than they should.  Narrow | wide with 16, 33, 48, 64 and
+// 96 rows each, * what is taken: 64 experts of 2048 x 2048 68* | 60, 82* | 62, 90* | 64, 101* | 64, 159 |
+// 71*; of 6144 x 2048 194* | 159, 235* | 167, 254* | 175, 281* | 181, 446 | 201*; of 4096 x 6144 317* | 301,
+// 385 | 306*, 420 | 312*, 464 | 320*, 716 | 347*; 256 of 2048 x 2048 257* | 207, 314* | 220, 341* | 229,
+// 381* | 236, 621 | 263*; 16 of 4096 x 6144 105* | 84, 121 | 86*, 132 | 87*, 146 | 89*, 182 | 96*.
 struct Plan {
   bool narrow;
   int tile_rows, splits;

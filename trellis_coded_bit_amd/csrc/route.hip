@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const char *x, int64_t x_ro
 
 // Eight columns a thread, 2048 of a token a workgroup; a token's rows eight at a time, all under way before
 // one is added.  The entries without a position are left out first: nothing of theirs is read.  4097
-// tokens of 6144 channels with half of 8 entries here (252 MB): 45 us, as a copy; row after row with cached
+// tokens of 6144 channels with half of 8 entries here (252 MB): 43 us, as a copy; row after row with cached
 // reads it took 95.  (All of a token's columns by one workgroup, one after the other, in us for the time
 // here: 256 tokens of 8 with 6144 channels 8.8 for 7.8, 4096 with 5120 channels 72.9 for 69.5, 2048 with
 // 20480 143 for 130; never less by more than 2 %.)

@@ -207,7 +207,7 @@ _ws_outgrown: Dict[Tuple[int, int], List[torch.Tensor]] = {}
 # Buffers outgrown while a call of another thread (or the program) held them: what such a call is yet
 # to set in an error word counts too.
 _ws_held: Dict[Tuple[int, int], List[torch.Tensor]] = {}
-_ws_lock = threading.Lock()
+_ws_lock = threading.RLock()  # (collected objects may call in while a buffer is made)
 
 
 def _ws_replace(key: Tuple[int, int], w: torch.Tensor, old: List[torch.Tensor]) -> None:
